@@ -297,6 +297,130 @@ moe_status moe_quantize_weights(int32_t n_mats, int32_t rows, int32_t cols, cons
 moe_status moe_quantize_act(int32_t rows, int32_t cols, const void* x_bf16, uint8_t* codes,
                             float* scales, hipStream_t stream);
 
+/* ---- Routing from given logits -------------------------------------------------------------
+ * For callers whose router is not the sigmoid of u^T e_i above (a softmax router, a learned or
+ * quantised product): the selection and its gradient, on logits the caller computed. */
+typedef enum moe_score {
+  MOE_SCORE_SIGMOID = 0,    /* s_i = 1 / (1 + exp(-l_i)) */
+  MOE_SCORE_SOFTMAX = 1     /* s_i = exp(l_i) / sum_j exp(l_j) */
+} moe_score;
+
+typedef enum moe_group_score {
+  MOE_GROUP_MAX = 0,        /* a group's score: its largest s+b */
+  MOE_GROUP_TOP2 = 1        /* the sum of its two largest s+b (of its only one, if it has one) */
+} moe_group_score;
+
+/* Limits: tokens >= 0; 1 <= n_routed <= 512; 1 <= top_k <= min(n_routed, 32);
+ * 1 <= topk_groups <= n_groups <= 64, n_routed % n_groups == 0 and
+ * topk_groups * n_routed / n_groups >= top_k; tokens * top_k < 2^31; scale finite. */
+typedef struct moe_gate_config {
+  int32_t tokens;        /* T */
+  int32_t n_routed;      /* N */
+  int32_t top_k;         /* K */
+  int32_t logits_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 (logits and their gradient) */
+  int32_t score;         /* moe_score */
+  int32_t n_groups;      /* equal groups of neighbouring experts; 1: no limit */
+  int32_t topk_groups;   /* groups that stay eligible for a token */
+  int32_t group_score;   /* moe_group_score */
+  int32_t renormalize;   /* non-zero: gates divided by the sum of the selected s */
+  float scale;           /* factor of every gate */
+  int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
+} moe_gate_config;
+
+/* Bytes of device workspace that moe_gate needs for `config` (0 without expert_load). */
+moe_status moe_gate_workspace_size(const moe_gate_config* config, size_t* bytes);
+
+/* Selection and gates.
+ *   logits      [T, N]  fp32 or bf16, rows logits_ld apart
+ *   bias        [N]     fp32, or NULL; only ranks experts
+ *   topk_idx    [T, K]  int32 out: experts by s+b descending, ties to the lower index; -1 where no
+ *                       eligible expert is left (moe_forward skips such entries)
+ *   topk_gate   [T, K]  fp32 out: scale * s (over the sum of the selected s if renormalize); 0 for -1
+ *   expert_load [N]     int32 out, or NULL: picks of each expert
+ * An expert whose logit or bias is -inf is not eligible; a token whose logits are all -inf (a
+ * padding row) picks nothing.  A NaN score ranks below every number, and its gates are NaN.  Scores,
+ * sums and gates are fp32.  T == 0 writes expert_load = 0.
+ * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512 or top_k > 32:
+ * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE if workspace_bytes is too small. */
+moe_status moe_gate(const moe_gate_config* config, const void* logits, const float* bias, int32_t* topk_idx,
+                    float* topk_gate, int32_t* expert_load, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream);
+
+/* Gradient of moe_gate's gates with the selection held fixed.
+ *   logits, topk_idx   as given to and written by moe_gate (entries outside [0, N) are skipped; the
+ *                      others of a row are distinct)
+ *   d_gate   [T, K]    fp32 dL/dgate
+ *   d_logits [T, N]    out, every element written: fp32 or bf16 (rounded once), rows d_logits_ld apart
+ *                      (0: n_routed); may not alias logits
+ * The bias gets no gradient.  Errors as moe_gate. */
+moe_status moe_gate_backward(const moe_gate_config* config, const void* logits, const int32_t* topk_idx,
+                             const float* d_gate, void* d_logits, int64_t d_logits_ld, hipStream_t stream);
+
+/* ---- FP8 products ---------------------------------------------------------------------------
+ * The dense layers beside the experts (a dense FFN, a projection), in the experts' FP8 scheme: E4M3
+ * codes with one fp32 scale per 1x128 run or 128x128 block, accumulated in fp32 (bf16 outputs: by
+ * the FP8 matrix instruction, whose sums of eight products keep 13 bits below the largest; fp32
+ * outputs: on the codes widened to f16, exact products in fp32). */
+typedef enum moe_fp8_form {
+  MOE_FP8_FORWARD = 0,      /* out = a b^T: a [m, k] in 1x128 runs, b [n, k] in 128x128 blocks */
+  MOE_FP8_INPUT_GRAD = 1,   /* out = a b:   a [m, k] in 1x128 runs, b [k, n] in 128x128 blocks */
+  MOE_FP8_WEIGHT_GRAD = 2   /* out = a b^T: a [m, k] and b [n, k], both in 1x128 runs */
+} moe_fp8_form;
+
+/* Limits: m, n, k >= 0, n a multiple of 16, k a multiple of 128; leading dimensions at least the row
+ * length, lda and ldb multiples of 16 below 2^24, ldo a multiple of 4. */
+typedef struct moe_matmul_shape {
+  int32_t m, n, k;
+  int32_t form;         /* moe_fp8_form */
+  int32_t out_dtype;    /* MOE_DTYPE_BF16 or MOE_DTYPE_F32 */
+  int32_t accumulate;   /* non-zero: out += the product (gradients of several micro-batches) */
+  int64_t lda, ldb;     /* elements between rows of a and b; 0: dense */
+  int64_t ldo;          /* elements between rows of out; 0: n */
+} moe_matmul_shape;
+
+/* Bytes of device workspace that moe_matmul_fp8 needs for `shape`. */
+moe_status moe_matmul_fp8_workspace_size(const moe_matmul_shape* shape, size_t* bytes);
+
+/* out = the product of `shape`'s form.
+ *   a, b      E4M3FN codes (16-byte aligned)
+ *   a_scale   fp32 [m, k/128] (moe_quantize_act, moe_quantize_act_t)
+ *   b_scale   fp32 [ceil(n/128), k/128] forward, [k/128, ceil(n/128)] input gradient (both as
+ *             moe_quantize_weights writes them for the stored matrix), [n, k/128] weight gradient
+ *   out       [m, n] bf16 or fp32 (16-byte aligned); aliases no input
+ * k == 0 gives zeros.  Errors: MOE_ERR_INVALID_ARG (unknown form or type, a negative size, a leading
+ * dimension below the row length, a null or misaligned pointer, out aliasing an operand),
+ * MOE_ERR_UNSUPPORTED (other limits), MOE_ERR_WORKSPACE. */
+moe_status moe_matmul_fp8(const moe_matmul_shape* shape, const uint8_t* a, const float* a_scale, const uint8_t* b,
+                          const float* b_scale, void* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+
+/* The operands of a weight gradient: x [rows, cols] bf16 transposed and quantised in runs of 128 rows:
+ *   codes  [cols, R]      E4M3FN, R = rows rounded up to 128, rows past the last as zeros
+ *   scales [cols, R/128]  fp32
+ * scale = amax * fp32(1/448) (1 for a run of zeros), code = round-to-nearest-even E4M3FN of
+ * fp32(x / scale), saturating at 448.  cols must be a multiple of 8 (MOE_ERR_UNSUPPORTED). */
+moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, uint8_t* codes, float* scales,
+                              hipStream_t stream);
+
+/* ---- SwiGLU with its inputs kept in 8 bits --------------------------------------------------
+ * moe_forward_train keeps a and b in bf16; here a run of 128 values keeps one fp32 scale
+ * amax * fp32(1/127) (1 for a run of zeros) and 8-bit integers round(x / scale), half the memory.  A run that holds an
+ * infinity or NaN keeps the scale NaN.
+ *   ab       [rows, 2I]      bf16: a then b
+ *   h        [rows, I]       bf16 out: a sigmoid(a) b; may be NULL
+ *   saved    [rows, 2I]      int8 out
+ *   scales   [rows, 2I/128]  fp32 out
+ * inter (I) must be a multiple of 128 (MOE_ERR_UNSUPPORTED). */
+moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void* h, int8_t* saved, float* scales,
+                               hipStream_t stream);
+
+/* The backward pass from what moe_swiglu_forward8 kept: with a~, b~ = saved * scale and sg = sigmoid(a~),
+ *   d_ab [rows, 2I] bf16 out: dh b~ sg (1 + a~ (1 - sg)), then dh a~ sg
+ *   h    [rows, I]  bf16 out: a~ sg b~ (the operand of the next layer's weight gradient); may be NULL
+ * for dh [rows, I] bf16. */
+moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, const int8_t* saved, const float* scales,
+                                void* d_ab, void* h, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int32_t status);
 

@@ -21,6 +21,9 @@ LIB_PATH = os.path.join(_HERE, "libmoe.so")
 
 MOE_DTYPE_F32, MOE_DTYPE_BF16, MOE_DTYPE_FP8_B128 = 0, 1, 2
 MOE_FORWARD_EVENTS = 6
+MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX = 0, 1
+MOE_GROUP_MAX, MOE_GROUP_TOP2 = 0, 1
+MOE_FP8_FORWARD, MOE_FP8_INPUT_GRAD, MOE_FP8_WEIGHT_GRAD = 0, 1, 2
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE",
           4: "MOE_ERR_HIP"}
 
@@ -45,6 +48,17 @@ class Weights(ctypes.Structure):
 
 class WeightGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_gate", "w_up", "w_down", "sh_gate", "sh_up", "sh_down")]
+
+
+class GateConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_routed", "top_k", "logits_dtype", "score", "n_groups",
+                                              "topk_groups", "group_score", "renormalize")] + [
+        ("scale", ctypes.c_float), ("logits_ld", ctypes.c_int64)]
+
+
+class MatmulShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("m", "n", "k", "form", "out_dtype", "accumulate")] + [
+        (n, ctypes.c_int64) for n in ("lda", "ldb", "ldo")]
 
 
 if not os.path.exists(LIB_PATH):
@@ -76,6 +90,14 @@ _SIG = {
                           ctypes.c_size_t, _P],
     "moe_backward_saved": [ctypes.POINTER(Shape), _P, _P, ctypes.POINTER(Weights), _P, _P, _P, ctypes.c_size_t, _P,
                            _P, _P, ctypes.POINTER(WeightGrads), _P, ctypes.c_size_t, _P],
+    "moe_gate_workspace_size": [ctypes.POINTER(GateConfig), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_gate": [ctypes.POINTER(GateConfig), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_gate_backward": [ctypes.POINTER(GateConfig), _P, _P, _P, _P, ctypes.c_int64, _P],
+    "moe_matmul_fp8_workspace_size": [ctypes.POINTER(MatmulShape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_matmul_fp8": [ctypes.POINTER(MatmulShape), _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_quantize_act_t": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P],
+    "moe_swiglu_forward8": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P],
+    "moe_swiglu_backward8": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P],
     "moe_status_string": [ctypes.c_int32],
 }
 for _name, _args in _SIG.items():
@@ -237,6 +259,58 @@ def moe_quantize_weights(n_mats, rows, cols, w_bf16, codes, scales, stream=None)
 def moe_quantize_act(rows, cols, x_bf16, codes, scales, stream=None):
     _check("moe_quantize_act", _lib.moe_quantize_act(rows, cols, _ptr(x_bf16), _ptr(codes), _ptr(scales),
                                                      _stream(stream)))
+
+
+def make_gate_config(tokens, n_routed, top_k, logits_dtype, score, n_groups=1, topk_groups=1,
+                     group_score=MOE_GROUP_MAX, renormalize=True, scale=1.0, logits_ld=0) -> GateConfig:
+    return GateConfig(tokens, n_routed, top_k, logits_dtype, score, n_groups, topk_groups, group_score,
+                      int(renormalize), scale, logits_ld)
+
+
+def moe_gate_workspace_size(config: GateConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_gate_workspace_size", _lib.moe_gate_workspace_size(ctypes.byref(config), ctypes.byref(n)))
+    return n.value
+
+
+def moe_gate(config, logits, bias, topk_idx, topk_gate, expert_load, workspace, stream=None):
+    _check("moe_gate", _lib.moe_gate(ctypes.byref(config), _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_gate),
+                                     _ptr(expert_load), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_gate_backward(config, logits, topk_idx, d_gate, d_logits, d_logits_ld=0, stream=None):
+    _check("moe_gate_backward", _lib.moe_gate_backward(ctypes.byref(config), _ptr(logits), _ptr(topk_idx),
+                                                       _ptr(d_gate), _ptr(d_logits), d_logits_ld, _stream(stream)))
+
+
+def make_matmul_shape(m, n, k, form, out_dtype, accumulate=False, lda=0, ldb=0, ldo=0) -> MatmulShape:
+    return MatmulShape(m, n, k, form, out_dtype, int(accumulate), lda, ldb, ldo)
+
+
+def moe_matmul_fp8_workspace_size(shape: MatmulShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_matmul_fp8_workspace_size", _lib.moe_matmul_fp8_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_matmul_fp8(shape, a, a_scale, b, b_scale, out, workspace=None, stream=None):
+    _check("moe_matmul_fp8", _lib.moe_matmul_fp8(ctypes.byref(shape), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
+                                                 _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_quantize_act_t(rows, cols, x_bf16, codes, scales, stream=None):
+    _check("moe_quantize_act_t", _lib.moe_quantize_act_t(rows, cols, _ptr(x_bf16), _ptr(codes), _ptr(scales),
+                                                         _stream(stream)))
+
+
+def moe_swiglu_forward8(rows, inter, ab, h, saved, scales, stream=None):
+    _check("moe_swiglu_forward8", _lib.moe_swiglu_forward8(rows, inter, _ptr(ab), _ptr(h), _ptr(saved), _ptr(scales),
+                                                           _stream(stream)))
+
+
+def moe_swiglu_backward8(rows, inter, dh, saved, scales, d_ab, h=None, stream=None):
+    _check("moe_swiglu_backward8", _lib.moe_swiglu_backward8(rows, inter, _ptr(dh), _ptr(saved), _ptr(scales),
+                                                             _ptr(d_ab), _ptr(h), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

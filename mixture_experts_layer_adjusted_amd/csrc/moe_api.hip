@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/moe.h: argument validation,
 // workspace layout, and the ordered launch of the kernels of each call.
+#include <cmath>
 #include <mutex>
 #include <new>
 
@@ -834,6 +835,126 @@ moe_status moe_quantize_act(int32_t rows, int32_t cols, const void* x_bf16, uint
   if ((int64_t)rows * cols == 0) return MOE_OK;
   if (!x_bf16 || !codes || !scales) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_quantize_act(rows, cols, x_bf16, codes, scales, stream));
+}
+
+static moe_status check_gate(const moe_gate_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->tokens < 0 || c->n_routed < 1 || c->top_k < 1 || c->top_k > c->n_routed) return MOE_ERR_INVALID_ARG;
+  if (c->logits_dtype != MOE_DTYPE_F32 && c->logits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SIGMOID && c->score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID_ARG;
+  if (c->group_score != MOE_GROUP_MAX && c->group_score != MOE_GROUP_TOP2) return MOE_ERR_INVALID_ARG;
+  if (c->n_groups < 1 || c->n_groups > 64 || c->topk_groups < 1 || c->topk_groups > c->n_groups)
+    return MOE_ERR_INVALID_ARG;
+  if (c->n_routed % c->n_groups != 0) return MOE_ERR_INVALID_ARG;
+  if ((int64_t)c->topk_groups * (c->n_routed / c->n_groups) < c->top_k) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(c->scale)) return MOE_ERR_INVALID_ARG;
+  if (c->logits_ld != 0 && c->logits_ld < c->n_routed) return MOE_ERR_INVALID_ARG;
+  if (c->n_routed > kMaxRouted || c->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)c->tokens * c->top_k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+static size_t gate_bytes(const moe_gate_config& c) {
+  const int64_t rows = gate_blocks(c);
+  return rows > 1 ? (size_t)rows * c.n_routed * 4 : 0;
+}
+
+moe_status moe_gate_workspace_size(const moe_gate_config* config, size_t* bytes) {
+  moe_status rc = check_gate(config);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = gate_bytes(*config);
+  return MOE_OK;
+}
+
+moe_status moe_gate(const moe_gate_config* config, const void* logits, const float* bias, int32_t* topk_idx,
+                    float* topk_gate, int32_t* expert_load, void* workspace, size_t workspace_bytes,
+                    hipStream_t stream) {
+  moe_status rc = check_gate(config);
+  if (rc != MOE_OK) return rc;
+  if (config->tokens > 0 && (!logits || !topk_idx || !topk_gate)) return MOE_ERR_INVALID_ARG;
+  const size_t need = expert_load ? gate_bytes(*config) : 0;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && !workspace) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_gate(*config, logits, bias, topk_idx, topk_gate, expert_load,
+                                static_cast<int32_t*>(workspace), stream));
+}
+
+moe_status moe_gate_backward(const moe_gate_config* config, const void* logits, const int32_t* topk_idx,
+                             const float* d_gate, void* d_logits, int64_t d_logits_ld, hipStream_t stream) {
+  moe_status rc = check_gate(config);
+  if (rc != MOE_OK) return rc;
+  if (d_logits_ld != 0 && d_logits_ld < config->n_routed) return MOE_ERR_INVALID_ARG;
+  if (config->tokens == 0) return MOE_OK;
+  if (!logits || !topk_idx || !d_gate || !d_logits || d_logits == logits) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_gate_backward(*config, logits, topk_idx, d_gate, d_logits, d_logits_ld, stream));
+}
+
+static moe_status check_matmul(const moe_matmul_shape* s) {
+  if (!s || s->m < 0 || s->n < 0 || s->k < 0) return MOE_ERR_INVALID_ARG;
+  if (s->form != MOE_FP8_FORWARD && s->form != MOE_FP8_INPUT_GRAD && s->form != MOE_FP8_WEIGHT_GRAD)
+    return MOE_ERR_INVALID_ARG;
+  if (s->out_dtype != MOE_DTYPE_F32 && s->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  const int64_t brow = s->form == MOE_FP8_INPUT_GRAD ? s->n : s->k;
+  const int64_t lda = s->lda ? s->lda : s->k, ldb = s->ldb ? s->ldb : brow, ldo = s->ldo ? s->ldo : s->n;
+  if (lda < s->k || ldb < brow || ldo < s->n) return MOE_ERR_INVALID_ARG;
+  if (s->n % 16 != 0 || s->k % 128 != 0 || lda % 16 != 0 || ldb % 16 != 0 || ldo % 4 != 0) return MOE_ERR_UNSUPPORTED;
+  // 32-bit byte offsets inside a tile of 256 rows
+  if (lda >= (int64_t(1) << 24) || ldb >= (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;
+  if (ceil_div(s->m, 64) * ceil_div(s->n, 64) >= (int64_t(1) << 30)) return MOE_ERR_UNSUPPORTED;   // tile indices
+  return MOE_OK;
+}
+
+moe_status moe_matmul_fp8_workspace_size(const moe_matmul_shape* shape, size_t* bytes) {
+  moe_status rc = check_matmul(shape);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = matmul_fp8_workspace(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_matmul_fp8(const moe_matmul_shape* shape, const uint8_t* a, const float* a_scale, const uint8_t* b,
+                          const float* b_scale, void* out, void* workspace, size_t workspace_bytes,
+                          hipStream_t stream) {
+  moe_status rc = check_matmul(shape);
+  if (rc != MOE_OK) return rc;
+  if (shape->m == 0 || shape->n == 0) return MOE_OK;
+  if (!out || (shape->k > 0 && (!a || !a_scale || !b || !b_scale))) return MOE_ERR_INVALID_ARG;
+  const uintptr_t at = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(out);
+  if (at % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (out == a || out == b || out == a_scale || out == b_scale) return MOE_ERR_INVALID_ARG;
+  const size_t need = matmul_fp8_workspace(*shape);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_matmul_fp8(*shape, a, a_scale, b, b_scale, out, static_cast<float*>(workspace), stream));
+}
+
+moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, uint8_t* codes, float* scales,
+                              hipStream_t stream) {
+  if (rows < 0 || cols < 0) return MOE_ERR_INVALID_ARG;
+  if (cols % 8 != 0 || ceil_div(cols, 64) > 65535) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)rows * cols == 0) return MOE_OK;
+  if (!x_bf16 || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_quantize_act_t(rows, cols, x_bf16, codes, scales, stream));
+}
+
+moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void* h, int8_t* saved, float* scales,
+                               hipStream_t stream) {
+  if (rows < 0 || inter < 0) return MOE_ERR_INVALID_ARG;
+  if (inter % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)rows * inter == 0) return MOE_OK;
+  if (!ab || !saved || !scales || h == ab || saved == ab) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_swiglu8_forward(rows, inter, ab, h, saved, scales, stream));
+}
+
+moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, const int8_t* saved, const float* scales,
+                                void* d_ab, void* h, hipStream_t stream) {
+  if (rows < 0 || inter < 0) return MOE_ERR_INVALID_ARG;
+  if (inter % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)rows * inter == 0) return MOE_OK;
+  if (!dh || !saved || !scales || !d_ab || d_ab == saved || d_ab == dh || h == dh || h == d_ab || h == saved)
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_swiglu8_backward(rows, inter, dh, saved, scales, d_ab, h, stream));
 }
 
 const char* moe_status_string(int32_t status) {

@@ -217,4 +217,23 @@ hipError_t launch_quantize_act(int64_t rows, int32_t cols, const void* x, uint8_
 hipError_t launch_quantize_weights(int32_t n_mats, int32_t rows, int32_t cols, const void* w,
                                    uint8_t* codes, float* scales, hipStream_t st);
 
+// routing from given logits (gate.hip); counts: int32 [gate_blocks, N] scratch (unused without load)
+int64_t gate_blocks(const moe_gate_config& c);
+hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float* bias, int32_t* idx, float* gate,
+                       int32_t* load, int32_t* counts, hipStream_t st);
+hipError_t launch_gate_backward(const moe_gate_config& c, const void* logits, const int32_t* idx, const float* d_gate,
+                                void* d_logits, int64_t d_ld, hipStream_t st);
+
+// dense FP8 products (matmul_fp8.hip)
+size_t matmul_fp8_workspace(const moe_matmul_shape& s);
+hipError_t launch_matmul_fp8(const moe_matmul_shape& s, const uint8_t* a, const float* a_scale, const uint8_t* b,
+                             const float* b_scale, void* out, float* ws, hipStream_t st);
+hipError_t launch_quantize_act_t(int rows, int cols, const void* x, uint8_t* codes, float* scales, hipStream_t st);
+
+// SwiGLU with 8-bit saved inputs (swiglu8.hip); h may be null
+hipError_t launch_swiglu8_forward(int64_t rows, int I, const void* ab, void* h, int8_t* codes, float* scales,
+                                  hipStream_t st);
+hipError_t launch_swiglu8_backward(int64_t rows, int I, const void* dh, const int8_t* codes, const float* scales,
+                                   void* dab, void* h, hipStream_t st);
+
 }  // namespace moe

@@ -1,0 +1,116 @@
+"""Host-side refusals of the gate, the FP8 product and the 8-bit SwiGLU: the documented status, nothing launched."""
+import ctypes
+
+import pytest
+
+import mixture_experts_layer_adjusted_amd as moe
+from mixture_experts_layer_adjusted_amd import binding
+
+lib = binding.raw_lib()
+P = [ctypes.c_void_p(0x10000 * (i + 1)) for i in range(8)]     # plausible, never dereferenced
+BIG = ctypes.c_size_t(1 << 40)
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+def gate(**kw):
+    d = dict(tokens=100, n_routed=64, top_k=4, logits_dtype=0, score=0, n_groups=1, topk_groups=1, group_score=0,
+             renormalize=True, scale=1.0, logits_ld=0)
+    d.update(kw)
+    return moe.make_gate_config(**d)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=-1), INVALID), (dict(n_routed=0), INVALID), (dict(top_k=0), INVALID), (dict(top_k=65), INVALID),
+    (dict(logits_dtype=2), INVALID), (dict(score=2), INVALID), (dict(group_score=-1), INVALID),
+    (dict(n_groups=0), INVALID), (dict(n_groups=3), INVALID), (dict(n_groups=4, topk_groups=5), INVALID),
+    (dict(n_groups=4, topk_groups=0), INVALID), (dict(n_groups=32, topk_groups=1), INVALID),
+    (dict(n_routed=512, n_groups=128), INVALID), (dict(logits_ld=63), INVALID), (dict(scale=float("inf")), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(n_routed=513), UNSUPPORTED), (dict(top_k=33), UNSUPPORTED),
+    (dict(tokens=1 << 30), UNSUPPORTED), (dict(), OK), (dict(logits_ld=64, n_groups=64, topk_groups=4), OK),
+])
+def test_gate_limits(kw, status):
+    c, n = gate(**kw), ctypes.c_size_t(0)
+    assert lib.moe_gate_workspace_size(ctypes.byref(c), ctypes.byref(n)) == status
+    if status:
+        assert lib.moe_gate(ctypes.byref(c), P[0], P[1], P[2], P[3], P[4], P[5], BIG, None) == status
+        assert lib.moe_gate_backward(ctypes.byref(c), P[0], P[1], P[2], P[3], 0, None) == status
+
+
+def test_gate_pointers_and_workspace():
+    c, n = gate(), ctypes.c_size_t(0)
+    assert lib.moe_gate_workspace_size(ctypes.byref(c), None) == INVALID
+    assert lib.moe_gate_workspace_size(None, ctypes.byref(n)) == INVALID
+    assert lib.moe_gate_workspace_size(ctypes.byref(c), ctypes.byref(n)) == OK and n.value > 0
+    call = lambda *a: lib.moe_gate(ctypes.byref(c), *a, None)  # noqa: E731
+    for i in (0, 2, 3):
+        a = [P[0], P[1], P[2], P[3], P[4], P[5], BIG]
+        a[i] = None
+        assert call(*a) == INVALID
+    assert call(P[0], P[1], P[2], P[3], P[4], P[5], ctypes.c_size_t(n.value - 1)) == WORKSPACE
+    assert call(P[0], P[1], P[2], P[3], P[4], None, BIG) == INVALID
+    back = lambda *a: lib.moe_gate_backward(ctypes.byref(c), *a, None)  # noqa: E731
+    assert back(P[0], P[1], P[2], P[0], 0) == INVALID            # in place
+    assert back(P[0], P[1], P[2], P[3], 63) == INVALID
+    for i in range(4):
+        a = list(P[:4])
+        a[i] = None
+        assert back(*a, 0) == INVALID
+    none = gate(tokens=0)
+    assert lib.moe_gate(ctypes.byref(none), None, None, None, None, None, None, 0, None) == OK
+    assert lib.moe_gate_backward(ctypes.byref(none), None, None, None, None, 0, None) == OK
+
+
+@pytest.mark.parametrize("args,kw,status", [
+    ((-1, 32, 128, 0, 1), {}, INVALID), ((4, 32, 128, 3, 1), {}, INVALID), ((4, 32, 128, 0, 2), {}, INVALID),
+    ((4, 32, 128, 0, 1), dict(lda=112), INVALID), ((4, 32, 128, 1, 1), dict(ldb=16), INVALID),
+    ((4, 32, 128, 0, 1), dict(ldo=28), INVALID), ((4, 24, 128, 0, 1), {}, UNSUPPORTED),
+    ((4, 32, 64, 0, 1), {}, UNSUPPORTED), ((4, 32, 128, 0, 1), dict(lda=136), UNSUPPORTED),
+    ((4, 32, 128, 0, 1), dict(ldb=1 << 24), UNSUPPORTED), ((4, 32, 128, 0, 1), dict(ldo=34), UNSUPPORTED),
+    (((1 << 31) - 1, 1 << 24, 128, 0, 1), {}, UNSUPPORTED),
+    ((4, 32, 128, 0, 1), {}, OK), ((4, 32, 128, 1, 0), dict(ldb=48), OK), ((0, 0, 0, 2, 0), {}, OK),
+])
+def test_matmul_limits(args, kw, status):
+    s, n = moe.make_matmul_shape(*args, **kw), ctypes.c_size_t(0)
+    assert lib.moe_matmul_fp8_workspace_size(ctypes.byref(s), ctypes.byref(n)) == status
+    if status:
+        assert lib.moe_matmul_fp8(ctypes.byref(s), P[0], P[1], P[2], P[3], P[4], P[5], BIG, None) == status
+
+
+def test_matmul_pointers_and_workspace():
+    s, n = moe.make_matmul_shape(200, 512, 8192, moe.MOE_FP8_FORWARD, moe.MOE_DTYPE_BF16), ctypes.c_size_t(0)
+    assert lib.moe_matmul_fp8_workspace_size(ctypes.byref(s), ctypes.byref(n)) == OK and n.value > 0   # split
+    call = lambda *a: lib.moe_matmul_fp8(ctypes.byref(s), *a, None)  # noqa: E731
+    assert call(*P[:6], ctypes.c_size_t(n.value - 1)) == WORKSPACE
+    assert call(*P[:5], None, BIG) == INVALID
+    for i in range(5):
+        a = list(P[:6])
+        a[i] = None
+        assert call(*a, BIG) == INVALID
+    for i in (0, 2, 4):
+        a = list(P[:6])
+        a[i] = ctypes.c_void_p(a[i].value + 8)                                # not 16-byte aligned
+        assert call(*a, BIG) == INVALID
+    assert call(P[0], P[1], P[2], P[3], P[0], P[5], BIG) == INVALID           # out is a
+    assert lib.moe_matmul_fp8_workspace_size(ctypes.byref(s), None) == INVALID
+    empty = moe.make_matmul_shape(0, 512, 128, moe.MOE_FP8_FORWARD, moe.MOE_DTYPE_BF16)
+    assert lib.moe_matmul_fp8(ctypes.byref(empty), None, None, None, None, None, None, 0, None) == OK
+
+
+def test_quantize_act_t_and_swiglu8():
+    q = lambda r, c, *a: lib.moe_quantize_act_t(r, c, *a, None)  # noqa: E731
+    assert q(-1, 8, *P[:3]) == INVALID and q(4, 12, *P[:3]) == UNSUPPORTED and q(4, 8 << 20, *P[:3]) == UNSUPPORTED
+    assert q(4, 8, None, P[1], P[2]) == INVALID and q(0, 8, None, None, None) == OK
+    f = lambda r, i, *a: lib.moe_swiglu_forward8(r, i, *a, None)  # noqa: E731
+    assert f(-1, 128, *P[:4]) == INVALID and f(4, 192, *P[:4]) == UNSUPPORTED and f(0, 128, *[None] * 4) == OK
+    for i in (0, 2, 3):
+        a = list(P[:4])
+        a[i] = None
+        assert f(4, 128, *a) == INVALID
+    assert f(4, 128, P[0], P[0], P[2], P[3]) == INVALID and f(4, 128, P[0], P[1], P[0], P[3]) == INVALID
+    b = lambda r, i, *a: lib.moe_swiglu_backward8(r, i, *a, None)  # noqa: E731
+    assert b(4, -128, *P[:5]) == INVALID and b(4, 64, *P[:5]) == UNSUPPORTED and b(4, 0, *[None] * 5) == OK
+    for i in range(4):
+        a = list(P[:5])
+        a[i] = None
+        assert b(4, 128, *a) == INVALID
+    assert b(4, 128, P[0], P[1], P[2], P[1], P[4]) == INVALID and b(4, 128, P[0], P[1], P[2], P[3], P[0]) == INVALID
