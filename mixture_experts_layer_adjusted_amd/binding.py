@@ -114,10 +114,21 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
+def _addr(t):
+    """A tensor's address for a void* argument, without the c_void_p in between."""
+    return None if t is None else t.data_ptr()
+
+
+# torch's own short way to the current stream's handle (0.2 us against 2.7 for the Stream object), if it is there
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(fn, rc):
@@ -274,13 +285,13 @@ def moe_gate_workspace_size(config: GateConfig) -> int:
 
 
 def moe_gate(config, logits, bias, topk_idx, topk_gate, expert_load, workspace, stream=None):
-    _check("moe_gate", _lib.moe_gate(ctypes.byref(config), _ptr(logits), _ptr(bias), _ptr(topk_idx), _ptr(topk_gate),
-                                     _ptr(expert_load), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _check("moe_gate", _lib.moe_gate(ctypes.byref(config), _addr(logits), _addr(bias), _addr(topk_idx), _addr(topk_gate),
+                                     _addr(expert_load), _addr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def moe_gate_backward(config, logits, topk_idx, d_gate, d_logits, d_logits_ld=0, stream=None):
-    _check("moe_gate_backward", _lib.moe_gate_backward(ctypes.byref(config), _ptr(logits), _ptr(topk_idx),
-                                                       _ptr(d_gate), _ptr(d_logits), d_logits_ld, _stream(stream)))
+    _check("moe_gate_backward", _lib.moe_gate_backward(ctypes.byref(config), _addr(logits), _addr(topk_idx),
+                                                       _addr(d_gate), _addr(d_logits), d_logits_ld, _stream(stream)))
 
 
 def make_matmul_shape(m, n, k, form, out_dtype, accumulate=False, lda=0, ldb=0, ldo=0) -> MatmulShape:
@@ -294,23 +305,23 @@ def moe_matmul_fp8_workspace_size(shape: MatmulShape) -> int:
 
 
 def moe_matmul_fp8(shape, a, a_scale, b, b_scale, out, workspace=None, stream=None):
-    _check("moe_matmul_fp8", _lib.moe_matmul_fp8(ctypes.byref(shape), _ptr(a), _ptr(a_scale), _ptr(b), _ptr(b_scale),
-                                                 _ptr(out), _ptr(workspace), _nbytes(workspace), _stream(stream)))
+    _check("moe_matmul_fp8", _lib.moe_matmul_fp8(ctypes.byref(shape), _addr(a), _addr(a_scale), _addr(b), _addr(b_scale),
+                                                 _addr(out), _addr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def moe_quantize_act_t(rows, cols, x_bf16, codes, scales, stream=None):
-    _check("moe_quantize_act_t", _lib.moe_quantize_act_t(rows, cols, _ptr(x_bf16), _ptr(codes), _ptr(scales),
+    _check("moe_quantize_act_t", _lib.moe_quantize_act_t(rows, cols, _addr(x_bf16), _addr(codes), _addr(scales),
                                                          _stream(stream)))
 
 
 def moe_swiglu_forward8(rows, inter, ab, h, saved, scales, stream=None):
-    _check("moe_swiglu_forward8", _lib.moe_swiglu_forward8(rows, inter, _ptr(ab), _ptr(h), _ptr(saved), _ptr(scales),
+    _check("moe_swiglu_forward8", _lib.moe_swiglu_forward8(rows, inter, _addr(ab), _addr(h), _addr(saved), _addr(scales),
                                                            _stream(stream)))
 
 
 def moe_swiglu_backward8(rows, inter, dh, saved, scales, d_ab, h=None, stream=None):
-    _check("moe_swiglu_backward8", _lib.moe_swiglu_backward8(rows, inter, _ptr(dh), _ptr(saved), _ptr(scales),
-                                                             _ptr(d_ab), _ptr(h), _stream(stream)))
+    _check("moe_swiglu_backward8", _lib.moe_swiglu_backward8(rows, inter, _addr(dh), _addr(saved), _addr(scales),
+                                                             _addr(d_ab), _addr(h), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

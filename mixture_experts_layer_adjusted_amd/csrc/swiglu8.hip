@@ -54,15 +54,22 @@ __device__ __forceinline__ float run_scale(const float (&v)[8]) {
   return m == 0u ? 1.0f : __uint_as_float(m) * (1.0f / 127.0f);
 }
 
-__device__ __forceinline__ uint32_t code4(const float* v, float scale) {
-  uint32_t w = 0;
+// The codes of a lane's eight values.  The quotients are correctly rounded without a division each: with r the
+// rounded 1 / scale and q = x r, the remainder e = x - q scale is exact in one fma and q + e r is the rounded quotient
+// (Markstein).  Scales below 2^-64, where the remainder could underflow, divide (and a subnormal scale is so coarse
+// that its quotients can pass 127).
+__device__ __forceinline__ uint2 code8(const float (&v)[8], float scale) {
+  const float r = __fdiv_rn(1.0f, scale);
+  const bool tiny = scale < 0x1p-64f;
+  uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // (a subnormal scale is coarse: its quotients can pass 127)
-    const int c = (int)fminf(fmaxf(rintf(__fdiv_rn(v[i], scale)), -127.0f), 127.0f);
-    w |= (uint32_t)(c & 0xFF) << (8 * i);
+  for (int i = 0; i < 8; ++i) {
+    float q = v[i] * r;
+    q = fmaf(fmaf(-q, scale, v[i]), r, q);
+    if (tiny) q = fminf(fmaxf(__fdiv_rn(v[i], scale), -127.0f), 127.0f);
+    w[i / 4] |= ((uint32_t)(int)rintf(q) & 0xFFu) << (8 * (i % 4));
   }
-  return scale != scale ? 0u : w;
+  return scale != scale ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ void decode8(const uint2& q, float scale, float (&v)[8]) {
@@ -87,8 +94,8 @@ __global__ void __launch_bounds__(kThreads) swiglu8_fwd_kernel(const uint16_t* _
     unpack8(*reinterpret_cast<const uint4*>(ab + r * 2 * I + I + f), b);
     // (the 16 lanes of a run are all here or none: units are whole runs)
     const float sa = run_scale(a), sb = run_scale(b);
-    *reinterpret_cast<uint2*>(codes + r * 2 * I + f) = make_uint2(code4(a, sa), code4(a + 4, sa));
-    *reinterpret_cast<uint2*>(codes + r * 2 * I + I + f) = make_uint2(code4(b, sb), code4(b + 4, sb));
+    *reinterpret_cast<uint2*>(codes + r * 2 * I + f) = code8(a, sa);
+    *reinterpret_cast<uint2*>(codes + r * 2 * I + I + f) = code8(b, sb);
     if (sub == 0) {
       scales[r * 2 * per_row + run] = sa;
       scales[r * 2 * per_row + per_row + run] = sb;
