@@ -23,7 +23,6 @@ namespace {
 
 constexpr int kBK = 128;            // elements (bytes) of one scale block
 constexpr int kXcds = 8;
-constexpr int kE8M0One = 127;       // E8M0 encoding of 2^0
 constexpr int kGroupM = 4;          // M-tiles per block of the tile order
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -73,9 +72,11 @@ __device__ __forceinline__ void store4(const MatmulArgs& g, int64_t row, int col
   }
 }
 
+// at most N of this wavefront's loads in flight, and none of its LDS reads
 template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
+__device__ __forceinline__ void wait_counts() {
+  static_assert(N < 64, "vmcnt");
+  __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4));
 }
 
 // ---- tiles staged in LDS -------------------------------------------------------------------------------------
@@ -123,15 +124,19 @@ struct Frag<true> {
       }
   }
 };
-__device__ __forceinline__ f32x4 contract(const Frag<false>& w, const Frag<false>& x) {
+__device__ __forceinline__ void contract(const Frag<false>* w, const Frag<false>& x, f32x4 (&p)[1]) {
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w.v, x.v, zero, 0, 0, 0, kE8M0One, 0, kE8M0One);
+  p[0] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w->v, x.v, zero, 0, 0, 0, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 contract(const Frag<true>& w, const Frag<true>& x) {
-  f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+// (U blocks in turn, so that no instruction waits for the one before)
+template <int U>
+__device__ __forceinline__ void contract(const Frag<true>* w, const Frag<true>& x, f32x4 (&p)[U]) {
 #pragma unroll
-  for (int s = 0; s < 4; ++s) p = __builtin_amdgcn_mfma_f32_16x16x32_f16(w.v[s], x.v[s], p, 0, 0, 0);
-  return p;
+  for (int u = 0; u < U; ++u) p[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < 4; ++s)
+#pragma unroll
+    for (int u = 0; u < U; ++u) p[u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(w[u].v[s], x.v[s], p[u], 0, 0, 0);
 }
 
 // 64 lanes x 16 (or 4) bytes at base + off + step into LDS at dst + 16 (or 4) lane
@@ -142,37 +147,61 @@ __device__ __forceinline__ void load_lds4(__amdgpu_buffer_rsrc_t base, uint8_t* 
   __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (lds_void_t*)dst, 4, off, step, 0, 0);
 }
 
-template <int BM, int BN, int WM, int WN, int STAGES>
+template <int FORM, int BM, int BN, int WM, int WN, int STAGES>
 struct TileShape {
+  static constexpr bool KN = FORM == MOE_FP8_INPUT_GRAD, ROWS = FORM == MOE_FP8_WEIGHT_GRAD;
   static constexpr int kWaves = WM * WN, kThreads = kWaves * 64;
   static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;
   static constexpr int kADma = BM / 8 / kWaves, kBDma = BN / 8 / kWaves;   // 1 KB loads of a wavefront per stage
   static constexpr int kDataBytes = (BM + BN) * kBK;
-  static constexpr int kScaleBytes = kWaves * 256;                          // 64 scales per wavefront
-  static constexpr int kLds = STAGES * (kDataBytes + kScaleBytes);
-  static_assert(BM % 64 == 0 && (BM + BN) / 64 <= kWaves, "a wavefront loads 64 scales at most");
+  static constexpr int kSpan = ROWS && STAGES == 3 ? 2 : 4;                 // K blocks whose scales are loaded together
+  static constexpr int kPart = 64 / kSpan;                                  // rows of one scale load
+  static constexpr int kAScale = BM * kSpan * 4;                            // a's scales of kSpan K blocks
+  static constexpr int kBScale = ROWS ? BN * kSpan * 4 : 256;               // b's: rows, or up to 16 column blocks
+  static constexpr int kScales = STAGES * kDataBytes;                        // where they start
+  static constexpr int kUnread = kScales + 3 * (kAScale + kBScale);          // where the L2 prefetch goes
+  static constexpr bool kPrefetch = STAGES == 2 && BM == 256 && !KN;
+  static constexpr int kLds = kUnread + (kPrefetch ? kWaves * 256 : 0);
+  static_assert(BM % 64 == 0 && BM / 64 + (ROWS ? BN / 64 : 1) <= kWaves, "one scale load of a wavefront per stage");
+  static_assert(STAGES - 1 <= kSpan, "three spans of scales hold all that is in use");
   static_assert(kADma * 8 * kWaves == BM && kBDma * 8 * kWaves == BN, "whole loads");
 };
 
-// One BM x BN tile of the output over the K blocks of slice blockIdx.y.  STAGES stages of one K block each, filled
-// by direct loads STAGES - 1 blocks ahead.  Rows and columns past the matrix read a valid row or column and are
-// not stored.
+// One BM x BN tile of the output over one slice of the K blocks.  STAGES stages of one K block each, filled by direct
+// loads.  Rows and columns past the matrix read a valid row or column and are not stored.
+//
+// A K block is worked off in row blocks of 16.  Before the last one, every fragment of the stage has been read: there
+// the wavefronts meet (the next stage has landed, this one may be filled again), and the next K block's first fragments
+// are on their way while the last row block's products run, so that the matrix units do not wait at a K block's start.
+//
+// Scales: a row's are neighbours along K, rows are far apart, and a load costs by the cache lines it touches (64 rows
+// a load kept the address unit busy 183 cycles, 29 a load of codes).  So a load takes several K blocks (a span) of fewer
+// rows, one load of a wavefront per stage, a span ahead, into one of three spans in LDS: [kPart rows][K block][row].
+//
+// L2: with two stages, what misses L2 is late (all hits: 199 us against 237 at 8192 x 4096 x 7168).  Of the tiles an XCD
+// works on at a time, eight share a's rows and four b's, so each asks for an eighth and a quarter of the lines of the
+// stage after those in flight: one load of a wavefront, into LDS that nothing reads (237 -> 210 us; every tile asking
+// for all its lines gained nothing).  More stages do not need it.
 template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES>
-__global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g, int MT, int NT) {
-  using S = TileShape<BM, BN, WM, WN, STAGES>;
+__global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g, int MT, int NT, int splits, int chunk) {
   constexpr bool KN = FORM == MOE_FP8_INPUT_GRAD, ROWS = FORM == MOE_FP8_WEIGHT_GRAD;
+  using S = TileShape<FORM, BM, BN, WM, WN, STAGES>;
   constexpr int kMB = S::kMB, kNB = S::kNB;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-  uint8_t* const scales = lds + STAGES * S::kDataBytes;
-  const int L = (int)xcd_logical(blockIdx.x);
-  if (L >= MT * NT) return;
+  constexpr int kSpan = S::kSpan, kPart = S::kPart;
+  uint8_t* const ascales = lds + S::kScales;
+  uint8_t* const bscales = ascales + 3 * S::kAScale;
+  // tiles of one slice after another, dealt to the XCDs in runs of `chunk`
+  const int64_t Ls = xcd_logical(blockIdx.x, chunk);
+  if (Ls >= (int64_t)MT * NT * splits) return;
+  const int slice = (int)(Ls / (MT * NT)), L = (int)(Ls - (int64_t)slice * MT * NT);
   const int grp = L / (kGroupM * NT), gm = min(kGroupM, MT - grp * kGroupM), rem = L - grp * kGroupM * NT;
   const int m0 = (grp * kGroupM + rem % gm) * BM, n0 = rem / gm * BN;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int KB = g.k / kBK;
-  const int kb0 = blockIdx.y * g.kb_per_split, nk = min(g.kb_per_split, KB - kb0);
+  const int kb0 = slice * g.kb_per_split, nk = min(g.kb_per_split, KB - kb0);
 
   // ---- where this lane's loads come from: 32-bit byte offsets from the tile's first row
   uint32_t aoff[S::kADma], boff[S::kBDma];
@@ -193,41 +222,65 @@ __global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g,
       boff[i] = (uint32_t)min(r, g.n - 1 - n0) * (uint32_t)g.ldb + src_chunk(r, lane & 7);
     }
   }
-  // scales: the first BM / 64 wavefronts a's rows, the next b's (its rows, or lane i its column block i);
-  // the others repeat a's, so that every wavefront has the same loads in flight
-  const float* sbase = g.a_scale + (int64_t)m0 * KB;
-  uint32_t soff = 0, sstep = 4;
-  if (wave < BM / 64 || wave >= (BM + BN) / 64 || (!ROWS && wave > BM / 64)) {
-    soff = (uint32_t)min((wave % (BM / 64)) * 64 + lane, g.m - 1 - m0) * (uint32_t)KB * 4;
-  } else if (ROWS) {
-    sbase = g.b_scale + (int64_t)n0 * KB;
-    soff = (uint32_t)min((wave - BM / 64) * 64 + lane, g.n - 1 - n0) * (uint32_t)KB * 4;
-  } else {
-    const int blk = min(n0 / kBK + lane, g.nblk - 1);
-    sbase = g.b_scale;
-    soff = (uint32_t)(KN ? blk : blk * KB) * 4;
-    sstep = KN ? g.nblk * 4 : 4;
-  }
+  // scales: in the load of stage s, lane (kb, r) takes K block kb and row r of part (s mod kSpan) BM / 64 + w of the span
+  // after s's; w: the wavefront among the first BM / 64 (a's rows) or the next (b's rows, or all the span's column blocks
+  // in each load).  The others repeat a's, so that every wavefront has the same loads in flight.
+  constexpr int kAW = BM / 64, kBW = ROWS ? BN / 64 : 1;
+  const bool for_a = wave < kAW || wave >= kAW + kBW, for_rows = for_a || ROWS;
+  const int s_wave = for_a ? wave % kAW : wave - kAW;
+  const int s_step = for_a ? kAW : ROWS ? kBW : 0;        // parts of one stage's loads
+  const int s_row = (for_rows ? s_wave * kPart : n0 / kBK) + lane % kPart;
+  const int s_last = for_a ? g.m - 1 - m0 : ROWS ? g.n - 1 - n0 : g.nblk - 1;
+  const uint32_t s_rowstep = KN && !for_a ? 1 : (uint32_t)KB, s_kstep = KN && !for_a ? (uint32_t)g.nblk : 1;
+  uint8_t* const s_dst = (for_a ? ascales : bscales) + (for_rows ? s_wave * 256 : 0);
+  const int s_span = for_a ? S::kAScale : S::kBScale;
   const uint8_t* abase = g.a + (int64_t)m0 * g.lda;
   const uint8_t* bbase = KN ? g.b + n0 : g.b + (int64_t)n0 * g.ldb;
   const __amdgpu_buffer_rsrc_t abuf =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(abase), (short)0, -1, 0x00020000);
+  const float* sbase = for_a ? g.a_scale + (int64_t)m0 * KB : ROWS ? g.b_scale + (int64_t)n0 * KB : g.b_scale;
   const __amdgpu_buffer_rsrc_t sbuf =
       __builtin_amdgcn_make_buffer_rsrc(const_cast<float*>(sbase), (short)0, -1, 0x00020000);
-  auto issue = [&](int kt) {
-    const int slot = kt % STAGES;
-    uint8_t* st = lds + slot * S::kDataBytes;
-    const uint32_t k0 = (uint32_t)(kb0 + kt) * kBK;
-#pragma unroll
-    for (int i = 0; i < S::kADma; ++i) load_lds16(abuf, st + (wave * S::kADma + i) * 1024, aoff[i], k0);
-    const __amdgpu_buffer_rsrc_t bbuf = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint8_t*>(KN ? bbase + (int64_t)k0 * g.ldb : bbase), (short)0, -1, 0x00020000);
-#pragma unroll
-    for (int i = 0; i < S::kBDma; ++i)
-      load_lds16(bbuf, st + BM * kBK + (wave * S::kBDma + i) * 1024, boff[i], KN ? 0u : k0);
-    load_lds4(sbuf, scales + slot * S::kScaleBytes + wave * 256, soff, (uint32_t)(kb0 + kt) * sstep);
+  auto issue_scales = [&](int span, int j) {
+    const uint32_t kb = (uint32_t)min(kb0 + span * kSpan + lane / kPart, KB - 1);
+    const uint32_t r = (uint32_t)min(s_row + j * s_step * kPart, s_last);
+    load_lds4(sbuf, s_dst + span % 3 * s_span + j * s_step * 256, (r * s_rowstep + kb * s_kstep) * 4, 0);
   };
+  // load p of this wavefront's share of stage kt: a's codes, b's, scales.  Past the last K block the last one again:
+  // no branch in the loop, where the compiler would carry folds across it
   constexpr int kLoads = S::kADma + S::kBDma + 1;
+  // what is issued after a stage's loads until the stage has to be there: its prefetch, then STAGES - 2 stages with theirs
+  constexpr int kPf = S::kPrefetch ? 1 : 0, kYounger = (STAGES - 2) * (kLoads + kPf) + kPf;
+  auto issue_load = [&](int kt, int p) {
+    uint8_t* st = lds + kt % STAGES * S::kDataBytes;
+    const uint32_t k0 = (uint32_t)(kb0 + min(kt, nk - 1)) * kBK;
+    if (p < S::kADma) {
+      load_lds16(abuf, st + (wave * S::kADma + p) * 1024, aoff[p], k0);
+    } else if (p < kLoads - 1) {
+      const __amdgpu_buffer_rsrc_t bbuf = __builtin_amdgcn_make_buffer_rsrc(
+          const_cast<uint8_t*>(KN ? bbase + (int64_t)k0 * g.ldb : bbase), (short)0, -1, 0x00020000);
+      const int i = p - S::kADma;
+      load_lds16(bbuf, st + BM * kBK + (wave * S::kBDma + i) * 1024, boff[i], KN ? 0u : k0);
+    } else {
+      issue_scales(kt / kSpan + 1, kt % kSpan);
+    }
+  };
+
+  // L2 prefetch: a wavefront's lines of a's rows (the first quarter of the wavefronts) or of b's
+  constexpr int kPfA = S::kWaves / 4, kPfB = S::kWaves - kPfA;
+  constexpr int kEachA = (BM / 8 + kPfA - 1) / kPfA, kEachB = (BN / 4 + kPfB - 1) / kPfB;
+  static_assert(kEachA <= 64 && kEachB <= 64, "a lane a line");
+  const bool pf_a = wave < kPfA;
+  const int pf_line = pf_a ? rem / gm % 8 * (BM / 8) + min(wave * kEachA + lane % kEachA, BM / 8 - 1)
+                           : rem % gm % 4 * (BN / 4) + min((wave - kPfA) * kEachB + lane % kEachB, BN / 4 - 1);
+  const uint32_t pf_off = pf_a ? (uint32_t)min(pf_line, g.m - 1 - m0) * (uint32_t)g.lda
+                               : (uint32_t)min(pf_line, g.n - 1 - n0) * (uint32_t)g.ldb;
+  const __amdgpu_buffer_rsrc_t pf_buf =
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(pf_a ? abase : bbase), (short)0, -1, 0x00020000);
+  auto prefetch = [&](int kt) {
+    if constexpr (S::kPrefetch)
+      load_lds4(pf_buf, lds + S::kUnread + wave * 256, pf_off, (uint32_t)(kb0 + min(kt, nk - 1)) * kBK);
+  };
 
   const int l16 = lane & 15, kq = lane >> 4;
   const int mrow = wm * (BM / WM), ncol = wn * (BN / WN);
@@ -243,73 +296,140 @@ __global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g,
 #pragma unroll
     for (int j = 0; j < kNB; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+  if (nk > 0) {
 #pragma unroll
-  for (int s = 0; s < STAGES - 1; ++s)
-    if (s < nk) issue(s);
-  for (int kt = 0; kt < nk; ++kt) {
-    // stage kt has landed once at most the STAGES - 2 younger ones are in flight
-    if (kt + STAGES - 1 <= nk)
-      wait_vmcnt<(STAGES - 2) * kLoads>();
-    else
-      wait_vmcnt<0>();
-    // every wavefront's part of stage kt is there, and stage kt - 1 is no longer read
+    for (int j = 0; j < kSpan; ++j) issue_scales(0, j);
+#pragma unroll
+    for (int s = 0; s < STAGES - 1; ++s) {
+#pragma unroll
+      for (int p = 0; p < kLoads; ++p) issue_load(s, p);
+      prefetch(STAGES - 1 + s);   // (as in the loop, whose waits count on it)
+    }
+  }
+
+  // Columns are taken kCols blocks at a time (widened fragments are twice as large: half the wavefront's).
+  constexpr int kGroups = EXACT ? 2 : 1, kCols = kNB / kGroups;
+  static_assert(kNB % kGroups == 0 && kMB > 1, "whole groups, and a row block before the last");
+  struct Start {   // a group's column fragments, read ahead
+    i32x8 w[kCols];
+  };
+  i32x8 next;         // the next row block's fragment
+  float sa_next;      // and scale
+  // reads group h of K block kt (stage kt mod STAGES)
+  auto read_start = [&](int kt, int h, Start& s) {
+    const uint8_t* st = lds + kt % STAGES * S::kDataBytes;
+#pragma unroll
+    for (int jj = 0; jj < kCols; ++jj) {
+      const int j = h * kCols + jj;
+      if constexpr (KN) {
+        // ds_read_b64_tr_b8: within 16 lanes, lane s names row 8 q + s / 2 at columns 8 (s % 2)..+7 of the 16 and
+        // receives its own column's eight rows
+        const uint8_t* wt = st + BM * kBK;
+        const int col = ncol + 16 * j + 8 * (lane & 1);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = 32 * kq + 8 * q + (l16 >> 1);
+          const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
+              (lds_i32x2*)(wt + r * BN + (((col >> 4) ^ kn_swz<BN>(r)) << 4) + (col & 15)));
+          s.w[jj][2 * q] = v[0];
+          s.w[jj][2 * q + 1] = v[1];
+        }
+      } else {
+        s.w[jj] = frag_at(st + wr + j * 16 * kBK + c0, st + wr + j * 16 * kBK + c1);
+      }
+    }
+  };
+  // the scale of row r (a multiple of 16, + what the caller adds) in the spans at `at`
+  auto scale_at = [&](const uint8_t* at, int span_bytes, int kt, int r) {
+    return reinterpret_cast<const float*>(at + kt / kSpan % 3 * span_bytes) + r / kPart * 64 + kt % kSpan * kPart + r % kPart;
+  };
+  auto read_rows = [&](int kt, int i) {   // row block i's fragment and scale
+    const uint8_t* st = lds + kt % STAGES * S::kDataBytes;
+    next = frag_at(st + xr + i * 16 * kBK + c0, st + xr + i * 16 * kBK + c1);
+    sa_next = scale_at(ascales, S::kAScale, kt, mrow + 16 * i)[l16];
+  };
+  // Group h of K block kt from `now`; `then` receives the start of the group after it.  Pieces of kUnit blocks: a
+  // piece's instructions, then the fold of the piece kLag before it, whose results are there by then, in this order (left
+  // to itself the compiler folds each result at once, waiting for it).
+  auto group = [&](int kt, int h, const Start& now, Start& then) {
+    constexpr int kUnit = EXACT && kCols > 1 ? 2 : 1, kLag = EXACT ? 1 : 2, kPer = kCols / kUnit, kPieces = kMB * kPer;
+    f32x4 part[kLag + 1][kUnit];
+    Frag<EXACT> wf[kCols], xf;
+    float sa[kMB], sw = 0.0f;
+    f32x4 swr[kCols];   // weight gradient: the lane's four columns'
+    if constexpr (!ROWS) sw = scale_at(bscales, S::kBScale, kt, 0)[wblk];
+#pragma unroll
+    for (int jj = 0; jj < kCols; ++jj) {
+      wf[jj].set(now.w[jj]);
+      if constexpr (ROWS) 
+        swr[jj] = *reinterpret_cast<const f32x4*>(scale_at(bscales, S::kBScale, kt, ncol + 16 * (h * kCols + jj)) + 4 * kq);
+    }
+#pragma unroll
+    for (int n = 0; n < kPieces + kLag; ++n) {
+      if (n < kPieces) {
+        const int i = n / kPer, jj = n % kPer * kUnit;
+        if (jj == 0) {
+          xf.set(next);
+          sa[i] = sa_next;
+          if (i + 1 < kMB) {
+            read_rows(kt, i + 1);
+          } else if (h + 1 < kGroups) {
+            read_start(kt, h + 1, then);
+            read_rows(kt, 0);
+          } else {
+            // the next stage has landed, and this wavefront's reads of this stage are done
+            prefetch(kt + STAGES);
+            wait_counts<kYounger>();
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_s_barrier();
+            asm volatile("" ::: "memory");
+            read_start(kt + 1, 0, then);
+            read_rows(kt + 1, 0);
+          }
+        }
+        // loads of the stage that the last meeting set free, one at a time between the pieces: issued together they
+        // fill the address unit's queue, and the wavefronts stand before it
+        constexpr int kSlots = kGroups * kPieces - kPer, kEach = (kLoads + kSlots - 1) / kSlots;   // all before the meeting
+#pragma unroll
+        for (int p = (h * kPieces + n) * kEach; p < (h * kPieces + n + 1) * kEach; ++p)
+          if (p < kLoads) issue_load(kt + STAGES - 1, p);
+        contract(&wf[jj], xf, part[n % (kLag + 1)]);
+      }
+      if (n >= kLag) {
+        const int q = n - kLag, i = q / kPer;
+#pragma unroll
+        for (int u = 0; u < kUnit; ++u) {
+          const int jj = q % kPer * kUnit + u;
+          const f32x4& p = part[q % (kLag + 1)][u];
+          const float f = ROWS ? sa[i] : sa[i] * sw;
+          f32x4& c = acc[i][h * kCols + jj];
+#pragma unroll
+          for (int v = 0; v < 4; ++v) c[v] = fmaf(p[v], ROWS ? f * swr[jj][v] : f, c[v]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  if (nk > 0) {
+    wait_counts<kYounger>();
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    if (kt + STAGES - 1 < nk) issue(kt + STAGES - 1);
-    const uint8_t* st = lds + (kt % STAGES) * S::kDataBytes;
-    const float* sc = reinterpret_cast<const float*>(scales + (kt % STAGES) * S::kScaleBytes);
-    const float sw = ROWS ? 0.0f : sc[BM + wblk];
-    // (widened fragments are twice as large: half the wavefront's columns at a time)
-    constexpr int kCols = EXACT ? kNB / 2 : kNB;
-#pragma unroll
-    for (int j0 = 0; j0 < kNB; j0 += kCols) {
-      if constexpr (EXACT) __builtin_amdgcn_sched_barrier(0);   // or the second half's reads move up, and spill
-      Frag<EXACT> wf[kCols];
-      f32x4 swr[kCols];
-#pragma unroll
-      for (int jj = 0; jj < kCols; ++jj) {
-        const int j = j0 + jj;
-        if constexpr (KN) {
-          // ds_read_b64_tr_b8: within 16 lanes, lane s names row 8 j + s / 2 at columns 8 (s % 2)..+7 of the 16 and
-          // receives its own column's eight rows
-          const uint8_t* wt = st + BM * kBK;
-          const int col = ncol + 16 * j + 8 * (lane & 1);
-          i32x8 f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int r = 32 * kq + 8 * q + (l16 >> 1);
-            const i32x2 v = __builtin_amdgcn_ds_read_tr8_b64_v2i32(
-                (lds_i32x2*)(wt + r * BN + (((col >> 4) ^ kn_swz<BN>(r)) << 4) + (col & 15)));
-            f[2 * q] = v[0];
-            f[2 * q + 1] = v[1];
-          }
-          wf[jj].set(f);
-        } else {
-          wf[jj].set(frag_at(st + wr + j * 16 * kBK + c0, st + wr + j * 16 * kBK + c1));
-        }
-        if constexpr (ROWS) swr[jj] = *reinterpret_cast<const f32x4*>(sc + BM + ncol + 16 * j + 4 * kq);
+    Start even, odd;
+    read_start(0, 0, even);
+    read_rows(0, 0);
+    if constexpr (kGroups == 2) {
+      for (int kt = 0; kt < nk; ++kt) {
+        group(kt, 0, even, odd);
+        group(kt, 1, odd, even);
       }
-      i32x8 xf_next = frag_at(st + xr + c0, st + xr + c1);
-      float sa_next = sc[mrow + l16];
-#pragma unroll
-      for (int i = 0; i < kMB; ++i) {
-        Frag<EXACT> xf;
-        xf.set(xf_next);
-        const float sa = sa_next;
-        if (i + 1 < kMB) {
-          xf_next = frag_at(st + xr + (i + 1) * 16 * kBK + c0, st + xr + (i + 1) * 16 * kBK + c1);
-          sa_next = sc[mrow + (i + 1) * 16 + l16];
-        }
-        const float f = sa * sw;
-#pragma unroll
-        for (int jj = 0; jj < kCols; ++jj) {
-          const f32x4 p = contract(wf[jj], xf);
-          f32x4& c = acc[i][j0 + jj];
-#pragma unroll
-          for (int v = 0; v < 4; ++v) c[v] = fmaf(p[v], ROWS ? sa * swr[jj][v] : f, c[v]);
-        }
+    } else {
+      int kt = 0;
+      for (; kt + 1 < nk; kt += 2) {
+        group(kt, 0, even, odd);
+        group(kt + 1, 0, odd, even);
       }
+      if (kt < nk) group(kt, 0, even, odd);
     }
   }
 #pragma unroll
@@ -321,11 +441,12 @@ __global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g,
       const int col = n0 + ncol + 16 * j + 4 * kq;
       if (col >= g.n) continue;
       if (g.part)
-        *reinterpret_cast<f32x4*>(g.part + ((int64_t)blockIdx.y * g.m + row) * g.n + col) = acc[i][j];
+        *reinterpret_cast<f32x4*>(g.part + ((int64_t)slice * g.m + row) * g.n + col) = acc[i][j];
       else
         store4(g, row, col, acc[i][j]);
     }
   }
+  wait_counts<0>();   // the loads past the last K block still write to this workgroup's LDS
 }
 
 // out = the sum of the slices, in their order
@@ -344,9 +465,8 @@ __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g, int spli
 // Up to 16 MB rows of a: b is read once, straight into the fragments.  A workgroup has 16 columns; its eight
 // wavefronts take the K blocks in turn (U of each in flight) and their sums meet in LDS.
 constexpr int kRowWaves = 8;
-template <int MB, bool EXACT>
+template <int MB, int U, bool EXACT>
 __global__ void __launch_bounds__(kRowWaves * 64) matmul_rows_kernel(MatmulArgs g) {
-  constexpr int U = MB == 1 ? 8 : 4;
   __shared__ f32x4 sums[kRowWaves][MB][64];
   const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, kq = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -388,9 +508,10 @@ __global__ void __launch_bounds__(kRowWaves * 64) matmul_rows_kernel(MatmulArgs 
 #pragma unroll
       for (int i = 0; i < MB; ++i) {
         x.set(xf[u][i]);
-        const f32x4 p = contract(w, x);
+        f32x4 p[1];
+        contract(&w, x, p);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(p[v], f[u][i], acc[i][v]);
+        for (int v = 0; v < 4; ++v) acc[i][v] = fmaf(p[0][v], f[u][i], acc[i][v]);
       }
     }
   }
@@ -459,59 +580,117 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
 
 // ---- which kernel ----------------------------------------------------------------------------------------------
 
+// The tiles, and what one K block of one takes (us) with every CU at work, for bf16 and for fp32 outputs: measured over
+// 17 shapes from m = 40 to 8192, each with 1, 2, 4 and 7 slices.
+enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64, kTiles };
+struct TileCost {
+  int bm, bn, per_cu;   // workgroups of a CU at a time
+  float step, step_f32;
+};
+constexpr TileCost kCost[kTiles] = {{256, 256, 1, 1.85f, 3.72f},
+                                    {128, 256, 1, 1.10f, 2.15f},
+                                    {128, 128, 1, 0.65f, 1.42f},
+                                    {128, 128, 2, 1.27f, 2.00f},
+                                    {64, 128, 1, 0.47f, 0.91f}};
+
 struct Plan {
+  int rows;            // rows of a that the plan covers (from the first)
   int rows_mb;         // > 0: the few-rows kernel with so many blocks of 16 rows
-  int bm, bn;          // else the tile
+  Tile tile;           // else the tile
   int splits, kb_per_split;
+  float us;
 };
 
-Plan plan_of(const moe_matmul_shape& s) {
-  Plan p{0, 0, 0, 1, s.k / kBK};
-  if (s.form == MOE_FP8_FORWARD && s.m <= 32) {
-    p.rows_mb = s.m <= 16 ? 1 : 2;
-    return p;
-  }
-  const int64_t big = ceil_div(s.m, 256) * ceil_div(s.n, 256);
-  p.bm = p.bn = 256;
-  if (big < 200) p.bm = p.bn = 128;
-  if (s.m <= 64) p.bm = 64, p.bn = 128;
-  const int64_t tiles = ceil_div(s.m, p.bm) * ceil_div(s.n, p.bn);
+// The plan for `rows` rows in one kernel (and the join): rounds of tiles over the CUs, a chip that is not full being up
+// to 28% faster, 5 us for a launch and a tile's start and end, and for slices 3.5 us and their sums' way to memory and
+// back.  kb / slices is 2 at least.
+Plan plan_one(const moe_matmul_shape& s, int rows) {
   const int kb = s.k / kBK;
-  if (p.bm < 256) {   // the chip has 256 CUs: slices of at least four K blocks
-    const int want = (int)std::min<int64_t>(std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), kb / 4), 16);
-    if (want > 1) {
-      p.kb_per_split = (int)ceil_div(kb, want);
-      p.splits = (int)ceil_div(kb, p.kb_per_split);
+  Plan best{rows, 0, kT64, 1, kb, 0.0f};
+  if (s.form == MOE_FP8_FORWARD && (rows <= 16 || (rows <= 32 && s.k <= 2048))) {
+    // straight from memory (1 x 4096 x 7168: 7.3 us against 11.3 with the best tile; 17 x 1024 x 1024: 6.2 against 7.6)
+    best.rows_mb = rows <= 16 ? 1 : 2;
+    best.us = 5.0f + (float)s.n * s.k / 1e7f;
+    return best;
+  }
+  const bool f32 = s.out_dtype == MOE_DTYPE_F32;
+  for (int i = 0; i < kTiles; ++i) {
+    if (i == kT256 && s.form == MOE_FP8_WEIGHT_GRAD && !f32) continue;   // its two vectors of scales spill there
+    const TileCost& c = kCost[i];
+    const int64_t tiles = ceil_div(rows, c.bm) * ceil_div(s.n, c.bn);
+    for (int want = 1; want <= 16 && (want == 1 || want * 2 <= kb); ++want) {
+      const int per = (int)ceil_div(kb, want), splits = per > 0 ? (int)ceil_div(kb, per) : 1;
+      if (splits != want) continue;
+      const int64_t total = tiles * splits, at_once = 256 * c.per_cu;
+      const float fill = total < at_once ? (float)total / at_once : 1.0f;
+      float us = 5.0f + (float)ceil_div(total, at_once) * per * (f32 ? c.step_f32 : c.step) * (0.72f + 0.28f * fill);
+      if (splits > 1) us += 3.5f + (float)splits * rows * s.n * 8 / 8e6f;
+      if ((i == 0 && want == 1) || us < best.us || best.us == 0.0f)
+        best = Plan{rows, 0, (Tile)i, splits, per, us};
     }
   }
-  return p;
+  return best;
+}
+
+// One kernel for all rows, or one for whole tiles of them and one for the rest (4097 rows: one more row of tiles).
+int plan_of(const moe_matmul_shape& s, Plan (&plans)[2]) {
+  plans[0] = plan_one(s, s.m);
+  int n = 1;
+  for (int bm : {256, 128}) {
+    const int rest = s.m % bm;
+    if (rest == 0 || s.m < bm) continue;
+    const Plan whole = plan_one(s, s.m - rest), last = plan_one(s, rest);
+    if (whole.us + last.us < (n == 1 ? plans[0].us : plans[0].us + plans[1].us)) {
+      plans[0] = whole;
+      plans[1] = last;
+      n = 2;
+    }
+  }
+  return n;
 }
 
 template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES>
 hipError_t launch_tile(const MatmulArgs& g, int splits, hipStream_t st) {
-  using S = TileShape<BM, BN, WM, WN, STAGES>;
+  using S = TileShape<FORM, BM, BN, WM, WN, STAGES>;
   static_assert(S::kLds <= 163840, "LDS");
   auto kern = &matmul_tile_kernel<FORM, EXACT, BM, BN, WM, WN, STAGES>;
   const hipError_t err = ensure_dynamic_lds(reinterpret_cast<const void*>(kern), S::kLds);
   if (err != hipSuccess) return err;
   const int64_t MT = ceil_div(g.m, BM), NT = ceil_div(g.n, BN);
-  const int64_t grid = ceil_div(MT * NT, kXcds * 32) * (kXcds * 32);
-  if (MT * NT >= (int64_t(1) << 31) - 256) return hipErrorInvalidValue;
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid, (unsigned)splits), dim3(S::kThreads), S::kLds, st, g, (int)MT, (int)NT);
+  const int64_t total = MT * NT * splits;
+  if (total >= (int64_t(1) << 31) - 256) return hipErrorInvalidValue;
+  // an XCD's 32 CUs take neighbouring tiles; fewer at a time where there are not enough for every XCD
+  const int chunk = (int)std::min<int64_t>(32, ceil_div(total, kXcds));
+  const int64_t grid = ceil_div(total, kXcds * chunk) * (kXcds * chunk);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, st, g, (int)MT, (int)NT, splits, chunk);
+  return hipGetLastError();
+}
+
+template <int MB, bool EXACT>
+hipError_t launch_rows(const MatmulArgs& g, hipStream_t st) {
+  const dim3 grid((unsigned)(g.n / 16)), block(kRowWaves * 64);
+  const int each = (int)ceil_div(g.k / kBK, kRowWaves);   // K blocks of a wavefront: all in flight at once if they fit
+  if (each > 4 && MB == 1) hipLaunchKernelGGL((matmul_rows_kernel<MB, 8, EXACT>), grid, block, 0, st, g);
+  else if (each > 2) hipLaunchKernelGGL((matmul_rows_kernel<MB, 4, EXACT>), grid, block, 0, st, g);
+  else hipLaunchKernelGGL((matmul_rows_kernel<MB, 2, EXACT>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
 template <int FORM, bool EXACT>
 hipError_t launch_form(const MatmulArgs& g, const Plan& p, hipStream_t st) {
-  if (p.rows_mb) {
-    const dim3 grid((unsigned)(g.n / 16)), block(kRowWaves * 64);
-    if (p.rows_mb == 1) hipLaunchKernelGGL((matmul_rows_kernel<1, EXACT>), grid, block, 0, st, g);
-    else hipLaunchKernelGGL((matmul_rows_kernel<2, EXACT>), grid, block, 0, st, g);
-    return hipGetLastError();
+  if constexpr (FORM == MOE_FP8_FORWARD) {
+    if (p.rows_mb == 1) return launch_rows<1, EXACT>(g, st);
+    if (p.rows_mb == 2) return launch_rows<2, EXACT>(g, st);
   }
-  if (p.bm == 256) return launch_tile<FORM, EXACT, 256, 256, 2, 4, 2>(g, p.splits, st);
-  if (p.bm == 128) return launch_tile<FORM, EXACT, 128, 128, 2, 2, 4>(g, p.splits, st);
-  return launch_tile<FORM, EXACT, 64, 128, 2, 2, 4>(g, p.splits, st);
+  switch (p.tile) {
+    case kT256:
+      if constexpr (FORM != MOE_FP8_WEIGHT_GRAD || EXACT) return launch_tile<FORM, EXACT, 256, 256, 2, 4, 2>(g, p.splits, st);
+      return hipErrorInvalidValue;   // never planned
+    case kT128x256: return launch_tile<FORM, EXACT, 128, 256, 2, 4, 3>(g, p.splits, st);
+    case kT128: return launch_tile<FORM, EXACT, 128, 128, 2, 4, 4>(g, p.splits, st);
+    case kT128Pair: return launch_tile<FORM, EXACT, 128, 128, 2, 2, 2>(g, p.splits, st);
+    default: return launch_tile<FORM, EXACT, 64, 128, 2, 2, 4>(g, p.splits, st);
+  }
 }
 
 template <int FORM>
@@ -519,29 +698,47 @@ hipError_t launch_product(const MatmulArgs& g, const Plan& p, hipStream_t st) {
   return g.out_f32 ? launch_form<FORM, true>(g, p, st) : launch_form<FORM, false>(g, p, st);
 }
 
+size_t sums_bytes(const moe_matmul_shape& s, const Plan& p) {
+  return p.splits > 1 ? (size_t)p.splits * p.rows * s.n * 4 : 0;
+}
+
 }  // namespace
 
 size_t matmul_fp8_workspace(const moe_matmul_shape& s) {
   if (s.m == 0 || s.n == 0 || s.k == 0) return 0;
-  const Plan p = plan_of(s);
-  return p.splits > 1 ? (size_t)p.splits * s.m * s.n * 4 : 0;
+  Plan plans[2];
+  const int n = plan_of(s, plans);
+  // (the second kernel's sums may take the first one's place: they run in order)
+  return std::max(sums_bytes(s, plans[0]), n > 1 ? sums_bytes(s, plans[1]) : 0);
 }
 
 hipError_t launch_matmul_fp8(const moe_matmul_shape& s, const uint8_t* a, const float* a_scale, const uint8_t* b,
                              const float* b_scale, void* out, float* ws, hipStream_t st) {
   if (s.m == 0 || s.n == 0) return hipSuccess;
-  const Plan p = plan_of(s);
-  MatmulArgs g{a, a_scale, b, b_scale, out, p.splits > 1 ? ws : nullptr, s.lda ? s.lda : s.k,
-               s.ldb ? s.ldb : (s.form == MOE_FP8_INPUT_GRAD ? s.n : s.k), s.ldo ? s.ldo : s.n, s.m, s.n, s.k,
-               (int)ceil_div(s.n, kBK), p.kb_per_split, s.out_dtype == MOE_DTYPE_F32, s.accumulate != 0};
-  hipError_t err = s.form == MOE_FP8_FORWARD ? launch_product<MOE_FP8_FORWARD>(g, p, st)
-                   : s.form == MOE_FP8_INPUT_GRAD ? launch_product<MOE_FP8_INPUT_GRAD>(g, p, st)
-                                                  : launch_product<MOE_FP8_WEIGHT_GRAD>(g, p, st);
-  if (err != hipSuccess || p.splits == 1) return err;
-  const int64_t quads = (int64_t)s.m * s.n / 4;
-  hipLaunchKernelGGL(matmul_join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(quads, 256), 4096)), dim3(256), 0, st, g,
-                     p.splits);
-  return hipGetLastError();
+  Plan plans[2];
+  const int n = plan_of(s, plans);
+  const int64_t lda = s.lda ? s.lda : s.k, ldo = s.ldo ? s.ldo : s.n;
+  const bool f32 = s.out_dtype == MOE_DTYPE_F32;
+  int64_t row = 0;
+  for (int i = 0; i < n; ++i) {
+    const Plan& p = plans[i];
+    const MatmulArgs g{a + row * lda, a_scale + row * (s.k / kBK), b, b_scale,
+                       static_cast<char*>(out) + row * ldo * (f32 ? 4 : 2), p.splits > 1 ? ws : nullptr, lda,
+                       s.ldb ? s.ldb : (s.form == MOE_FP8_INPUT_GRAD ? s.n : s.k), ldo, p.rows, s.n, s.k,
+                       (int)ceil_div(s.n, kBK), p.kb_per_split, f32, s.accumulate != 0};
+    hipError_t err = s.form == MOE_FP8_FORWARD      ? launch_product<MOE_FP8_FORWARD>(g, p, st)
+                     : s.form == MOE_FP8_INPUT_GRAD ? launch_product<MOE_FP8_INPUT_GRAD>(g, p, st)
+                                                    : launch_product<MOE_FP8_WEIGHT_GRAD>(g, p, st);
+    if (err == hipSuccess && p.splits > 1) {
+      const int64_t quads = (int64_t)p.rows * s.n / 4;
+      hipLaunchKernelGGL(matmul_join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(quads, 256), 4096)), dim3(256), 0, st,
+                         g, p.splits);
+      err = hipGetLastError();
+    }
+    if (err != hipSuccess) return err;
+    row += p.rows;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_quantize_act_t(int rows, int cols, const void* x, uint8_t* codes, float* scales, hipStream_t st) {
