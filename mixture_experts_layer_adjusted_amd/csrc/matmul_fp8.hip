@@ -530,28 +530,38 @@ __global__ void __launch_bounds__(kRowWaves * 64) matmul_rows_kernel(MatmulArgs 
 
 // ---- the transposing quantiser -------------------------------------------------------------------------------
 //
-// codes[c, r] of x[r, c] (bf16), one scale per column and run of 128 rows: amax times fp32(1 / 448), 1 for a run of zeros; rows
-// past the last are zeros.  A 128-row x 64-column block goes through LDS in fp32: a thread loads 32 columns of one
-// row, then four neighbouring threads take one column's rows, 32 each.
+// codes[c, r] of x[r, c] (bf16), one scale per column and run of 128 rows: amax times fp32(1 / 448), 1 for a run of
+// zeros; rows past the last are zeros.  A 128-row x 64-column block goes through LDS as words of two rows: eight lanes
+// load 16 bytes each of a row pair (128 bytes of both rows), and four lanes then take one column's rows, 32 each; the
+// pitch of 65 words keeps either side on distinct banks.  The quotients are rounded without a division each: with r
+// the rounded 1 / scale and q = v r, the remainder v - q scale is exact in one fma and q + remainder r is the rounded
+// quotient (Markstein); scales outside 2^-64..2^64, where it could underflow or overflow, divide.
 __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __restrict__ x, int rows, int cols,
                                                           uint8_t* __restrict__ codes, float* __restrict__ scales) {
-  __shared__ float tile[64][129];
+  __shared__ uint32_t tile[64][65];
   const int64_t r0 = (int64_t)blockIdx.x * 128;
   const int c0 = blockIdx.y * 64, tid = threadIdx.x;
   const int64_t runs = gridDim.x;
   {
-    const int rl = tid >> 1, h = (tid & 1) * 32;
-    const int64_t r = r0 + rl;
+    const int cl = (tid & 7) * 8, c = c0 + cl;
+    uint4 w[2][2];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int c = c0 + h + 8 * q;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows && c < cols) w = *reinterpret_cast<const uint4*>(x + r * cols + c);   // (cols: a multiple of 8)
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int64_t r = r0 + 2 * ((tid >> 3) + 32 * h) + e;
+        w[h][e] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < rows && c < cols) w[h][e] = *reinterpret_cast<const uint4*>(x + r * cols + c);   // (cols: a multiple of 8)
+      }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t lo[4] = {w[h][0].x, w[h][0].y, w[h][0].z, w[h][0].w};
+      const uint32_t hi[4] = {w[h][1].x, w[h][1].y, w[h][1].z, w[h][1].w};
+      const int p = (tid >> 3) + 32 * h;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        tile[h + 8 * q + 2 * i][rl] = __uint_as_float(v[i] << 16);
-        tile[h + 8 * q + 2 * i + 1][rl] = __uint_as_float(v[i] & 0xFFFF0000u);
+        tile[cl + 2 * i][p] = (lo[i] & 0xFFFFu) | (hi[i] << 16);
+        tile[cl + 2 * i + 1][p] = (lo[i] >> 16) | (hi[i] & 0xFFFF0000u);
       }
     }
   }
@@ -559,19 +569,30 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
   const int c = tid >> 2, q = tid & 3;
   float v[32], amax = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = tile[c][32 * q + i];
-    amax = fmaxf(amax, fabsf(v[i]));
+  for (int i = 0; i < 16; ++i) {
+    const uint32_t w = tile[c][16 * q + i];
+    v[2 * i] = __uint_as_float(w << 16);
+    v[2 * i + 1] = __uint_as_float(w & 0xFFFF0000u);
+    amax = fmaxf(amax, fmaxf(fabsf(v[2 * i]), fabsf(v[2 * i + 1])));
   }
   amax = fmaxf(amax, __shfl_xor(amax, 1, 64));
   amax = fmaxf(amax, __shfl_xor(amax, 2, 64));
   if (c0 + c >= cols) return;
   const float scale = amax > 0.0f ? amax * (1.0f / 448.0f) : 1.0f;
+  const float inv = __fdiv_rn(1.0f, scale);
+  if (scale >= 0x1p-64f && scale < 0x1p64f) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      const float s = v[i] * inv;
+      v[i] = fmaf(fmaf(-s, scale, v[i]), inv, s);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __fdiv_rn(v[i], scale);
+  }
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    w[i] = e4m3x4_from_f32(__fdiv_rn(v[4 * i], scale), __fdiv_rn(v[4 * i + 1], scale), __fdiv_rn(v[4 * i + 2], scale),
-                           __fdiv_rn(v[4 * i + 3], scale));
+  for (int i = 0; i < 8; ++i) w[i] = e4m3x4_from_f32(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
   uint8_t* p = codes + (int64_t)(c0 + c) * runs * 128 + r0 + 32 * q;
   *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
   *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);

@@ -59,16 +59,21 @@ __device__ __forceinline__ float run_scale(const float (&v)[8]) {
 // (Markstein).  Scales below 2^-64, where the remainder could underflow, divide (and a subnormal scale is so coarse
 // that its quotients can pass 127).
 __device__ __forceinline__ uint2 code8(const float (&v)[8], float scale) {
-  const float r = __fdiv_rn(1.0f, scale);
-  const bool tiny = scale < 0x1p-64f;
+  float q[8];
+  if (scale >= 0x1p-64f) {
+    const float r = __fdiv_rn(1.0f, scale);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      q[i] = v[i] * r;
+      q[i] = fmaf(fmaf(-q[i], scale, v[i]), r, q[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = fminf(fmaxf(__fdiv_rn(v[i], scale), -127.0f), 127.0f);
+  }
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float q = v[i] * r;
-    q = fmaf(fmaf(-q, scale, v[i]), r, q);
-    if (tiny) q = fminf(fmaxf(__fdiv_rn(v[i], scale), -127.0f), 127.0f);
-    w[i / 4] |= ((uint32_t)(int)rintf(q) & 0xFFu) << (8 * (i % 4));
-  }
+  for (int i = 0; i < 8; ++i) w[i / 4] |= ((uint32_t)(int)rintf(q[i]) & 0xFFu) << (8 * (i % 4));
   return scale != scale ? make_uint2(0u, 0u) : make_uint2(w[0], w[1]);
 }
 
