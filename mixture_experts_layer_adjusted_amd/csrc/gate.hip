@@ -12,9 +12,10 @@
 //   softmax  plain          dl_i = scale p_i (dg_i [i picked] - sum_j dg_j p_j), every i
 // and zero elsewhere.
 //
-// Lanes hold neighbouring experts: lane i of a token has the experts CPL i .. CPL i + CPL - 1 (one vector load), in
-// lists of four sorted by key, so that a round of the selection is the largest head over the lanes and one pop, and
-// equal keys leave in index order (lowest lane first, the sort being stable).
+// L lanes hold a token, CPL neighbouring experts each (one load of up to 64 bytes), in lists of four sorted by key: a
+// round of the selection is the largest head over the lanes and one pop, and equal keys leave in index order (lowest
+// lane, lowest list, stable sort).  What bounds it is instructions, not bytes (a 64-lane round costs 30 for one token, a
+// 16-lane one 60 for four): T=16384, 256 experts in 8 groups: 18.1 us with 64 lanes, 10.7 with 16; one token 4.4 and 6.0 us.
 #include "moe_internal.h"
 
 namespace moe {
@@ -45,6 +46,8 @@ __device__ __forceinline__ float exp_of(float x) {
   const float e = __builtin_amdgcn_exp2f(y);
   return fabsf(x) < 150.0f ? fmaf(e, r * 0.693147182f, e) : e;   // (e may be infinite, and r NaN)
 }
+
+__device__ __forceinline__ float sigmoid_of(float l) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-l)); }
 
 // CPL neighbouring logits (rows start anywhere: the loads need no more than the element's alignment)
 template <int CPL>
@@ -101,6 +104,11 @@ template <int CTRL, int ROW_MASK>
 __device__ __forceinline__ uint32_t moved(uint32_t other, uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROW_MASK, 0xF, false);
 }
+// v from the lane that the DPP control names, where every lane has one (rotations, permutations)
+template <int CTRL>
+__device__ __forceinline__ uint32_t turned(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
 
 // A reduction over the L lanes of a token, the result in each of them.  L = 16: four rotations of the 16-lane row
 // (row_ror:8, 4, 2, 1).  L = 32: then the other row by a shuffle.  L = 64: row shifts by 1, 2, 4, 8, row 0's and 2's
@@ -117,10 +125,10 @@ __device__ __forceinline__ uint32_t reduce(uint32_t v, uint32_t neutral, Op op) 
     v = op(v, moved<0x143, 0xC>(neutral, v));
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
   } else {
-    v = op(v, moved<0x128, 0xF>(v, v));
-    v = op(v, moved<0x124, 0xF>(v, v));
-    v = op(v, moved<0x122, 0xF>(v, v));
-    v = op(v, moved<0x121, 0xF>(v, v));
+    v = op(v, turned<0x128>(v));
+    v = op(v, turned<0x124>(v));
+    v = op(v, turned<0x122>(v));
+    v = op(v, turned<0x121>(v));
     if constexpr (L == 32) v = op(v, (uint32_t)__shfl_xor((int)v, 16, 64));
     return v;
   }
@@ -187,98 +195,157 @@ __device__ __forceinline__ uint64_t open_groups(const uint32_t* keys, const Gate
   return open;
 }
 
-// L lanes a token: 64, or 16 where a token's experts are few (four tokens a wavefront).
+// Whether the lane's group stays open, groups being `per` whole lanes: the lanes' two largest join over the group, and
+// the group's rank counts the groups above it, or equal to it and before it.  Scores as in open_groups.
+template <int L>
+__device__ __forceinline__ bool group_open(uint32_t k1, uint32_t k2, const GateArgs& a, int lane, int per) {
+  auto join = [&](uint32_t o1, uint32_t o2) {
+    k2 = max(max(k2, o2), min(k1, o1));
+    k1 = max(k1, o1);
+  };
+  if (per >= 2) join(turned<0xB1>(k1), turned<0xB1>(k2));       // quad_perm: lanes 1 0 3 2
+  if (per >= 4) join(turned<0x4E>(k1), turned<0x4E>(k2));       // lanes 2 3 0 1
+  if (per >= 8) join(turned<0x141>(k1), turned<0x141>(k2));     // row_half_mirror
+  if (per >= 16) join(turned<0x140>(k1), turned<0x140>(k2));    // row_mirror
+  if (L >= 32 && per >= 32) join(__shfl_xor(k1, 16, 64), __shfl_xor(k2, 16, 64));
+  if (L >= 64 && per >= 64) join(__shfl_xor(k1, 32, 64), __shfl_xor(k2, 32, 64));
+  uint32_t score = k1;
+  if (a.top2 && k2 > kNanKey) score = key_of(score_of(k1) + score_of(k2));
+  const int g = lane / per;
+  int rank = 0;
+  for (int h = 0; h < a.G; ++h) {
+    const uint32_t o = (uint32_t)__shfl((int)score, h * per, L);
+    rank += (o > score || (o == score && h < g)) ? 1 : 0;
+  }
+  return rank < a.TG;
+}
+
+// `per`: lanes of a group where groups are whole lanes (0: they are not; 64 lanes only)
 template <int CPL, int L, typename TL, bool SOFTMAX>
-__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int lanes_log2) {
+__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int lanes_log2) {
   constexpr int kTokens = 64 / L;                    // tokens of a wavefront
   constexpr int kLists = (CPL + 3) / 4, kLen = CPL < 4 ? CPL : 4;
   __shared__ int32_t hist[kMaxRouted];
   __shared__ uint32_t keys[L == 64 ? kWaves : 1][kMaxRouted];
-  __shared__ int2 won[kWaves][kTokens][kMaxTopK];    // the picks: expert, and its score (softmax renormalised: logit)
+  __shared__ int32_t won[kWaves][kTokens][kMaxTopK];
   const int tid = threadIdx.x, wl = tid & 63, lane = wl & (L - 1), slot = wl / L;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = a.N, K = a.K;
   for (int e = tid; e < N; e += kThreads) hist[e] = 0;
-  const bool limited = L == 64 && a.TG < a.G;
+  const bool limited = a.TG < a.G;
   const int first = lane * CPL, left = N - first;
-  float bias[CPL];
-  int group[CPL];
+  float bias[CPL];   // -inf past the last expert
+  if (a.bias) {
+    load_run<CPL>(a.bias + first, left, bias);
+  } else {
 #pragma unroll
-  for (int j = 0; j < CPL; ++j) {
-    bias[j] = j < left ? (a.bias ? a.bias[first + j] : 0.0f) : kNegInf;
-    group[j] = limited && j < left ? (first + j) / (N / a.G) : 0;
+    for (int j = 0; j < CPL; ++j) bias[j] = j < left ? 0.0f : kNegInf;
   }
-  // lanes before this one in its token's 16 (for the first of equals)
-  const uint32_t before = L == 64 ? 0u : ((1u << lane) - 1u) << (wl & 16);
+  // this lane's predecessors in its token, as bits of the ballot's half
+  const uint32_t before = L == 64 ? 0u : ((1u << lane) - 1u) << (wl & (32 - L));
   __syncthreads();
   const int64_t per_block = (int64_t)kWaves * kTokens;
   for (int64_t t0 = (int64_t)blockIdx.x * per_block + wave * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * per_block) {
-    const int64_t t = t0 + slot;
-    const bool real = t < a.T;   // (16 lanes a token: the last wavefront may have fewer than four)
-    float l[CPL], s[CPL];
-    load_run<CPL>(static_cast<const TL*>(a.logits) + (real ? t : t0) * a.ld + first, left, l);
-    if constexpr (SOFTMAX) {
-      float top = l[0];
-#pragma unroll
-      for (int j = 1; j < CPL; ++j) top = fmaxf(top, l[j]);
-      top = max_of<L>(top);
-      if (top == kNegInf) top = 0.0f;
-      float sum = 0.0f;
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) {
-        s[j] = exp_of(l[j] - top);
-        sum += s[j];
-      }
-      sum = sum_of<L>(sum);
-      const float r = sum == 0.0f ? 0.0f : 1.0f / sum;   // 0: every expert masked
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) s[j] *= r;
-    } else {
-#pragma unroll
-      for (int j = 0; j < CPL; ++j) s[j] = __builtin_amdgcn_rcpf(1.0f + exp_of(-l[j]));
-    }
+    const bool real = t0 + slot < a.T;   // (several tokens a wavefront: the last one may have fewer)
+    const int64_t t = real ? t0 + slot : t0;
+    const TL* row = static_cast<const TL*>(a.logits) + t * a.ld;
     uint32_t key[kLists][4];
-    uint32_t order[kLists];       // which expert of the lane each entry is, a byte each
+    uint32_t order[kLists];              // which expert of the lane each entry is, a byte each
+    float total = 0.0f, top = 0.0f;      // softmax: the row's sum and maximum
+    float l[CPL];
+    load_run<CPL>(row + first, left, l);
+    {
+      float s[CPL];
+      if constexpr (SOFTMAX) {
+        top = l[0];
 #pragma unroll
-    for (int q = 0; q < kLists; ++q) {
-      order[q] = 0;
+        for (int j = 1; j < CPL; ++j) top = fmaxf(top, l[j]);
+        top = max_of<L>(top);
+        if (top == kNegInf) top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = 4 * q + j;
-        key[q][j] = j < kLen && !(l[i] == kNegInf || bias[i] == kNegInf) ? key_of(s[i] + bias[i]) : kOut;
+        for (int j = 0; j < CPL; ++j) {
+          s[j] = exp_of(l[j] - top);
+          total += s[j];
+        }
+        total = sum_of<L>(total);
+        total = total == 0.0f ? 0.0f : 1.0f / total;   // 0: every expert masked
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) s[j] *= total;
+      } else {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) s[j] = sigmoid_of(l[j]);
+      }
+#pragma unroll
+      for (int q = 0; q < kLists; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (j >= kLen) {
+            key[q][j] = kOut;
+            continue;
+          }
+          const int i = 4 * q + j;
+          float c = s[i] + bias[i];
+          c = l[i] == kNegInf ? kNegInf : c;   // (scores are finite: a bias of -inf leaves -inf too)
+          const uint32_t k = key_of(c);
+          key[q][j] = c == kNegInf ? kOut : k;
+        }
+    }
+    if (limited && per == 0) {
+      if constexpr (L == 64) {
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+          if (j < left) keys[wave][first + j] = key[j / 4][j % 4];
+        __builtin_amdgcn_wave_barrier();   // LDS operations of one wavefront take effect in program order
+        const uint64_t open = open_groups(keys[wave], a, lane, lanes_log2);
+        __builtin_amdgcn_wave_barrier();
+        const float inv = (float)a.G / (float)N;   // (small integers: half a step in, the quotient is exact enough)
+#pragma unroll
+        for (int j = 0; j < CPL; ++j)
+          if (!((open >> (int)(((float)(first + j) + 0.5f) * inv)) & 1ull)) key[j / 4][j % 4] = kOut;
       }
     }
-    if (limited) {
-#pragma unroll
-      for (int j = 0; j < CPL; ++j)
-        if (j < left) keys[wave][first + j] = key[j / 4][j % 4];
-      __builtin_amdgcn_wave_barrier();   // LDS operations of one wavefront take effect in program order
-      const uint64_t open = open_groups(keys[wave], a, lane, lanes_log2);
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int j = 0; j < CPL; ++j)
-        if (!((open >> group[j]) & 1ull)) key[j / 4][j % 4] = kOut;
-    }
-    // each list in descending order, equal keys as they stand (neighbours change places only if the later is larger)
+    // each list in descending order, equal keys as they stand: an entry's place is the number of larger ones, and of
+    // equal ones before it
 #pragma unroll
     for (int q = 0; q < kLists; ++q) {
-      uint32_t at[4] = {4u * q, 4u * q + 1u, 4u * q + 2u, 4u * q + 3u};
-#pragma unroll
-      for (int end = kLen - 1; end > 0; --end)
-#pragma unroll
-        for (int j = 0; j < end; ++j) {
-          const bool swap = key[q][j + 1] > key[q][j];
-          const uint32_t hi = max(key[q][j], key[q][j + 1]), lo = min(key[q][j], key[q][j + 1]);
-          const uint32_t x = swap ? at[j + 1] : at[j], y = swap ? at[j] : at[j + 1];
-          key[q][j] = hi, key[q][j + 1] = lo, at[j] = x, at[j + 1] = y;
-        }
-      order[q] = at[0] | (at[1] << 8) | (at[2] << 16) | (at[3] << 24);
+      uint32_t(&k)[4] = key[q];
+      if constexpr (kLen == 4) {
+        const uint32_t c01 = k[1] > k[0] ? 8 : 0, c02 = k[2] > k[0] ? 8 : 0, c03 = k[3] > k[0] ? 8 : 0;
+        const uint32_t c12 = k[2] > k[1] ? 8 : 0, c13 = k[3] > k[1] ? 8 : 0, c23 = k[3] > k[2] ? 8 : 0;
+        order[q] = (1u << (8 - c01 + c12 + c13)) + (2u << (16 - c02 - c12 + c23)) + (3u << (24 - c03 - c13 - c23)) +
+                   4u * q * 0x01010101u;
+        const uint32_t hi0 = max(k[0], k[1]), lo0 = min(k[0], k[1]), hi1 = max(k[2], k[3]), lo1 = min(k[2], k[3]);
+        k[0] = max(hi0, hi1), k[3] = min(lo0, lo1);
+        const uint32_t x = min(hi0, hi1), y = max(lo0, lo1);
+        k[1] = max(x, y), k[2] = min(x, y);
+      } else if constexpr (kLen == 2) {
+        order[q] = k[1] > k[0] ? 0x0001u : 0x0100u;
+        const uint32_t hi = max(k[0], k[1]);
+        k[1] = min(k[0], k[1]), k[0] = hi;
+      } else {
+        order[q] = 0;
+      }
     }
-    for (int k = lane; k < K; k += L) won[wave][slot][k] = make_int2(-1, __float_as_int(kNegInf));
+    if (limited && per > 0) {
+      uint32_t k1 = kOut, k2 = kOut;
+#pragma unroll
+      for (int q = 0; q < kLists; ++q) {
+        k2 = max(max(k2, kLen > 1 ? key[q][1] : kOut), min(k1, key[q][0]));
+        k1 = max(k1, key[q][0]);
+      }
+      if (!group_open<L>(k1, k2, a, lane, per)) {
+#pragma unroll
+        for (int q = 0; q < kLists; ++q)
+#pragma unroll
+          for (int j = 0; j < kLen; ++j) key[q][j] = kOut;
+      }
+    }
+    for (int k = lane; k < K; k += L) won[wave][slot][k] = -1;
     __builtin_amdgcn_wave_barrier();
     for (int k = 0; k < K; ++k) {
       uint32_t head = key[0][0];
-      if constexpr (kLists > 1) head = max(head, key[1][0]);
+#pragma unroll
+      for (int q = 1; q < kLists; ++q) head = max(head, key[q][0]);
       const uint32_t best = max_of<L>(head);
       if (L == 64 ? best == kOut : __ballot(best != kOut) == 0) break;
       const uint64_t at = __ballot(head == best && best != kOut);
@@ -289,50 +356,54 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int lanes_lo
         const uint32_t half = wl < 32 ? (uint32_t)at : (uint32_t)(at >> 32);
         mine = head == best && best != kOut && (half & before) == 0;
       }
-      if (mine) {
-        const int q = kLists == 1 || key[0][0] == best ? 0 : 1;   // the first list's expert comes first
-        uint32_t j = order[0] & 0xFFu;
-        if (kLists > 1 && q == 1) j = order[kLists - 1] & 0xFFu;
-        float v = (SOFTMAX && a.renorm) ? l[0] : s[0];
+      if (mine) {   // the first list whose head it is
+        bool found = false;
+        uint32_t j = 0;
 #pragma unroll
-        for (int i = 1; i < CPL; ++i)
-          if (j == (uint32_t)i) v = (SOFTMAX && a.renorm) ? l[i] : s[i];
-        // (a softmax over a NaN has no number: the score says so where the logit may not)
-        if (SOFTMAX && a.renorm && best == kNanKey) v = __builtin_nanf("");
-        won[wave][slot][k] = make_int2(first + (int)j, __float_as_int(v));
+        for (int q = 0; q < kLists; ++q) {
+          const bool here = !found && key[q][0] == best;
+          found = found || here;
+          j = here ? order[q] & 0xFFu : j;
+          order[q] = here ? order[q] >> 8 : order[q];
 #pragma unroll
-        for (int p = 0; p < kLists; ++p)
-          if (p == q) {
-#pragma unroll
-            for (int i = 0; i + 1 < kLen; ++i) key[p][i] = key[p][i + 1];
-            key[p][kLen - 1] = kOut;
-            order[p] >>= 8;
-          }
+          for (int i = 0; i < kLen; ++i) key[q][i] = here ? (i + 1 < kLen ? key[q][i + 1] : kOut) : key[q][i];
+        }
+        won[wave][slot][k] = first + (int)j;
       }
     }
     __builtin_amdgcn_wave_barrier();
+    // the picks' gates, from their logits again
     constexpr int kHalves = L == 16 ? 2 : 1;   // 16 lanes hold up to 32 picks
     float g[kHalves], v[kHalves];
     int e[kHalves];
+    float most = kNegInf;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      e[h] = -1, v[h] = kNegInf;
-      if (lane + L * h < K) {
-        const int2 w = won[wave][slot][lane + L * h];
-        e[h] = w.x, v[h] = __int_as_float(w.y);
-      }
-    }
-    float top = 0.0f;
-    if (SOFTMAX && a.renorm) {   // from the picked logits, so that no picked score has underflowed
-      top = v[0];
+      e[h] = lane + L * h < K ? won[wave][slot][lane + L * h] : -1;
+      v[h] = kNegInf;
+      if constexpr (CPL <= 4) {   // from the lane that has it
 #pragma unroll
-      for (int h = 1; h < kHalves; ++h) top = fmaxf(top, v[h]);
-      top = max_of<L>(top);
+        for (int j = 0; j < CPL; ++j) {
+          const float o = __shfl(l[j], max(e[h], 0) / CPL, L);
+          if (e[h] >= 0 && e[h] % CPL == j) v[h] = o;
+        }
+      } else {
+        if (e[h] >= 0) load_run<1>(row + e[h], 1, reinterpret_cast<float(&)[1]>(v[h]));
+      }
+      most = fmaxf(most, v[h]);
     }
     float sum = 0.0f;
+    if (SOFTMAX && a.renorm) {   // over the picks alone, so that no picked score has underflowed
+      most = max_of<L>(most);
+      if (most == kNegInf) most = 0.0f;
+    }
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      g[h] = e[h] < 0 ? 0.0f : SOFTMAX && a.renorm ? exp_of(v[h] - top) : v[h];
+      if constexpr (SOFTMAX)   // (total is NaN where a NaN or an infinity leaves the row without a number)
+        g[h] = a.renorm ? (total != total ? total : exp_of(v[h] - most)) : exp_of(v[h] - top) * total;
+      else
+        g[h] = sigmoid_of(v[h]);
+      if (e[h] < 0) g[h] = 0.0f;
       sum += g[h];
     }
     if (a.renorm) {
@@ -495,25 +566,44 @@ __global__ void __launch_bounds__(kBwdThreads) gate_bwd_kernel(GateBwdArgs a) {
   }
 }
 
-// 16 lanes a token where they hold its experts (no group limit: that one wants the wavefront)
-bool narrow(const moe_gate_config& c) { return c.n_routed <= 64 && c.topk_groups >= c.n_groups; }
+// How a call's tokens lie on lanes: 16 lanes a token (32 above 256 experts), or 64 for groups that do not fall on a power
+// of two of whole lanes.  Not by the number of tokens: a token's sums, and so its gates, are the same in every batch.
+struct GateLanes {
+  int lanes, cpl;
+  int per;   // lanes of a group, 0 where groups are not whole lanes
+};
+GateLanes lanes_of(const moe_gate_config& c) {
+  auto with = [&](int lanes) {
+    GateLanes g{lanes, 1, 0};
+    while (g.cpl * lanes < c.n_routed) g.cpl *= 2;
+    const int gs = c.n_routed / c.n_groups;
+    const int per = gs % g.cpl == 0 ? gs / g.cpl : 0;
+    if (per > 0 && (per & (per - 1)) == 0) g.per = per;
+    return g;
+  };
+  const GateLanes few = with(c.n_routed <= 256 ? 16 : 32);
+  const bool limited = c.topk_groups < c.n_groups;
+  return !limited || few.per > 0 ? few : with(64);
+}
 
 template <typename TL, bool SOFTMAX>
-hipError_t gate_forward_t(const GateArgs& a, bool few, int lanes_log2, unsigned grid, hipStream_t st) {
-#define MOE_GATE_CASE(C, L) \
-  hipLaunchKernelGGL((gate_kernel<C, L, TL, SOFTMAX>), dim3(grid), dim3(kThreads), 0, st, a, lanes_log2)
-  if (few) {
-    if (a.N <= 16) MOE_GATE_CASE(1, 16);
-    else if (a.N <= 32) MOE_GATE_CASE(2, 16);
-    else MOE_GATE_CASE(4, 16);
-  } else if (a.N <= 64) {
+hipError_t gate_forward_t(const GateArgs& a, const GateLanes& g, int lanes_log2, unsigned grid, hipStream_t st) {
+#define MOE_GATE_CASE(C, L)                                                                                            \
+  case L * 100 + C:                                                                                                    \
+    hipLaunchKernelGGL((gate_kernel<C, L, TL, SOFTMAX>), dim3(grid), dim3(kThreads), 0, st, a, g.per, lanes_log2);      \
+    break
+  switch (g.lanes * 100 + g.cpl) {
+    MOE_GATE_CASE(1, 16);
+    MOE_GATE_CASE(2, 16);
+    MOE_GATE_CASE(4, 16);
+    MOE_GATE_CASE(8, 16);
+    MOE_GATE_CASE(16, 16);
+    MOE_GATE_CASE(16, 32);
     MOE_GATE_CASE(1, 64);
-  } else if (a.N <= 128) {
     MOE_GATE_CASE(2, 64);
-  } else if (a.N <= 256) {
     MOE_GATE_CASE(4, 64);
-  } else {
     MOE_GATE_CASE(8, 64);
+    default: return hipErrorInvalidValue;
   }
 #undef MOE_GATE_CASE
   return hipGetLastError();
@@ -549,7 +639,7 @@ hipError_t gate_backward_l(const GateBwdArgs& a, bool softmax, hipStream_t st) {
 }  // namespace
 
 int64_t gate_blocks(const moe_gate_config& c) {
-  return std::min<int64_t>(ceil_div(c.tokens, narrow(c) ? 4 * kWaves : kWaves), 512);
+  return std::min<int64_t>(ceil_div(c.tokens, kWaves * (64 / lanes_of(c).lanes)), 512);
 }
 
 hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float* bias, int32_t* idx, float* gate,
@@ -565,14 +655,15 @@ hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float
                    load ? (grid == 1 ? load : counts) : nullptr};
   int lanes_log2 = 0;   // as many lanes per group as leave a set for every group
   while ((2 << lanes_log2) * c.n_groups <= 64) ++lanes_log2;
-  const bool f32 = c.logits_dtype == MOE_DTYPE_F32, few = narrow(c);
+  const bool f32 = c.logits_dtype == MOE_DTYPE_F32;
+  const GateLanes g = lanes_of(c);
   hipError_t err;
   if (c.score == MOE_SCORE_SOFTMAX)
-    err = f32 ? gate_forward_t<float, true>(a, few, lanes_log2, grid, st)
-              : gate_forward_t<uint16_t, true>(a, few, lanes_log2, grid, st);
+    err = f32 ? gate_forward_t<float, true>(a, g, lanes_log2, grid, st)
+              : gate_forward_t<uint16_t, true>(a, g, lanes_log2, grid, st);
   else
-    err = f32 ? gate_forward_t<float, false>(a, few, lanes_log2, grid, st)
-              : gate_forward_t<uint16_t, false>(a, few, lanes_log2, grid, st);
+    err = f32 ? gate_forward_t<float, false>(a, g, lanes_log2, grid, st)
+              : gate_forward_t<uint16_t, false>(a, g, lanes_log2, grid, st);
   if (err != hipSuccess || !load || grid == 1) return err;
   hipLaunchKernelGGL(gate_load_kernel, dim3((unsigned)ceil_div(c.n_routed, 64)), dim3(kThreads), 0, st, counts, (int)grid,
                      c.n_routed, load);
