@@ -93,7 +93,8 @@ __device__ __forceinline__ int src_chunk(int r, int s) { return kchunk(s ^ swz(r
 // 16-byte unit of the banks twice.
 template <int BN>
 __device__ __forceinline__ int kn_swz(int r) {
-  return BN == 256 ? (r & 7) | (((r >> 5) & 1) << 3) : ((r >> 1) & 3) | (((r >> 5) & 1) << 2);
+  const int quarter = (r >> 5) & 1;   // of the K quarters, neighbours apart
+  return BN == 256 ? (r & 7) | quarter << 3 : BN == 128 ? ((r >> 1) & 3) | quarter << 2 : ((r >> 2) & 1) | quarter << 1;
 }
 
 __device__ __forceinline__ i32x8 frag_at(const uint8_t* p0, const uint8_t* p1) {
@@ -454,6 +455,7 @@ __global__ void __launch_bounds__(256) matmul_join_kernel(MatmulArgs g, int spli
   const int64_t per = (int64_t)g.m * g.n, quads = per / 4;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < quads; i += (int64_t)gridDim.x * 256) {
     f32x4 v = *reinterpret_cast<const f32x4*>(g.part + 4 * i);
+#pragma unroll 8
     for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const f32x4*>(g.part + s * per + 4 * i);
     const int64_t row = 4 * i / g.n;
     store4(g, row, (int)(4 * i - row * g.n), v);
@@ -603,7 +605,7 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
 
 // The tiles, and what one K block of one takes (us) with every CU at work, for bf16 and for fp32 outputs: measured over
 // 17 shapes from m = 40 to 8192, each with 1, 2, 4 and 7 slices.
-enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64, kTiles };
+enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64x128, kT64Pair, kTiles };
 struct TileCost {
   int bm, bn, per_cu;   // workgroups of a CU at a time
   float step, step_f32;
@@ -612,7 +614,8 @@ constexpr TileCost kCost[kTiles] = {{256, 256, 1, 1.85f, 3.72f},
                                     {128, 256, 1, 1.10f, 2.15f},
                                     {128, 128, 1, 0.65f, 1.42f},
                                     {128, 128, 2, 1.27f, 2.00f},
-                                    {64, 128, 1, 0.47f, 0.91f}};
+                                    {64, 128, 1, 0.47f, 0.91f},
+                                    {64, 64, 2, 0.40f, 0.69f}};
 
 struct Plan {
   int rows;            // rows of a that the plan covers (from the first)
@@ -627,9 +630,9 @@ struct Plan {
 // back.  kb / slices is 2 at least.
 Plan plan_one(const moe_matmul_shape& s, int rows) {
   const int kb = s.k / kBK;
-  Plan best{rows, 0, kT64, 1, kb, 0.0f};
+  Plan best{rows, 0, kT64Pair, 1, kb, 0.0f};
   if (s.form == MOE_FP8_FORWARD && (rows <= 16 || (rows <= 32 && s.k <= 2048))) {
-    // straight from memory (1 x 4096 x 7168: 7.3 us against 11.3 with the best tile; 17 x 1024 x 1024: 6.2 against 7.6)
+    // straight from memory (1 x 4096 x 7168: 7.3 us against 11 with the best tile; 17 x 1024 x 1024: 6.2 against 7.6)
     best.rows_mb = rows <= 16 ? 1 : 2;
     best.us = 5.0f + (float)s.n * s.k / 1e7f;
     return best;
@@ -710,7 +713,8 @@ hipError_t launch_form(const MatmulArgs& g, const Plan& p, hipStream_t st) {
     case kT128x256: return launch_tile<FORM, EXACT, 128, 256, 2, 4, 3>(g, p.splits, st);
     case kT128: return launch_tile<FORM, EXACT, 128, 128, 2, 4, 4>(g, p.splits, st);
     case kT128Pair: return launch_tile<FORM, EXACT, 128, 128, 2, 2, 2>(g, p.splits, st);
-    default: return launch_tile<FORM, EXACT, 64, 128, 2, 2, 4>(g, p.splits, st);
+    case kT64x128: return launch_tile<FORM, EXACT, 64, 128, 2, 2, 4>(g, p.splits, st);
+    default: return launch_tile<FORM, EXACT, 64, 64, 2, 2, 4>(g, p.splits, st);
   }
 }
 
