@@ -398,7 +398,8 @@ moe_status moe_matmul_fp8(const moe_matmul_shape* shape, const uint8_t* a, const
  *   codes  [cols, R]      E4M3FN, R = rows rounded up to 128, rows past the last as zeros
  *   scales [cols, R/128]  fp32
  * scale = amax * fp32(1/448) (1 for a run of zeros), code = round-to-nearest-even E4M3FN of
- * fp32(x / scale), saturating at 448.  cols must be a multiple of 8 (MOE_ERR_UNSUPPORTED). */
+ * fp32(x / scale), saturating at 448.  cols must be a multiple of 8 (MOE_ERR_UNSUPPORTED), x and codes
+ * 16-byte aligned (MOE_ERR_INVALID_ARG). */
 moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, uint8_t* codes, float* scales,
                               hipStream_t stream);
 
@@ -410,7 +411,8 @@ moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, ui
  *   h        [rows, I]       bf16 out: a sigmoid(a) b; may be NULL
  *   saved    [rows, 2I]      int8 out
  *   scales   [rows, 2I/128]  fp32 out
- * inter (I) must be a multiple of 128 (MOE_ERR_UNSUPPORTED). */
+ * inter (I) must be a multiple of 128 (MOE_ERR_UNSUPPORTED); ab, h and saved 16-byte aligned, none in
+ * place of another (MOE_ERR_INVALID_ARG), here and below. */
 moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void* h, int8_t* saved, float* scales,
                                hipStream_t stream);
 
@@ -420,6 +422,36 @@ moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void
  * for dh [rows, I] bf16. */
 moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, const int8_t* saved, const float* scales,
                                 void* d_ab, void* h, hipStream_t stream);
+
+/* ---- The layer under a router of the caller's own, with its SwiGLU inputs kept in 8 bits ------
+ * moe_gate picks and weighs, moe_forward_train8 runs the experts, moe_backward_gates returns the
+ * gates' gradients for moe_gate_backward.  BF16 and FP8_B128, shapes as moe_backward.
+ *
+ * moe_saved8_size: bytes of the buffer that moe_forward_train8 writes (about half of
+ * moe_saved_inputs_size: int8 codes and a scale per 128 values of every row's a and b, as
+ * moe_swiglu_forward8 keeps them).  moe_train8_workspace_size: bytes of its workspace. */
+moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes);
+moe_status moe_train8_workspace_size(const moe_shape* shape, size_t* bytes);
+
+/* moe_forward_train (same output, to the bit) that keeps a and b in 8 bits in `saved8`, for
+ * moe_backward_gates with the same topk_idx.  Errors as moe_forward_train. */
+moe_status moe_forward_train8(const moe_shape* shape, const void* u, const moe_weights* weights,
+                              const int32_t* topk_idx, const float* topk_gate, void* out, void* saved8,
+                              size_t saved8_bytes, void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* moe_backward without its router: the gates are inputs, and their gradients come back.
+ *   saved8   from moe_forward_train8, or NULL (a and b are computed again, as in moe_backward)
+ *   du       [T, d]   bf16 out: the residual and the experts' input gradients; the router's term
+ *                     (d_logits times the caller's router weights) is the caller's to add
+ *   d_gate   [T, K_r] fp32 out: <dout, FFN_k(u)>, 0 where topk_idx is outside [0, N_r)
+ *   dw       as in moe_backward
+ * Workspace: moe_backward_workspace_size.  Errors as moe_backward; MOE_ERR_INVALID_ARG for a null
+ * d_gate (T > 0); MOE_ERR_WORKSPACE if saved8_bytes < moe_saved8_size. */
+moe_status moe_backward_gates(const moe_shape* shape, const void* u, const moe_weights* weights,
+                              const int32_t* topk_idx, const float* topk_gate, const void* saved8,
+                              size_t saved8_bytes, const void* dout, void* du, float* d_gate,
+                              const moe_weight_grads* dw, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream);
 
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int32_t status);

@@ -98,6 +98,12 @@ _SIG = {
     "moe_quantize_act_t": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P],
     "moe_swiglu_forward8": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P],
     "moe_swiglu_backward8": [ctypes.c_int32, ctypes.c_int32, _P, _P, _P, _P, _P, _P],
+    "moe_saved8_size": [ctypes.POINTER(Shape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_train8_workspace_size": [ctypes.POINTER(Shape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_forward_train8": [ctypes.POINTER(Shape), _P, ctypes.POINTER(Weights), _P, _P, _P, _P, ctypes.c_size_t, _P,
+                           ctypes.c_size_t, _P],
+    "moe_backward_gates": [ctypes.POINTER(Shape), _P, ctypes.POINTER(Weights), _P, _P, _P, ctypes.c_size_t, _P, _P, _P,
+                           ctypes.POINTER(WeightGrads), _P, ctypes.c_size_t, _P],
     "moe_status_string": [ctypes.c_int32],
 }
 for _name, _args in _SIG.items():
@@ -322,6 +328,33 @@ def moe_swiglu_forward8(rows, inter, ab, h, saved, scales, stream=None):
 def moe_swiglu_backward8(rows, inter, dh, saved, scales, d_ab, h=None, stream=None):
     _check("moe_swiglu_backward8", _lib.moe_swiglu_backward8(rows, inter, _addr(dh), _addr(saved), _addr(scales),
                                                              _addr(d_ab), _addr(h), _stream(stream)))
+
+
+def moe_saved8_size(shape: Shape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_saved8_size", _lib.moe_saved8_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_train8_workspace_size(shape: Shape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_train8_workspace_size", _lib.moe_train8_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_forward_train8(shape, u, weights: Weights, topk_idx, topk_gate, out, saved8, workspace, stream=None):
+    _check("moe_forward_train8", _lib.moe_forward_train8(
+        ctypes.byref(shape), _addr(u), ctypes.byref(weights), _addr(topk_idx), _addr(topk_gate), _addr(out),
+        _addr(saved8), _nbytes(saved8), _addr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_backward_gates(shape, u, weights: Weights, topk_idx, topk_gate, saved8, dout, du, d_gate, weight_grads,
+                       workspace, stream=None):
+    """saved8: what moe_forward_train8 kept, or None."""
+    _check("moe_backward_gates", _lib.moe_backward_gates(
+        ctypes.byref(shape), _addr(u), ctypes.byref(weights), _addr(topk_idx), _addr(topk_gate), _addr(saved8),
+        _nbytes(saved8), _addr(dout), _addr(du), _addr(d_gate), ctypes.byref(weight_grads), _addr(workspace),
+        _nbytes(workspace), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

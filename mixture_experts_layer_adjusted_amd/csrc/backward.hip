@@ -60,11 +60,13 @@ __global__ void row_gate_kernel(const int32_t* __restrict__ perm_row, const floa
   }
 }
 
+// ROUTER false: the gates' gradients go to d_gate, for a router of the caller's own
+template <bool ROUTER>
 __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
     const uint16_t* __restrict__ u, const float* __restrict__ E, const int32_t* __restrict__ idx,
     const int32_t* __restrict__ perm_row, const float* __restrict__ dg_part, int NT,
     const int32_t* __restrict__ seg_off, const uint16_t* __restrict__ dout, const uint16_t* __restrict__ dX, int d,
-    int N, int K, int Ns, uint16_t* __restrict__ du, float* __restrict__ row_dz) {
+    int N, int K, int Ns, uint16_t* __restrict__ du, float* __restrict__ row_dz, float* __restrict__ d_gate) {
   __shared__ float wsum[kRouterThreads / 64][kMaxTopK];
   __shared__ float s_k[kMaxTopK], dg_k[kMaxTopK], dz_k[kMaxTopK];
   __shared__ int32_t e_k[kMaxTopK], row_k[kMaxTopK];
@@ -82,7 +84,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
   // thread's 8-column slices (the u slice loaded once for all eight), then a fixed-order butterfly
   // within each wavefront and the wavefronts' sums in order
   const uint16_t* urow = u + t * d;
-  for (int k0 = 0; k0 < K; k0 += 8) {
+  for (int k0 = 0; ROUTER && k0 < K; k0 += 8) {
     float acc[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (int j = tid * 8; j < d; j += kRouterThreads * 8) {
       float uv[8];
@@ -117,16 +119,18 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
   __syncthreads();
   if (tid < K) {
     float z = 0.0f;
-    for (int w = 0; w < kRouterThreads / 64; ++w) z += wsum[w][tid];
+    if constexpr (ROUTER)
+      for (int w = 0; w < kRouterThreads / 64; ++w) z += wsum[w][tid];
     float dg = 0.0f;
     const int r = row_k[tid];
     if (r >= 0)
       for (int q = 0; q < NT; ++q) dg += dg_part[(int64_t)r * NT + q];
     s_k[tid] = r >= 0 ? 1.0f / (1.0f + expf(-z)) : 0.0f;
     dg_k[tid] = dg;
+    if constexpr (!ROUTER) d_gate[t * K + tid] = dg;
   }
   __syncthreads();
-  if (tid < K) {
+  if (ROUTER && tid < K) {
     float S = 0.0f, D = 0.0f;
     for (int k = 0; k < K; ++k) {
       S += s_k[k];
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kRouterThreads) router_bwd_kernel(
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[i] += v[i];
     }
-    for (int k = 0; k < K; ++k) {
+    for (int k = 0; ROUTER && k < K; ++k) {
       if (e_k[k] < 0) continue;
       const float* erow = E + (int64_t)e_k[k] * d + j;
       const float4 e0 = *reinterpret_cast<const float4*>(erow);
@@ -456,12 +460,13 @@ hipError_t launch_swiglu_bwd_saved(const void* ab, const void* dhu, const float*
 
 hipError_t launch_router_bwd(const moe_shape& s, const void* u, const float* centroids, const int32_t* idx,
                              const int32_t* perm_row, const float* dg_part, const int32_t* seg_off, const void* dout,
-                             const void* dX, void* du, float* row_dz, hipStream_t st) {
+                             const void* dX, void* du, float* row_dz, float* d_gate, hipStream_t st) {
   if (s.tokens == 0) return hipSuccess;
-  hipLaunchKernelGGL(router_bwd_kernel, dim3((unsigned)s.tokens), dim3(kRouterThreads), 0, st,
+  auto kern = d_gate ? &router_bwd_kernel<false> : &router_bwd_kernel<true>;
+  hipLaunchKernelGGL(kern, dim3((unsigned)s.tokens), dim3(kRouterThreads), 0, st,
                      static_cast<const uint16_t*>(u), centroids, idx, perm_row, dg_part, s.inter / 128, seg_off,
                      static_cast<const uint16_t*>(dout), static_cast<const uint16_t*>(dX), s.hidden, s.n_routed,
-                     s.top_k, s.n_shared, static_cast<uint16_t*>(du), row_dz);
+                     s.top_k, s.n_shared, static_cast<uint16_t*>(du), row_dz, d_gate);
   return hipGetLastError();
 }
 

@@ -133,10 +133,35 @@ static moe_status check_shape(const moe_shape* s) {
 
 static moe_status hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 
-// saved: null, or (BF16, FP8_B128) [max_rows, 2I] bf16 for the gate/up GEMM's SwiGLU inputs [a b]
+// 8-bit saved SwiGLU inputs of the permuted rows: int8 codes [max_rows, 2I], then fp32 scales [max_rows, 2I / 128]
+struct Saved8 {
+  int8_t* codes;
+  float* scales;
+};
+static size_t saved8_codes_bytes(const moe_shape& s, const WorkspacePlan& p) {
+  return align_up((size_t)p.max_rows * 2 * s.inter, 256);
+}
+static size_t saved8_bytes_for(const moe_shape& s, const WorkspacePlan& p) {
+  return saved8_codes_bytes(s, p) + (size_t)p.max_rows * (2 * s.inter / 128) * 4;
+}
+static Saved8 saved8_at(const moe_shape& s, const WorkspacePlan& p, const void* saved) {
+  char* at = const_cast<char*>(static_cast<const char*>(saved));
+  return {reinterpret_cast<int8_t*>(at), reinterpret_cast<float*>(at + saved8_codes_bytes(s, p))};
+}
+// moe_forward_train8's bf16 [a b] between the gate/up GEMM and the packing: where the down GEMM then writes y, if it
+// fits there, else past the forward's workspace
+static size_t train8_ab(const moe_shape& s, const WorkspacePlan& p) {
+  return 2 * (int64_t)s.inter <= s.hidden ? p.y : p.total;
+}
+static size_t train8_bytes(const moe_shape& s, const WorkspacePlan& p) {
+  return train8_ab(s, p) == p.y ? p.total : p.total + (size_t)p.max_rows * 2 * s.inter * 2;
+}
+
+// saved: null, or (BF16, FP8_B128) [max_rows, 2I] bf16 for the gate/up GEMM's SwiGLU inputs [a b]; saved8: null, or
+// where they go in 8 bits
 static moe_status forward_impl(const moe_shape* shape, const void* u, const moe_weights* w, const int32_t* idx,
                                const float* gate, void* out, void* ws, size_t ws_bytes, hipStream_t st,
-                               hipEvent_t* ev, int32_t n_ev, void* saved = nullptr) {
+                               hipEvent_t* ev, int32_t n_ev, void* saved = nullptr, void* saved8 = nullptr) {
   moe_status rc = check_shape(shape);
   if (rc != MOE_OK) return rc;
   const moe_shape& s = *shape;
@@ -156,8 +181,9 @@ static moe_status forward_impl(const moe_shape* shape, const void* u, const moe_
     return MOE_ERR_INVALID_ARG;
   if (out == u) return MOE_ERR_INVALID_ARG;
   const WorkspacePlan p = plan_workspace(s);
-  if (ws_bytes < p.total) return MOE_ERR_WORKSPACE;
+  if (ws_bytes < (saved8 ? train8_bytes(s, p) : p.total)) return MOE_ERR_WORKSPACE;
   char* wsb = static_cast<char*>(ws);
+  if (saved8) saved = wsb + train8_ab(s, p);
 
   if (mark(0) != hipSuccess) return MOE_ERR_HIP;
   if ((rc = hip_status(launch_permute(s, idx, p, wsb, st))) != MOE_OK) return rc;
@@ -204,6 +230,12 @@ static moe_status forward_impl(const moe_shape* shape, const void* u, const moe_
     g1.out2 = saved;
     if ((rc = hip_status(fp8 ? launch_gemm_fp8_swiglu_save(g1, st) : launch_gemm_bf16_swiglu_save(g1, st))) != MOE_OK)
       return rc;
+    if (saved8) {
+      const Saved8 at = saved8_at(s, p, saved8);
+      if ((rc = hip_status(launch_swiglu8_forward(p.max_rows, g1.seg_off + g1.n_seg, s.inter, saved, nullptr, at.codes,
+                                                  at.scales, st))) != MOE_OK)
+        return rc;
+    }
   } else if ((rc = hip_status(launch_gemm_swiglu(s.dtype, g1, st))) != MOE_OK) {
     return rc;
   }
@@ -242,6 +274,12 @@ static moe_status forward_impl(const moe_shape* shape, const void* u, const moe_
 }  // namespace moe
 
 using namespace moe;
+
+// whether every pointer (null ones aside) is a multiple of 16
+template <typename... P>
+static bool aligned16(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 15) == 0;
+}
 
 extern "C" {
 
@@ -387,7 +425,7 @@ moe_status moe_forward_profiled(const moe_shape* shape, const void* u, const moe
 static moe_status fp8_backward(const moe_shape& s, const WorkspacePlan& p, char* wsb, const void* u,
                                const float* centroids, const moe_weights* w, const int32_t* topk_idx,
                                const void* dout, void* du, const moe_weight_grads* dw, hipStream_t stream,
-                               const void* saved) {
+                               const void* saved, const void* saved8, float* d_gate) {
   moe_status rc;
   const int64_t T = s.tokens, d = s.hidden, I = s.inter, Nr = s.n_routed, Ns = s.n_shared, P = p.max_rows;
   const int64_t p8 = P / 128;
@@ -439,7 +477,7 @@ static moe_status fp8_backward(const moe_shape& s, const WorkspacePlan& p, char*
   };
   if (T > 0) {
     // E4M3 copies of u and dout (1 x 128 tiles along d)
-    if (!saved && (rc = hip_status(launch_quantize_act(T, (int)d, u, u_q, u_s, stream))) != MOE_OK) return rc;
+    if (!saved && !saved8 && (rc = hip_status(launch_quantize_act(T, (int)d, u, u_q, u_s, stream))) != MOE_OK) return rc;
     if ((rc = hip_status(launch_quantize_act(T, (int)d, dout, dout_q, dout_s, stream))) != MOE_OK) return rc;
     GemmOperands g{};
     g.tile_seg = reinterpret_cast<const int32_t*>(at(p.tile_seg));
@@ -465,7 +503,12 @@ static moe_status fp8_backward(const moe_shape& s, const WorkspacePlan& p, char*
     g1.kn_split = (int)d;
     g1.out = dhu;
     if ((rc = hip_status(launch_gemm_fp8_dgrad(g1, stream))) != MOE_OK) return rc;
-    if (saved) {
+    if (saved8) {
+      const Saved8 at = saved8_at(s, p, saved8);
+      if ((rc = hip_status(launch_swiglu_bwd_saved8(at.codes, at.scales, dhu, row_gate, row_token, seg_off + Nr + Ns, P,
+                                                    (int)I, dab, hb, dg_part, stream))) != MOE_OK)
+        return rc;
+    } else if (saved) {
       // [dA dB], H and the gate-gradient partials from the forward's saved [a b]
       if ((rc = hip_status(launch_swiglu_bwd_saved(saved, dhu, row_gate, row_token, seg_off + Nr + Ns, P, (int)I, dab,
                                                    hb, dg_part, stream))) != MOE_OK)
@@ -515,7 +558,7 @@ static moe_status fp8_backward(const moe_shape& s, const WorkspacePlan& p, char*
     g3.out = dx;
     if ((rc = hip_status(launch_gemm_fp8_dgrad(g3, stream))) != MOE_OK) return rc;
     if ((rc = hip_status(launch_router_bwd(s, u, centroids, topk_idx, perm_row, dg_part, seg_off, dout, dx, du,
-                                           row_dz, stream))) != MOE_OK)
+                                           row_dz, d_gate, stream))) != MOE_OK)
       return rc;
     // weight-gradient operands: (g dout)^T, H^T, [dA dB]^T, X^T, quantised per run of 128 rows
     auto tq = [&](const void* src, int64_t lds, bool gather, const float* scale, uint8_t* dst, float* ds, int64_t C) {
@@ -589,16 +632,20 @@ moe_status moe_forward_train(const moe_shape* shape, const void* u, const moe_we
 static moe_status backward_impl(const moe_shape* shape, const void* u, const float* centroids, const moe_weights* w,
                                 const int32_t* topk_idx, const float* topk_gate, const void* dout, void* du,
                                 float* d_centroids, const moe_weight_grads* dw, void* workspace,
-                                size_t workspace_bytes, hipStream_t stream, const void* saved) {
+                                size_t workspace_bytes, hipStream_t stream, const void* saved,
+                                const void* saved8 = nullptr, float* d_gate = nullptr, bool router = true) {
   moe_status rc = check_backward_shape(shape);
   if (rc != MOE_OK) return rc;
   const moe_shape& s = *shape;
-  if (!u || !centroids || !w || !dout || !du || !d_centroids || !dw || !workspace) return MOE_ERR_INVALID_ARG;
+  if (router ? !centroids || !d_centroids : s.tokens > 0 && !d_gate) return MOE_ERR_INVALID_ARG;
+  // (an empty batch's tensors may have no address; with the router they have always had to have one)
+  if ((router || s.tokens > 0) && (!u || !dout || !du)) return MOE_ERR_INVALID_ARG;
+  if (!w || !dw || !workspace) return MOE_ERR_INVALID_ARG;
   if (s.tokens > 0 && (!topk_idx || !topk_gate)) return MOE_ERR_INVALID_ARG;
   if (!w->w_gate || !w->w_up || !w->w_down || !dw->w_gate || !dw->w_up || !dw->w_down) return MOE_ERR_INVALID_ARG;
   if (s.n_shared > 0 && (!w->sh_gate || !w->sh_up || !w->sh_down || !dw->sh_gate || !dw->sh_up || !dw->sh_down))
     return MOE_ERR_INVALID_ARG;
-  if (du == u || du == dout) return MOE_ERR_INVALID_ARG;
+  if (du && (du == u || du == dout)) return MOE_ERR_INVALID_ARG;
   const bool fp8 = s.dtype == MOE_DTYPE_FP8_B128;
   if (fp8 && (!w->w_gate_scale || !w->w_up_scale || !w->w_down_scale)) return MOE_ERR_INVALID_ARG;
   if (fp8 && s.n_shared > 0 && (!w->sh_gate_scale || !w->sh_up_scale || !w->sh_down_scale))
@@ -631,7 +678,9 @@ static moe_status backward_impl(const moe_shape* shape, const void* u, const flo
       MOE_OK)
     return rc;
   if (fp8) {
-    if ((rc = fp8_backward(s, p, wsb, u, centroids, w, topk_idx, dout, du, dw, stream, saved)) != MOE_OK) return rc;
+    if ((rc = fp8_backward(s, p, wsb, u, centroids, w, topk_idx, dout, du, dw, stream, saved, saved8, d_gate)) != MOE_OK)
+      return rc;
+    if (!router) return MOE_OK;
     return hip_status(launch_dcentroid(s, u, row_token, row_dz, seg_off, tile_seg, p.max_tiles, dc_part,
                                        d_centroids, stream));
   }
@@ -690,7 +739,12 @@ static moe_status backward_impl(const moe_shape* shape, const void* u, const flo
     GemmOperands g1 = grouped(dout, row_token, T, bf(w->w_down), bf(w->sh_down), (int)d, (int)I, dhu);
     g1.kn_split = (int)d;
     if ((rc = hip_status(launch_gemm_bf16_dgrad(g1, stream))) != MOE_OK) return rc;
-    if (saved) {
+    if (saved8) {
+      const Saved8 at = saved8_at(s, p, saved8);
+      if ((rc = hip_status(launch_swiglu_bwd_saved8(at.codes, at.scales, dhu, row_gate, row_token, seg_off + Nr + Ns, P,
+                                                    (int)I, dab, hb, dg_part, stream))) != MOE_OK)
+        return rc;
+    } else if (saved) {
       // [dA dB], H and the gate-gradient partials from the forward's saved [a b]
       if ((rc = hip_status(launch_swiglu_bwd_saved(saved, dhu, row_gate, row_token, seg_off + Nr + Ns, P, (int)I, dab,
                                                    hb, dg_part, stream))) != MOE_OK)
@@ -716,7 +770,7 @@ static moe_status backward_impl(const moe_shape* shape, const void* u, const flo
     if ((rc = hip_status(launch_gemm_bf16_dgrad(g3, stream))) != MOE_OK) return rc;
     // router backward and du
     if ((rc = hip_status(launch_router_bwd(s, u, centroids, topk_idx, perm_row, dg_part, seg_off, dout, dx, du,
-                                           row_dz, stream))) != MOE_OK)
+                                           row_dz, d_gate, stream))) != MOE_OK)
       return rc;
     // K-contiguous (transposed) activations of every permuted row for the weight-gradient GEMMs:
     // (g dout)^T [d][P], H^T [I][P], [dA dB]^T [2I][P], X^T [d][P]; padding rows are zero
@@ -730,6 +784,7 @@ static moe_status backward_impl(const moe_shape* shape, const void* u, const flo
   if ((rc = wgrad(dy_t, (int)d, h_t, (int)I, dw->w_down, dw->sh_down)) != MOE_OK) return rc;
   if ((rc = wgrad(dab_t, (int)I, x_t, (int)d, dw->w_gate, dw->sh_gate)) != MOE_OK) return rc;
   if ((rc = wgrad(dab_t + I * P, (int)I, x_t, (int)d, dw->w_up, dw->sh_up)) != MOE_OK) return rc;
+  if (!router) return MOE_OK;
   return hip_status(launch_dcentroid(s, u, row_token, row_dz, seg_off, tile_seg, p.max_tiles, dc_part,
                                      d_centroids, stream));
 }
@@ -753,6 +808,47 @@ moe_status moe_backward_saved(const moe_shape* shape, const void* u, const float
   if (saved == du) return MOE_ERR_INVALID_ARG;
   return backward_impl(shape, u, centroids, w, topk_idx, topk_gate, dout, du, d_centroids, dw, workspace,
                        workspace_bytes, stream, saved);
+}
+
+moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes) {
+  moe_status rc = check_backward_shape(shape);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = saved8_bytes_for(*shape, plan_workspace(*shape));
+  return MOE_OK;
+}
+
+moe_status moe_train8_workspace_size(const moe_shape* shape, size_t* bytes) {
+  moe_status rc = check_backward_shape(shape);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = train8_bytes(*shape, plan_workspace(*shape));
+  return MOE_OK;
+}
+
+moe_status moe_forward_train8(const moe_shape* shape, const void* u, const moe_weights* weights, const int32_t* topk_idx,
+                              const float* topk_gate, void* out, void* saved8, size_t saved8_bytes, void* workspace,
+                              size_t workspace_bytes, hipStream_t stream) {
+  moe_status rc = check_backward_shape(shape);
+  if (rc != MOE_OK) return rc;
+  if (shape->tokens == 0) return MOE_OK;
+  if (!saved8) return MOE_ERR_INVALID_ARG;
+  if (saved8_bytes < saved8_bytes_for(*shape, plan_workspace(*shape))) return MOE_ERR_WORKSPACE;
+  if (saved8 == u || saved8 == out || saved8 == workspace || !aligned16(saved8)) return MOE_ERR_INVALID_ARG;
+  return forward_impl(shape, u, weights, topk_idx, topk_gate, out, workspace, workspace_bytes, stream, nullptr, 0, nullptr,
+                      saved8);
+}
+
+moe_status moe_backward_gates(const moe_shape* shape, const void* u, const moe_weights* w, const int32_t* topk_idx,
+                              const float* topk_gate, const void* saved8, size_t saved8_bytes, const void* dout, void* du,
+                              float* d_gate, const moe_weight_grads* dw, void* workspace, size_t workspace_bytes,
+                              hipStream_t stream) {
+  moe_status rc = check_backward_shape(shape);
+  if (rc != MOE_OK) return rc;
+  if (saved8 && saved8_bytes < saved8_bytes_for(*shape, plan_workspace(*shape))) return MOE_ERR_WORKSPACE;
+  if (saved8 && (saved8 == du || !aligned16(saved8))) return MOE_ERR_INVALID_ARG;
+  return backward_impl(shape, u, nullptr, w, topk_idx, topk_gate, dout, du, nullptr, dw, workspace, workspace_bytes, stream,
+                       nullptr, saved8, d_gate, false);
 }
 
 moe_status moe_update_bias(int32_t n_routed, int64_t total_assignments, const int32_t* expert_load, float* bias,
@@ -920,12 +1016,11 @@ moe_status moe_matmul_fp8(const moe_matmul_shape* shape, const uint8_t* a, const
   if (rc != MOE_OK) return rc;
   if (shape->m == 0 || shape->n == 0) return MOE_OK;
   if (!out || (shape->k > 0 && (!a || !a_scale || !b || !b_scale))) return MOE_ERR_INVALID_ARG;
-  const uintptr_t at = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(out);
-  if (at % 16 != 0) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(a, b, out, workspace)) return MOE_ERR_INVALID_ARG;
   if (out == a || out == b || out == a_scale || out == b_scale) return MOE_ERR_INVALID_ARG;
   const size_t need = matmul_fp8_workspace(*shape);
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
-  if (need > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % 16 != 0)) return MOE_ERR_INVALID_ARG;
+  if (need > 0 && !workspace) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_matmul_fp8(*shape, a, a_scale, b, b_scale, out, static_cast<float*>(workspace), stream));
 }
 
@@ -934,7 +1029,7 @@ moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, ui
   if (rows < 0 || cols < 0) return MOE_ERR_INVALID_ARG;
   if (cols % 8 != 0 || ceil_div(cols, 64) > 65535) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)rows * cols == 0) return MOE_OK;
-  if (!x_bf16 || !codes || !scales) return MOE_ERR_INVALID_ARG;
+  if (!x_bf16 || !codes || !scales || !aligned16(x_bf16, codes)) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_quantize_act_t(rows, cols, x_bf16, codes, scales, stream));
 }
 
@@ -943,8 +1038,8 @@ moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void
   if (rows < 0 || inter < 0) return MOE_ERR_INVALID_ARG;
   if (inter % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)rows * inter == 0) return MOE_OK;
-  if (!ab || !saved || !scales || h == ab || saved == ab) return MOE_ERR_INVALID_ARG;
-  return hip_status(launch_swiglu8_forward(rows, inter, ab, h, saved, scales, stream));
+  if (!ab || !saved || !scales || h == ab || saved == ab || !aligned16(ab, h, saved)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_swiglu8_forward(rows, nullptr, inter, ab, h, saved, scales, stream));
 }
 
 moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, const int8_t* saved, const float* scales,
@@ -954,6 +1049,7 @@ moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, con
   if ((int64_t)rows * inter == 0) return MOE_OK;
   if (!dh || !saved || !scales || !d_ab || d_ab == saved || d_ab == dh || h == dh || h == d_ab || h == saved)
     return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dh, saved, d_ab, h)) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_swiglu8_backward(rows, inter, dh, saved, scales, d_ab, h, stream));
 }
 

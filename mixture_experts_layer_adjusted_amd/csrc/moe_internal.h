@@ -190,9 +190,11 @@ struct TransposeQuantArgs {
 hipError_t launch_transpose_quant(const TransposeQuantArgs& a, hipStream_t st);
 hipError_t launch_row_gate(const moe_shape& s, const int32_t* perm_row, const float* gate, const int32_t* seg_off,
                            int64_t max_rows, float* row_gate, float* row_dz, hipStream_t st);
+// d_gate null: the sigmoid router's backward (row_dz, the centroids' part of du).  Else the gates' gradients are written
+// to d_gate [T, K_r] and du takes nothing from a router (centroids, row_dz unused)
 hipError_t launch_router_bwd(const moe_shape& s, const void* u, const float* centroids, const int32_t* idx,
                              const int32_t* perm_row, const float* dg_part, const int32_t* seg_off, const void* dout,
-                             const void* dX, void* du, float* row_dz, hipStream_t st);
+                             const void* dX, void* du, float* row_dz, float* d_gate, hipStream_t st);
 // SwiGLU backward from saved inputs: ab [rows, 2I] (a then b), dhu [rows, I] -> dab [rows, 2I],
 // h [rows, I], dg_part [rows, I / 128], for the rows [0, *seg_end) (padding rows: zeros)
 hipError_t launch_swiglu_bwd_saved(const void* ab, const void* dhu, const float* row_gate, const int32_t* row_token,
@@ -230,10 +232,14 @@ hipError_t launch_matmul_fp8(const moe_matmul_shape& s, const uint8_t* a, const 
                              const float* b_scale, void* out, float* ws, hipStream_t st);
 hipError_t launch_quantize_act_t(int rows, int cols, const void* x, uint8_t* codes, float* scales, hipStream_t st);
 
-// SwiGLU with 8-bit saved inputs (swiglu8.hip); h may be null
-hipError_t launch_swiglu8_forward(int64_t rows, int I, const void* ab, void* h, int8_t* codes, float* scales,
-                                  hipStream_t st);
+// SwiGLU with 8-bit saved inputs (swiglu8.hip); h may be null; row_end: rows in use as a device value, or null (all)
+hipError_t launch_swiglu8_forward(int64_t rows, const int32_t* row_end, int I, const void* ab, void* h, int8_t* codes,
+                                  float* scales, hipStream_t st);
 hipError_t launch_swiglu8_backward(int64_t rows, int I, const void* dh, const int8_t* codes, const float* scales,
                                    void* dab, void* h, hipStream_t st);
+// launch_swiglu_bwd_saved from the 8-bit codes [max_rows, 2I] and scales [max_rows, 2I / 128]
+hipError_t launch_swiglu_bwd_saved8(const int8_t* codes, const float* scales, const void* dhu, const float* row_gate,
+                                    const int32_t* row_token, const int32_t* row_end, int64_t max_rows, int I, void* dab,
+                                    void* h, float* dg_part, hipStream_t st);
 
 }  // namespace moe

@@ -8,6 +8,10 @@
 // amax / 254 over the run, against x / 16 for E4M3's values (for normal values 0.6% of their size against 2.3%).
 // A run with an infinity or NaN gets the scale NaN, so that its gradients are NaN and not plausible numbers.
 //
+// The layer's rows (moe_forward_train8, moe_backward_gates) are those of the permuted layout: as many as *row_end says;
+// the backward pass weighs dh by the row's gate, writes padding rows (row_token < 0) as zeros and hands back, for every
+// row and run, the sum of dh H before the gate (its share of the gate's gradient).
+//
 // 16 lanes share one run of 128 features of a row, 8 features a lane: 16-byte loads and stores, the run's amax by
 // four row rotations.
 #include "moe_internal.h"
@@ -85,12 +89,13 @@ __device__ __forceinline__ void decode8(const uint2& q, float scale, float (&v)[
   }
 }
 
-// h may be null (the codes alone)
-__global__ void __launch_bounds__(kThreads) swiglu8_fwd_kernel(const uint16_t* __restrict__ ab, int64_t units, int I,
+// h may be null (the codes alone); row_end may be null (rows)
+__global__ void __launch_bounds__(kThreads) swiglu8_fwd_kernel(const uint16_t* __restrict__ ab, int64_t rows,
+                                                               const int32_t* __restrict__ row_end, int I,
                                                                uint16_t* __restrict__ h, int8_t* __restrict__ codes,
                                                                float* __restrict__ scales) {
   const int sub = threadIdx.x & 15, per_row = I / 128;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
+  const int64_t units = (row_end ? (int64_t)*row_end : rows) * per_row, step = (int64_t)gridDim.x * (kThreads / 16);
   for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); u < units; u += step) {
     const int64_t r = u / per_row;
     const int run = (int)(u - r * per_row), f = run * 128 + sub * 8;
@@ -114,12 +119,22 @@ __global__ void __launch_bounds__(kThreads) swiglu8_fwd_kernel(const uint16_t* _
   }
 }
 
+struct Swiglu8Rows {
+  const int32_t* row_end;
+  const float* row_gate;
+  const int32_t* row_token;
+  float* dg_part;   // [rows, I / 128]
+};
+
+// h may be null (LAYER: it is not)
+template <bool LAYER>
 __global__ void __launch_bounds__(kThreads) swiglu8_bwd_kernel(const uint16_t* __restrict__ dh,
                                                                const int8_t* __restrict__ codes,
-                                                               const float* __restrict__ scales, int64_t units, int I,
-                                                               uint16_t* __restrict__ dab, uint16_t* __restrict__ h) {
+                                                               const float* __restrict__ scales, int64_t rows, int I,
+                                                               uint16_t* __restrict__ dab, uint16_t* __restrict__ h,
+                                                               Swiglu8Rows w) {
   const int sub = threadIdx.x & 15, per_row = I / 128;
-  const int64_t step = (int64_t)gridDim.x * (kThreads / 16);
+  const int64_t units = (LAYER ? (int64_t)*w.row_end : rows) * per_row, step = (int64_t)gridDim.x * (kThreads / 16);
   for (int64_t u = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); u < units; u += step) {
     const int64_t r = u / per_row;
     const int run = (int)(u - r * per_row), f = run * 128 + sub * 8;
@@ -127,16 +142,27 @@ __global__ void __launch_bounds__(kThreads) swiglu8_bwd_kernel(const uint16_t* _
     decode8(*reinterpret_cast<const uint2*>(codes + r * 2 * I + f), scales[r * 2 * per_row + run], a);
     decode8(*reinterpret_cast<const uint2*>(codes + r * 2 * I + I + f), scales[r * 2 * per_row + per_row + run], b);
     unpack8(*reinterpret_cast<const uint4*>(dh + r * I + f), d);
+    const bool pad = LAYER && w.row_token[r] < 0;
+    const float gate = LAYER ? w.row_gate[r] : 1.0f;
+    float part = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float sg = 1.0f / (1.0f + __expf(-a[i]));
-      da[i] = d[i] * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
-      db[i] = d[i] * a[i] * sg;
-      o[i] = a[i] * sg * b[i];
+      const float sg = 1.0f / (1.0f + __expf(-a[i])), dg = LAYER ? gate * d[i] : d[i];
+      da[i] = pad ? 0.0f : dg * b[i] * sg * (1.0f + a[i] * (1.0f - sg));
+      db[i] = pad ? 0.0f : dg * a[i] * sg;
+      o[i] = pad ? 0.0f : a[i] * sg * b[i];
+      if (LAYER) part = pad ? 0.0f : fmaf(d[i], o[i], part);
     }
     *reinterpret_cast<uint4*>(dab + r * 2 * I + f) = pack8(da);
     *reinterpret_cast<uint4*>(dab + r * 2 * I + I + f) = pack8(db);
     if (h) *reinterpret_cast<uint4*>(h + r * I + f) = pack8(o);
+    if constexpr (LAYER) {
+      part += __uint_as_float(rotated<0x128>(__float_as_uint(part)));
+      part += __uint_as_float(rotated<0x124>(__float_as_uint(part)));
+      part += __uint_as_float(rotated<0x122>(__float_as_uint(part)));
+      part += __uint_as_float(rotated<0x121>(__float_as_uint(part)));
+      if (sub == 0) w.dg_part[r * per_row + run] = part;
+    }
   }
 }
 
@@ -146,12 +172,12 @@ unsigned blocks_for(int64_t units) {
 
 }  // namespace
 
-hipError_t launch_swiglu8_forward(int64_t rows, int I, const void* ab, void* h, int8_t* codes, float* scales,
-                                  hipStream_t st) {
+hipError_t launch_swiglu8_forward(int64_t rows, const int32_t* row_end, int I, const void* ab, void* h, int8_t* codes,
+                                  float* scales, hipStream_t st) {
   const int64_t units = rows * (I / 128);
   if (units == 0) return hipSuccess;
   hipLaunchKernelGGL(swiglu8_fwd_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, st,
-                     static_cast<const uint16_t*>(ab), units, I, static_cast<uint16_t*>(h), codes, scales);
+                     static_cast<const uint16_t*>(ab), rows, row_end, I, static_cast<uint16_t*>(h), codes, scales);
   return hipGetLastError();
 }
 
@@ -159,9 +185,20 @@ hipError_t launch_swiglu8_backward(int64_t rows, int I, const void* dh, const in
                                    void* dab, void* h, hipStream_t st) {
   const int64_t units = rows * (I / 128);
   if (units == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu8_bwd_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, st,
-                     static_cast<const uint16_t*>(dh), codes, scales, units, I, static_cast<uint16_t*>(dab),
-                     static_cast<uint16_t*>(h));
+  hipLaunchKernelGGL(swiglu8_bwd_kernel<false>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
+                     static_cast<const uint16_t*>(dh), codes, scales, rows, I, static_cast<uint16_t*>(dab),
+                     static_cast<uint16_t*>(h), Swiglu8Rows{});
+  return hipGetLastError();
+}
+
+hipError_t launch_swiglu_bwd_saved8(const int8_t* codes, const float* scales, const void* dhu, const float* row_gate,
+                                    const int32_t* row_token, const int32_t* row_end, int64_t max_rows, int I, void* dab,
+                                    void* h, float* dg_part, hipStream_t st) {
+  const int64_t units = max_rows * (I / 128);
+  if (units == 0) return hipSuccess;
+  hipLaunchKernelGGL(swiglu8_bwd_kernel<true>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
+                     static_cast<const uint16_t*>(dhu), codes, scales, max_rows, I, static_cast<uint16_t*>(dab),
+                     static_cast<uint16_t*>(h), Swiglu8Rows{row_end, row_gate, row_token, dg_part});
   return hipGetLastError();
 }
 

@@ -114,3 +114,41 @@ def test_quantize_act_t_and_swiglu8():
         a[i] = None
         assert b(4, 128, *a) == INVALID
     assert b(4, 128, P[0], P[1], P[2], P[1], P[4]) == INVALID and b(4, 128, P[0], P[1], P[2], P[3], P[0]) == INVALID
+
+
+def test_layer_under_a_given_router():
+    sb = moe.make_shape(300, 256, 16, 4, 1, 128, moe.MOE_DTYPE_BF16)
+    s32 = moe.make_shape(300, 256, 16, 4, 1, 128, moe.MOE_DTYPE_F32)
+    n, m = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    assert lib.moe_saved8_size(ctypes.byref(sb), ctypes.byref(n)) == OK
+    rows = 128 * ((300 * 4 + 16 * 127) // 128 + 3)
+    assert n.value == rows * 256 + rows * 2 * 4                     # codes (a multiple of 256 bytes), scales
+    assert lib.moe_saved8_size(ctypes.byref(s32), ctypes.byref(n)) == UNSUPPORTED
+    assert lib.moe_saved8_size(ctypes.byref(sb), None) == INVALID
+    assert lib.moe_workspace_size(ctypes.byref(sb), ctypes.byref(m)) == OK
+    t8 = ctypes.c_size_t(0)
+    assert lib.moe_train8_workspace_size(ctypes.byref(sb), ctypes.byref(t8)) == OK and t8.value == m.value   # 2I <= d
+    wide = moe.make_shape(300, 256, 16, 4, 1, 256, moe.MOE_DTYPE_BF16)
+    assert lib.moe_workspace_size(ctypes.byref(wide), ctypes.byref(m)) == OK
+    assert lib.moe_train8_workspace_size(ctypes.byref(wide), ctypes.byref(t8)) == OK
+    assert t8.value == m.value + rows * 512 * 2
+    w = moe.Weights(*(0x10000,) * 6)
+    fwd = lambda s, sv, sb_, wsb: lib.moe_forward_train8(  # noqa: E731
+        ctypes.byref(s), P[0], ctypes.byref(w), P[1], P[2], P[3], sv, sb_, P[5], wsb, None)
+    assert fwd(sb, None, BIG, BIG) == INVALID and fwd(sb, P[4], 16, BIG) == WORKSPACE
+    assert fwd(sb, P[0], BIG, BIG) == INVALID and fwd(sb, P[4], BIG, 16) == WORKSPACE
+    assert fwd(sb, ctypes.c_void_p(P[4].value + 8), BIG, BIG) == INVALID and fwd(s32, P[4], BIG, BIG) == UNSUPPORTED
+    wg = moe.WeightGrads(*(0x70000,) * 6)
+    bwd = lambda s, sv, sb_, du, dg, wsb: lib.moe_backward_gates(  # noqa: E731
+        ctypes.byref(s), P[0], ctypes.byref(w), P[1], P[2], sv, sb_, P[3], du, dg, ctypes.byref(wg), P[5], wsb, None)
+    assert bwd(sb, None, 0, P[4], None, BIG) == INVALID and bwd(sb, None, 0, None, P[6], BIG) == INVALID
+    assert bwd(sb, P[7], 16, P[4], P[6], BIG) == WORKSPACE and bwd(sb, P[7], BIG, P[7], P[6], BIG) == INVALID
+    assert bwd(sb, None, 0, P[0], P[6], BIG) == INVALID and bwd(sb, None, 0, P[4], P[6], 16) == WORKSPACE
+    assert bwd(s32, None, 0, P[4], P[6], BIG) == UNSUPPORTED
+
+
+def test_misaligned_pointers():
+    off = lambda i: ctypes.c_void_p(P[i].value + 8)  # noqa: E731
+    assert lib.moe_quantize_act_t(4, 8, off(0), P[1], P[2], None) == INVALID
+    assert lib.moe_swiglu_forward8(4, 128, P[0], off(1), P[2], P[3], None) == INVALID
+    assert lib.moe_swiglu_backward8(4, 128, P[0], P[1], P[2], off(3), P[4], None) == INVALID
