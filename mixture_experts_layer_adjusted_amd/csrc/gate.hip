@@ -618,8 +618,8 @@ hipError_t gate_backward_t(const GateBwdArgs& a, hipStream_t st) {
   hipLaunchKernelGGL((gate_bwd_kernel<L, C, TL, SOFTMAX, DENSE>), dim3(grid), dim3(kBwdThreads), lds, st, a)
   if (a.N <= 4 * L) MOE_GATE_CASE(1);
   else if (a.N <= 8 * L) MOE_GATE_CASE(2);
-  else if (a.N <= 16 * L) MOE_GATE_CASE(4);
-  else MOE_GATE_CASE(8);
+  else if (L == 32 || a.N <= 16 * L) MOE_GATE_CASE(4);   // (512 experts at most)
+  else if constexpr (L == 16) MOE_GATE_CASE(8);
 #undef MOE_GATE_CASE
   return hipGetLastError();
 }

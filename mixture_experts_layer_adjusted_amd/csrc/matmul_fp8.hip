@@ -604,17 +604,16 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
 // ---- which kernel ----------------------------------------------------------------------------------------------
 
 // The tiles, and what one K block of one takes (us) with every CU at work, for bf16 and for fp32 outputs: measured over
-// 17 shapes from m = 40 to 8192, each with 1, 2, 4 and 7 slices.
-enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64x128, kT64Pair, kTiles };
+// 17 shapes from m = 40 to 8192, each with 1, 2, 4 and 7 slices.  (0: not built.)
+enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64Pair, kTiles };
 struct TileCost {
   int bm, bn, per_cu;   // workgroups of a CU at a time
   float step, step_f32;
 };
 constexpr TileCost kCost[kTiles] = {{256, 256, 1, 1.85f, 3.72f},
-                                    {128, 256, 1, 1.10f, 2.15f},
+                                    {128, 256, 1, 1.10f, 0.0f},
                                     {128, 128, 1, 0.65f, 1.42f},
                                     {128, 128, 2, 1.27f, 2.00f},
-                                    {64, 128, 1, 0.47f, 0.91f},
                                     {64, 64, 2, 0.40f, 0.69f}};
 
 struct Plan {
@@ -640,6 +639,7 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
   const bool f32 = s.out_dtype == MOE_DTYPE_F32;
   for (int i = 0; i < kTiles; ++i) {
     if (i == kT256 && s.form == MOE_FP8_WEIGHT_GRAD && !f32) continue;   // its two vectors of scales spill there
+    if (i == kT128x256 && f32) continue;   // 2.15 us, two pairs of 128 x 128 2.00
     const TileCost& c = kCost[i];
     const int64_t tiles = ceil_div(rows, c.bm) * ceil_div(s.n, c.bn);
     for (int want = 1; want <= 16 && (want == 1 || want * 2 <= kb); ++want) {
@@ -649,7 +649,7 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
       const float fill = total < at_once ? (float)total / at_once : 1.0f;
       float us = 5.0f + (float)ceil_div(total, at_once) * per * (f32 ? c.step_f32 : c.step) * (0.72f + 0.28f * fill);
       if (splits > 1) us += 3.5f + (float)splits * rows * s.n * 8 / 8e6f;
-      if ((i == 0 && want == 1) || us < best.us || best.us == 0.0f)
+      if (best.us == 0.0f || us < best.us)
         best = Plan{rows, 0, (Tile)i, splits, per, us};
     }
   }
@@ -694,9 +694,18 @@ template <int MB, bool EXACT>
 hipError_t launch_rows(const MatmulArgs& g, hipStream_t st) {
   const dim3 grid((unsigned)(g.n / 16)), block(kRowWaves * 64);
   const int each = (int)ceil_div(g.k / kBK, kRowWaves);   // K blocks of a wavefront: all in flight at once if they fit
-  if (each > 4 && MB == 1) hipLaunchKernelGGL((matmul_rows_kernel<MB, 8, EXACT>), grid, block, 0, st, g);
-  else if (each > 2) hipLaunchKernelGGL((matmul_rows_kernel<MB, 4, EXACT>), grid, block, 0, st, g);
-  else hipLaunchKernelGGL((matmul_rows_kernel<MB, 2, EXACT>), grid, block, 0, st, g);
+  if constexpr (MB == 1) {
+    if (each > 4) {
+      hipLaunchKernelGGL((matmul_rows_kernel<1, 8, EXACT>), grid, block, 0, st, g);
+      return hipGetLastError();
+    }
+    if (each > 2) {
+      hipLaunchKernelGGL((matmul_rows_kernel<1, 4, EXACT>), grid, block, 0, st, g);
+      return hipGetLastError();
+    }
+  }
+  // (two blocks of rows come with k <= 2048 only: no wavefront has more than two K blocks)
+  hipLaunchKernelGGL((matmul_rows_kernel<MB, 2, EXACT>), grid, block, 0, st, g);
   return hipGetLastError();
 }
 
@@ -710,10 +719,11 @@ hipError_t launch_form(const MatmulArgs& g, const Plan& p, hipStream_t st) {
     case kT256:
       if constexpr (FORM != MOE_FP8_WEIGHT_GRAD || EXACT) return launch_tile<FORM, EXACT, 256, 256, 2, 4, 2>(g, p.splits, st);
       return hipErrorInvalidValue;   // never planned
-    case kT128x256: return launch_tile<FORM, EXACT, 128, 256, 2, 4, 3>(g, p.splits, st);
+    case kT128x256:
+      if constexpr (!EXACT) return launch_tile<FORM, EXACT, 128, 256, 2, 4, 3>(g, p.splits, st);
+      return hipErrorInvalidValue;   // never planned: two of 128 x 128 are done sooner
     case kT128: return launch_tile<FORM, EXACT, 128, 128, 2, 4, 4>(g, p.splits, st);
     case kT128Pair: return launch_tile<FORM, EXACT, 128, 128, 2, 2, 2>(g, p.splits, st);
-    case kT64x128: return launch_tile<FORM, EXACT, 64, 128, 2, 2, 4>(g, p.splits, st);
     default: return launch_tile<FORM, EXACT, 64, 64, 2, 2, 4>(g, p.splits, st);
   }
 }

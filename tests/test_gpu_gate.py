@@ -88,6 +88,23 @@ def test_against_float64(case):
     check(make(T, N, K, softmax, G, TG, top2, renorm, bias, bf16, scale), logits, b, softmax, G, TG, top2, renorm, scale)
 
 
+@pytest.mark.parametrize("K", [5, 16, 17, 30])
+@pytest.mark.parametrize("N,G", [(16, 1), (30, 1), (64, 1), (117, 1), (256, 1), (500, 1), (63, 9), (120, 5), (252, 9), (511, 7)])
+def test_every_layout_of_a_token_on_lanes(N, G, K):
+    """Experts a lane and lanes a token, groups of whole lanes and others, both types and both scores."""
+    if K > N // G * max(1, G // 2):
+        K = N // G * max(1, G // 2)
+    for softmax in (False, True):
+        for renorm in (False, True):
+            for bf16 in (False, True):
+                g = torch.Generator("cuda").manual_seed(N + K)
+                logits = (1.5 * torch.randn(40, N, device="cuda", generator=g)).clamp(-6, 6)
+                logits = logits.bfloat16() if bf16 else logits
+                b = (0.3 / N if softmax else 0.1) * torch.randn(N, device="cuda", generator=g)
+                args = softmax, G, max(1, G // 2), True, renorm
+                check(make(40, N, K, *args, True, bf16, 1.0), logits, b, *args, 1.0)
+
+
 @pytest.mark.parametrize("softmax", [False, True])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_masked_experts_and_empty_rows(softmax, renorm):

@@ -72,6 +72,45 @@ def test_against_float64(size, form, f32):
     check(product(form, *size, *ops, f32), form, *ops, f32)
 
 
+# every tile, alone and with the contraction split, and rows left over from whole tiles
+LARGER = [("forward", False, 1, 16, 2176), ("forward", True, 1, 16, 2432), ("forward", False, 25, 16, 2176),
+          ("forward", True, 25, 16, 2304), ("forward", False, 2710, 752, 128), ("forward", True, 775, 2512, 128),
+          ("forward", False, 2783, 2848, 1024), ("forward", True, 1695, 2576, 128), ("forward", True, 2213, 928, 2176),
+          ("forward", False, 1537, 2624, 128), ("forward", False, 2987, 2800, 256), ("forward", True, 2696, 2800, 256),
+          ("forward", True, 1690, 1184, 1408), ("forward", False, 7319, 2208, 768),
+          ("input_grad", False, 703, 2992, 128), ("input_grad", True, 670, 2992, 128),
+          ("input_grad", False, 2707, 2944, 1280), ("input_grad", True, 2325, 1824, 128),
+          ("input_grad", True, 1162, 1760, 2304), ("input_grad", False, 1799, 2272, 128),
+          ("input_grad", False, 2949, 3040, 1280), ("input_grad", True, 2847, 2912, 128), ("input_grad", False, 1, 16, 2816),
+          ("input_grad", True, 11002, 144, 3456), ("input_grad", False, 2428, 6880, 640),
+          ("weight_grad", False, 2345, 864, 128), ("weight_grad", True, 671, 3040, 128),
+          ("weight_grad", False, 2738, 2832, 896), ("weight_grad", True, 1722, 2448, 128),
+          ("weight_grad", True, 2718, 736, 2304), ("weight_grad", False, 2370, 1744, 128),
+          ("weight_grad", True, 2933, 3008, 1408), ("weight_grad", True, 4852, 3424, 384),
+          ("weight_grad", False, 1176, 6992, 1408), ("weight_grad", False, 1, 16, 2688)]
+
+
+@pytest.mark.parametrize("case", LARGER, ids=lambda c: "-".join(map(str, c)))
+def test_larger_sizes(case):
+    """As test_against_float64, the float64 product computed on the GPU."""
+    form, f32, m, n, k = case
+    a, sa, b, sb = operands(form, m, n, k, torch.Generator("cuda").manual_seed(m + n + k))
+    out = product(form, m, n, k, a, sa, b, sb, f32).double()
+    wide = lambda s, cols: s.double().repeat_interleave(128, 1)[:, :cols]  # noqa: E731
+    x, y = a.double() * wide(sa, k), wide(sb, b.shape[1])
+    if form != "weight_grad":
+        y = y.repeat_interleave(128, 0)[:b.shape[0]]
+    y = y * b.double()
+    y = y if form == "input_grad" else y.t().contiguous()
+    ref, size = x @ y, x.abs() @ y.abs()
+    err = (out - ref).abs()
+    if f32:
+        assert (err <= (k + 64) * 2.0 ** -24 * size).all()
+    else:
+        assert (err <= 2.0 ** -8 * ref.abs() + 2.0 ** -10 * size).all()
+        assert err.norm() <= 3e-3 * ref.norm()
+
+
 @pytest.mark.parametrize("f32", [False, True], ids=["bf16", "f32"])
 @pytest.mark.parametrize("form", list(FORMS))
 @pytest.mark.parametrize("m", [5, 200, 2100])
