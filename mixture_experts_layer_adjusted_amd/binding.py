@@ -125,15 +125,16 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-# torch's own short way to the current stream's handle (0.2 us against 2.7 for the Stream object), if it is there
+# torch's own short way to the current stream's handle (0.1 us against 2.7 for the Stream object), if it is there
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -208,7 +209,7 @@ def moe_workspace_size(shape: Shape) -> int:
 
 
 def _nbytes(t):
-    return t.numel() * t.element_size() if t is not None else 0
+    return 0 if t is None else t.nbytes
 
 
 def moe_route(shape, u, centroids, bias, topk_idx, topk_gate, expert_load, workspace, stream=None):

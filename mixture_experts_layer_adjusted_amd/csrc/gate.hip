@@ -15,21 +15,22 @@
 // L lanes hold a token, CPL neighbouring experts each (one load of up to 64 bytes), in lists of four sorted by key: a
 // round of the selection is the largest head over the lanes and one pop, and equal keys leave in index order (lowest
 // lane, lowest list, stable sort).  What bounds it is instructions, not bytes (a 64-lane round costs 30 for one token, a
-// 16-lane one 60 for four): T=16384, 256 experts in 8 groups: 18.1 us with 64 lanes, 10.7 with 16; one token 4.4 and 6.0 us.
+// 16-lane one 60 for four): T=16384, 256 experts in 8 groups: 19.4 us with 64 lanes, 10.4 with 16, 13.8 with 8; T=32768,
+// 64 experts: 19.5, 7.4 and 8.2; one token of 256 experts 4.4 with 64 and 5.6 with 16.
 #include "moe_internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
+constexpr int kWaves = 16;   // wavefronts of a workgroup at most
+constexpr int kMaxBlocks = 512;
 constexpr uint32_t kOut = 0u;       // key of an expert that is out (masked, in a closed group, or taken)
 constexpr uint32_t kNanKey = 1u;    // a NaN ranks below every number
 constexpr float kNegInf = -__builtin_inff();
 
-// larger score, larger key; -0 and +0 are one score
+// larger score, larger key (a score, a sum with a term that is no less than +0, is never -0)
 __device__ __forceinline__ uint32_t key_of(float c) {
-  const uint32_t b = __float_as_uint(c + 0.0f);
+  const uint32_t b = __float_as_uint(c);
   const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
   return c != c ? kNanKey : k;
 }
@@ -37,14 +38,13 @@ __device__ __forceinline__ float score_of(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? (key ^ 0x80000000u) : ~key);
 }
 
-// exp(x) from the 2^y instruction: y = x log2(e) rounded, and what the rounding (and the constant's) left out as a
-// factor 1 + r.  Within 2 units in the last place; results below 2^-126 are 0, infinities and NaN as they should be.
+// exp(x) from the 2^y instruction: y = x log2(e) rounded, and r = x - y ln(2) (ln(2) in two parts) as a factor 1 + r.
+// Within 2 units in the last place; results below 2^-126 are 0, infinities and NaN as they should be.
 __device__ __forceinline__ float exp_of(float x) {
   const float y = x * 1.44269502f;
-  float r = fmaf(x, 1.44269502f, -y);
-  r = fmaf(x, 1.92596299e-8f, r);
+  const float r = fmaf(y, 1.90465421e-9f, fmaf(y, -0.693147182f, x));
   const float e = __builtin_amdgcn_exp2f(y);
-  return fabsf(x) < 150.0f ? fmaf(e, r * 0.693147182f, e) : e;   // (e may be infinite, and r NaN)
+  return fabsf(x) < 150.0f ? fmaf(e, r, e) : e;   // (e may be infinite, and r NaN)
 }
 
 __device__ __forceinline__ float sigmoid_of(float l) { return __builtin_amdgcn_rcpf(1.0f + exp_of(-l)); }
@@ -99,55 +99,59 @@ __device__ __forceinline__ void store_run4(uint16_t* p, int left, const float (&
   }
 }
 
-// v from the lane that the DPP control names; lanes without one, or outside row_mask, get `other`
-template <int CTRL, int ROW_MASK>
-__device__ __forceinline__ uint32_t moved(uint32_t other, uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)other, (int)v, CTRL, ROW_MASK, 0xF, false);
-}
 // v from the lane that the DPP control names, where every lane has one (rotations, permutations)
 template <int CTRL>
 __device__ __forceinline__ uint32_t turned(uint32_t v) {
   return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
 
-// A reduction over the L lanes of a token, the result in each of them.  L = 16: four rotations of the 16-lane row
-// (row_ror:8, 4, 2, 1).  L = 32: then the other row by a shuffle.  L = 64: row shifts by 1, 2, 4, 8, row 0's and 2's
-// result into the row after (row_bcast:15), lane 31's into the upper rows (row_bcast:31), and lane 63's to all.
-// The order is fixed, so sums repeat to the bit.
+// A reduction over the L lanes of a token, the result in each of them: neighbours first, then pairs of them and so on
+// (quad_perm 1 0 3 2, quad_perm 2 3 0 1, row_half_mirror, row_mirror, the odd rows, the upper half).  With sum_run the
+// order of a sum is that of its terms alone, however many lanes and registers they lie in.
 template <int L, typename Op>
-__device__ __forceinline__ uint32_t reduce(uint32_t v, uint32_t neutral, Op op) {
-  if constexpr (L == 64) {
-    v = op(v, moved<0x111, 0xF>(neutral, v));
-    v = op(v, moved<0x112, 0xF>(neutral, v));
-    v = op(v, moved<0x114, 0xF>(neutral, v));
-    v = op(v, moved<0x118, 0xF>(neutral, v));
-    v = op(v, moved<0x142, 0xA>(neutral, v));
-    v = op(v, moved<0x143, 0xC>(neutral, v));
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-  } else {
-    v = op(v, turned<0x128>(v));
-    v = op(v, turned<0x124>(v));
-    v = op(v, turned<0x122>(v));
-    v = op(v, turned<0x121>(v));
-    if constexpr (L == 32) v = op(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-    return v;
+__device__ __forceinline__ uint32_t reduce(uint32_t v, Op op) {
+  v = op(v, turned<0xB1>(v));
+  v = op(v, turned<0x4E>(v));
+  v = op(v, turned<0x141>(v));
+  v = op(v, turned<0x140>(v));
+  if constexpr (L >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(p[0], p[1]);
   }
+  if constexpr (L >= 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = op(p[0], p[1]);
+  }
+  return v;
 }
 template <int L>
 __device__ __forceinline__ uint32_t max_of(uint32_t v) {
-  return reduce<L>(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+  return reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
 template <int L>
 __device__ __forceinline__ float max_of(float v) {
-  return __uint_as_float(reduce<L>(__float_as_uint(v), __float_as_uint(kNegInf), [](uint32_t a, uint32_t b) {
+  return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
   }));
 }
 template <int L>
 __device__ __forceinline__ float sum_of(float v) {
-  return __uint_as_float(reduce<L>(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+  return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
     return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
   }));
+}
+
+// the sum of a lane's run, in the order of `reduce`
+template <int N>
+__device__ __forceinline__ float sum_run(const float (&v)[N]) {
+  float s[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) s[j] = v[j];
+#pragma unroll
+  for (int w = 1; w < N; w *= 2)
+#pragma unroll
+    for (int j = 0; j < N; j += 2 * w) s[j] += s[j + w];
+  return s[0];
 }
 
 struct GateArgs {
@@ -222,7 +226,7 @@ __device__ __forceinline__ bool group_open(uint32_t k1, uint32_t k2, const GateA
 
 // `per`: lanes of a group where groups are whole lanes (0: they are not; 64 lanes only)
 template <int CPL, int L, typename TL, bool SOFTMAX>
-__global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int lanes_log2) {
+__global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, int lanes_log2) {
   constexpr int kTokens = 64 / L;                    // tokens of a wavefront
   constexpr int kLists = (CPL + 3) / 4, kLen = CPL < 4 ? CPL : 4;
   __shared__ int32_t hist[kMaxRouted];
@@ -231,7 +235,8 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
   const int tid = threadIdx.x, wl = tid & 63, lane = wl & (L - 1), slot = wl / L;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int N = a.N, K = a.K;
-  for (int e = tid; e < N; e += kThreads) hist[e] = 0;
+  const int threads = blockDim.x;
+  for (int e = tid; e < N; e += threads) hist[e] = 0;
   const bool limited = a.TG < a.G;
   const int first = lane * CPL, left = N - first;
   float bias[CPL];   // -inf past the last expert
@@ -244,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
   // this lane's predecessors in its token, as bits of the ballot's half
   const uint32_t before = L == 64 ? 0u : ((1u << lane) - 1u) << (wl & (32 - L));
   __syncthreads();
-  const int64_t per_block = (int64_t)kWaves * kTokens;
+  const int64_t per_block = threads / L;
   for (int64_t t0 = (int64_t)blockIdx.x * per_block + wave * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * per_block) {
     const bool real = t0 + slot < a.T;   // (several tokens a wavefront: the last one may have fewer)
     const int64_t t = real ? t0 + slot : t0;
@@ -263,14 +268,9 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
         top = max_of<L>(top);
         if (top == kNegInf) top = 0.0f;
 #pragma unroll
-        for (int j = 0; j < CPL; ++j) {
-          s[j] = exp_of(l[j] - top);
-          total += s[j];
-        }
-        total = sum_of<L>(total);
+        for (int j = 0; j < CPL; ++j) s[j] = exp_of(l[j] - top);
+        total = sum_of<L>(sum_run<CPL>(s));
         total = total == 0.0f ? 0.0f : 1.0f / total;   // 0: every expert masked
-#pragma unroll
-        for (int j = 0; j < CPL; ++j) s[j] *= total;
       } else {
 #pragma unroll
         for (int j = 0; j < CPL; ++j) s[j] = sigmoid_of(l[j]);
@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
             continue;
           }
           const int i = 4 * q + j;
-          float c = s[i] + bias[i];
+          float c = SOFTMAX ? fmaf(s[i], total, bias[i]) : s[i] + bias[i];
           c = l[i] == kNegInf ? kNegInf : c;   // (scores are finite: a bias of -inf leaves -inf too)
           const uint32_t k = key_of(c);
           key[q][j] = c == kNegInf ? kOut : k;
@@ -392,7 +392,6 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
       }
       most = fmaxf(most, v[h]);
     }
-    float sum = 0.0f;
     if (SOFTMAX && a.renorm) {   // over the picks alone, so that no picked score has underflowed
       most = max_of<L>(most);
       if (most == kNegInf) most = 0.0f;
@@ -404,10 +403,12 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
       else
         g[h] = sigmoid_of(v[h]);
       if (e[h] < 0) g[h] = 0.0f;
-      sum += g[h];
     }
-    if (a.renorm) {
-      sum = sum_of<L>(sum);
+    if (a.renorm) {   // (picks are 32 at most: two runs of 16 lanes, or one of 32)
+      float part[kHalves];
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) part[h] = sum_of<kHalves == 2 ? 16 : 32>(g[h]);
+      const float sum = sum_run<kHalves>(part);
 #pragma unroll
       for (int h = 0; h < kHalves; ++h) g[h] = sum == 0.0f ? 0.0f : g[h] / sum;
     }
@@ -422,11 +423,11 @@ __global__ void __launch_bounds__(kThreads) gate_kernel(GateArgs a, int per, int
   }
   if (!a.counts) return;
   __syncthreads();
-  for (int e = tid; e < N; e += kThreads) a.counts[(int64_t)blockIdx.x * N + e] = hist[e];
+  for (int e = tid; e < N; e += threads) a.counts[(int64_t)blockIdx.x * N + e] = hist[e];
 }
 
 // load[e] = sum over the workgroups of counts[w, e]: 64 experts per workgroup, its wavefronts every 16th row
-__global__ void __launch_bounds__(kThreads) gate_load_kernel(const int32_t* __restrict__ counts, int rows, int N,
+__global__ void __launch_bounds__(kWaves * 64) gate_load_kernel(const int32_t* __restrict__ counts, int rows, int N,
                                                              int32_t* __restrict__ load) {
   __shared__ int32_t part[kWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -567,20 +568,25 @@ __global__ void __launch_bounds__(kBwdThreads) gate_bwd_kernel(GateBwdArgs a) {
 }
 
 // How a call's tokens lie on lanes: 16 lanes a token (32 above 256 experts), or 64 for groups that do not fall on a power
-// of two of whole lanes.  Not by the number of tokens: a token's sums, and so its gates, are the same in every batch.
+// of two of whole lanes, and for up to four tokens, where a token's own time counts (one token, 256 experts: 4.4 us
+// against 5.6).  Sums do not depend on it, so a token's gates are the same in every batch.  Workgroups are small while
+// kMaxBlocks of them hold every token, and so reach more CUs (T=4096, 256 experts: 8.9 us against 13.1).
 struct GateLanes {
   int lanes, cpl;
-  int per;   // lanes of a group, 0 where groups are not whole lanes
+  int per;     // lanes of a group, 0 where groups are not whole lanes
+  int waves;   // of a workgroup
 };
 GateLanes lanes_of(const moe_gate_config& c) {
   auto with = [&](int lanes) {
-    GateLanes g{lanes, 1, 0};
+    GateLanes g{lanes, 1, 0, 4};
     while (g.cpl * lanes < c.n_routed) g.cpl *= 2;
     const int gs = c.n_routed / c.n_groups;
     const int per = gs % g.cpl == 0 ? gs / g.cpl : 0;
     if (per > 0 && (per & (per - 1)) == 0) g.per = per;
+    if (c.tokens > kMaxBlocks * 4 * (64 / lanes)) g.waves = kWaves;
     return g;
   };
+  if (c.tokens <= 4 && c.n_routed > 64) return with(64);
   const GateLanes few = with(c.n_routed <= 256 ? 16 : 32);
   const bool limited = c.topk_groups < c.n_groups;
   return !limited || few.per > 0 ? few : with(64);
@@ -590,7 +596,7 @@ template <typename TL, bool SOFTMAX>
 hipError_t gate_forward_t(const GateArgs& a, const GateLanes& g, int lanes_log2, unsigned grid, hipStream_t st) {
 #define MOE_GATE_CASE(C, L)                                                                                            \
   case L * 100 + C:                                                                                                    \
-    hipLaunchKernelGGL((gate_kernel<C, L, TL, SOFTMAX>), dim3(grid), dim3(kThreads), 0, st, a, g.per, lanes_log2);      \
+    hipLaunchKernelGGL((gate_kernel<C, L, TL, SOFTMAX>), dim3(grid), dim3(g.waves * 64), 0, st, a, g.per, lanes_log2);      \
     break
   switch (g.lanes * 100 + g.cpl) {
     MOE_GATE_CASE(1, 16);
@@ -639,7 +645,8 @@ hipError_t gate_backward_l(const GateBwdArgs& a, bool softmax, hipStream_t st) {
 }  // namespace
 
 int64_t gate_blocks(const moe_gate_config& c) {
-  return std::min<int64_t>(ceil_div(c.tokens, kWaves * (64 / lanes_of(c).lanes)), 512);
+  const GateLanes g = lanes_of(c);
+  return std::min<int64_t>(ceil_div(c.tokens, g.waves * (64 / g.lanes)), kMaxBlocks);
 }
 
 hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float* bias, int32_t* idx, float* gate,
@@ -665,7 +672,7 @@ hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float
     err = f32 ? gate_forward_t<float, false>(a, g, lanes_log2, grid, st)
               : gate_forward_t<uint16_t, false>(a, g, lanes_log2, grid, st);
   if (err != hipSuccess || !load || grid == 1) return err;
-  hipLaunchKernelGGL(gate_load_kernel, dim3((unsigned)ceil_div(c.n_routed, 64)), dim3(kThreads), 0, st, counts, (int)grid,
+  hipLaunchKernelGGL(gate_load_kernel, dim3((unsigned)ceil_div(c.n_routed, 64)), dim3(kWaves * 64), 0, st, counts, (int)grid,
                      c.n_routed, load);
   return hipGetLastError();
 }

@@ -246,3 +246,17 @@ def test_replayed_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(want, (idx, gate, load, d)))
+
+
+@pytest.mark.parametrize("softmax,renorm,K", [(False, True, 8), (True, True, 19), (True, False, 8)])
+@pytest.mark.parametrize("N,G", [(70, 1), (256, 8), (512, 4), (288, 3)])
+def test_a_token_alone_and_in_any_batch(N, G, softmax, renorm, K):
+    """The same bits, whatever the number of lanes and of wavefronts that a call of this length takes."""
+    g = torch.Generator("cuda").manual_seed(N + K)
+    logits, bias = torch.randn(9001, N, device="cuda", generator=g), 0.01 * torch.randn(N, device="cuda", generator=g)
+    outs = []
+    for T in (1, 4, 5, 300, 9001):
+        idx, gate, _ = run(make(T, N, K, softmax, G, (G + 1) // 2, True, renorm), logits[:T], bias)
+        outs.append((T, idx, gate))
+    for T, idx, gate in outs[:-1]:
+        assert torch.equal(idx, outs[-1][1][:T]) and torch.equal(gate, outs[-1][2][:T])
