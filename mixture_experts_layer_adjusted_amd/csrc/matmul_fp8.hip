@@ -183,13 +183,21 @@ struct TileShape {
 // works on at a time, eight share a's rows and four b's, so each asks for an eighth and a quarter of the lines of the
 // stage after those in flight: one load of a wavefront, into LDS that nothing reads (237 -> 210 us; every tile asking
 // for all its lines gained nothing).  More stages do not need it.
-template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES>
-__global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g, int MT, int NT, int splits, int chunk) {
+//
+// SETS = 2: where there is no second workgroup for a CU, a second set of wavefronts takes the second half of the K blocks
+// in an LDS of its own, and the first adds its sums at the end (77 x 7168 x 2048 to fp32: 13.7 us -> 11.7;
+// 1000 x 2816 x 2048: 26.2 -> 22.5; a bf16 input gradient 77 x 2048 x 7168: 14.6 -> 12.6).
+template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES, int SETS>
+__global__ void __launch_bounds__(WM * WN * 64 * SETS) matmul_tile_kernel(MatmulArgs g, int MT, int NT, int splits, int chunk) {
   constexpr bool KN = FORM == MOE_FP8_INPUT_GRAD, ROWS = FORM == MOE_FP8_WEIGHT_GRAD;
   using S = TileShape<FORM, BM, BN, WM, WN, STAGES>;
   constexpr int kMB = S::kMB, kNB = S::kNB;
-  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t all_lds[];
   constexpr int kSpan = S::kSpan, kPart = S::kPart;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int first_wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int set = SETS == 1 ? 0 : first_wave / S::kWaves, wave = first_wave - set * S::kWaves;
+  uint8_t* const lds = all_lds + set * S::kLds;
   uint8_t* const ascales = lds + S::kScales;
   uint8_t* const bscales = ascales + 3 * S::kAScale;
   // tiles of one slice after another, dealt to the XCDs in runs of `chunk`
@@ -198,11 +206,14 @@ __global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g,
   const int slice = (int)(Ls / (MT * NT)), L = (int)(Ls - (int64_t)slice * MT * NT);
   const int grp = L / (kGroupM * NT), gm = min(kGroupM, MT - grp * kGroupM), rem = L - grp * kGroupM * NT;
   const int m0 = (grp * kGroupM + rem % gm) * BM, n0 = rem / gm * BN;
-  const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int KB = g.k / kBK;
-  const int kb0 = slice * g.kb_per_split, nk = min(g.kb_per_split, KB - kb0);
+  int kb0 = slice * g.kb_per_split, nk = min(g.kb_per_split, KB - kb0);
+  const int meetings = nk > 0 ? 1 + (nk + SETS - 1) / SETS : 0;   // of the set with the most K blocks
+  if constexpr (SETS == 2) {
+    kb0 += set * ((nk + 1) / 2);
+    nk = (nk + 1 - set) / 2;
+  }
 
   // ---- where this lane's loads come from: 32-bit byte offsets from the tile's first row
   uint32_t aoff[S::kADma], boff[S::kBDma];
@@ -433,6 +444,31 @@ __global__ void __launch_bounds__(WM * WN * 64) matmul_tile_kernel(MatmulArgs g,
       if (kt < nk) group(kt, 0, even, odd);
     }
   }
+  if constexpr (SETS == 2) {
+    for (int i = nk > 0 ? 1 + nk : 0; i < meetings; ++i) __builtin_amdgcn_s_barrier();
+    // the second set's sums, through its own part of LDS once nothing is on its way there
+    wait_counts<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    f32x4* const sums = reinterpret_cast<f32x4*>(all_lds + S::kLds) + wave * (kMB * kNB * 64) + lane;
+    static_assert(BM * BN * 4 <= S::kLds, "a tile's sums");
+    if (set == 1) {
+#pragma unroll
+      for (int i = 0; i < kMB; ++i)
+#pragma unroll
+        for (int j = 0; j < kNB; ++j) sums[(i * kNB + j) * 64] = acc[i][j];
+    }
+    wait_counts<0>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (set == 1) return;
+#pragma unroll
+    for (int i = 0; i < kMB; ++i)
+#pragma unroll
+      for (int j = 0; j < kNB; ++j) acc[i][j] += sums[(i * kNB + j) * 64];
+  }
 #pragma unroll
   for (int i = 0; i < kMB; ++i) {
     const int row = m0 + mrow + 16 * i + l16;
@@ -603,18 +639,18 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
 
 // ---- which kernel ----------------------------------------------------------------------------------------------
 
-// The tiles, and what one K block of one takes (us) with every CU at work, for bf16 and for fp32 outputs: measured over
-// 17 shapes from m = 40 to 8192, each with 1, 2, 4 and 7 slices.  (0: not built.)
-enum Tile { kT256, kT128x256, kT128, kT128Pair, kT64Pair, kTiles };
+// The tiles (Sets: two sets of wavefronts, each on half of the K blocks), and for bf16 and for fp32 outputs what a launch
+// of one takes apart from its K blocks and what a K block takes with every CU at work (us; 0: not built), fitted to
+// 138 shapes from 16 to 9000 rows with up to 8 slices: the choice is 1% slower than the best of them on average.
+enum Tile { kT256, kT128x256, kT128, kT128Pair, kT128Sets, kT64Pair, kT64Sets, kTiles };
 struct TileCost {
   int bm, bn, per_cu;   // workgroups of a CU at a time
-  float step, step_f32;
+  float base, step, base_f32, step_f32;
 };
-constexpr TileCost kCost[kTiles] = {{256, 256, 1, 1.85f, 3.72f},
-                                    {128, 256, 1, 1.10f, 0.0f},
-                                    {128, 128, 1, 0.65f, 1.42f},
-                                    {128, 128, 2, 1.27f, 2.00f},
-                                    {64, 64, 2, 0.40f, 0.69f}};
+constexpr TileCost kCost[kTiles] = {{256, 256, 1, 6.8f, 1.59f, 9.9f, 3.19f}, {128, 256, 1, 5.9f, 1.08f, 0.0f, 0.0f},
+                                    {128, 128, 1, 5.1f, 0.65f, 0.0f, 0.0f},  {128, 128, 2, 4.5f, 1.44f, 4.8f, 1.88f},
+                                    {128, 128, 1, 0.0f, 0.0f, 5.8f, 1.18f},  {64, 64, 2, 4.4f, 0.51f, 3.2f, 1.10f},
+                                    {64, 64, 1, 5.0f, 0.25f, 4.5f, 0.55f}};
 
 struct Plan {
   int rows;            // rows of a that the plan covers (from the first)
@@ -625,8 +661,7 @@ struct Plan {
 };
 
 // The plan for `rows` rows in one kernel (and the join): rounds of tiles over the CUs, a chip that is not full being up
-// to 28% faster, 5 us for a launch and a tile's start and end, and for slices 3.5 us and their sums' way to memory and
-// back.  kb / slices is 2 at least.
+// to 22% faster (38% where a CU has one workgroup in place of two), and for slices 2.3 us and their sums' way to memory and back.  kb / slices is 2 at least.
 Plan plan_one(const moe_matmul_shape& s, int rows) {
   const int kb = s.k / kBK;
   Plan best{rows, 0, kT64Pair, 1, kb, 0.0f};
@@ -639,16 +674,21 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
   const bool f32 = s.out_dtype == MOE_DTYPE_F32;
   for (int i = 0; i < kTiles; ++i) {
     if (i == kT256 && s.form == MOE_FP8_WEIGHT_GRAD && !f32) continue;   // its two vectors of scales spill there
-    if (i == kT128x256 && f32) continue;   // 2.15 us, two pairs of 128 x 128 2.00
     const TileCost& c = kCost[i];
+    const float step = f32 ? c.step_f32 : c.step;
+    if (step == 0.0f) continue;
+    // (two sets gain least in a bf16 forward, which is nearest to memory: 77 x 7168 x 2048 8.9 us without, 9.4 with;
+    // with 31 K blocks, 308 x 1680, 13.2 and 11.4)
+    const float base = f32 ? c.base_f32 : i == kT64Sets && s.form == MOE_FP8_FORWARD ? c.base + 2.0f : c.base;
+    const float faster = c.per_cu == 2 ? 0.38f : 0.22f;
     const int64_t tiles = ceil_div(rows, c.bm) * ceil_div(s.n, c.bn);
     for (int want = 1; want <= 16 && (want == 1 || want * 2 <= kb); ++want) {
       const int per = (int)ceil_div(kb, want), splits = per > 0 ? (int)ceil_div(kb, per) : 1;
       if (splits != want) continue;
       const int64_t total = tiles * splits, at_once = 256 * c.per_cu;
       const float fill = total < at_once ? (float)total / at_once : 1.0f;
-      float us = 5.0f + (float)ceil_div(total, at_once) * per * (f32 ? c.step_f32 : c.step) * (0.72f + 0.28f * fill);
-      if (splits > 1) us += 3.5f + (float)splits * rows * s.n * 8 / 8e6f;
+      float us = base + (float)ceil_div(total, at_once) * per * step * (1.0f - faster * (1.0f - fill));
+      if (splits > 1) us += 2.3f + (float)splits * rows * s.n * 8 / 4.2e6f;
       if (best.us == 0.0f || us < best.us)
         best = Plan{rows, 0, (Tile)i, splits, per, us};
     }
@@ -673,12 +713,12 @@ int plan_of(const moe_matmul_shape& s, Plan (&plans)[2]) {
   return n;
 }
 
-template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES>
+template <int FORM, bool EXACT, int BM, int BN, int WM, int WN, int STAGES, int SETS = 1>
 hipError_t launch_tile(const MatmulArgs& g, int splits, hipStream_t st) {
   using S = TileShape<FORM, BM, BN, WM, WN, STAGES>;
-  static_assert(S::kLds <= 163840, "LDS");
-  auto kern = &matmul_tile_kernel<FORM, EXACT, BM, BN, WM, WN, STAGES>;
-  const hipError_t err = ensure_dynamic_lds(reinterpret_cast<const void*>(kern), S::kLds);
+  static_assert(SETS * S::kLds <= 163840, "LDS");
+  auto kern = &matmul_tile_kernel<FORM, EXACT, BM, BN, WM, WN, STAGES, SETS>;
+  const hipError_t err = ensure_dynamic_lds(reinterpret_cast<const void*>(kern), SETS * S::kLds);
   if (err != hipSuccess) return err;
   const int64_t MT = ceil_div(g.m, BM), NT = ceil_div(g.n, BN);
   const int64_t total = MT * NT * splits;
@@ -686,7 +726,7 @@ hipError_t launch_tile(const MatmulArgs& g, int splits, hipStream_t st) {
   // an XCD's 32 CUs take neighbouring tiles; fewer at a time where there are not enough for every XCD
   const int chunk = (int)std::min<int64_t>(32, ceil_div(total, kXcds));
   const int64_t grid = ceil_div(total, kXcds * chunk) * (kXcds * chunk);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(S::kThreads), S::kLds, st, g, (int)MT, (int)NT, splits, chunk);
+  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(SETS * S::kThreads), SETS * S::kLds, st, g, (int)MT, (int)NT, splits, chunk);
   return hipGetLastError();
 }
 
@@ -721,9 +761,15 @@ hipError_t launch_form(const MatmulArgs& g, const Plan& p, hipStream_t st) {
       return hipErrorInvalidValue;   // never planned
     case kT128x256:
       if constexpr (!EXACT) return launch_tile<FORM, EXACT, 128, 256, 2, 4, 3>(g, p.splits, st);
-      return hipErrorInvalidValue;   // never planned: two of 128 x 128 are done sooner
-    case kT128: return launch_tile<FORM, EXACT, 128, 128, 2, 4, 4>(g, p.splits, st);
+      return hipErrorInvalidValue;
+    case kT128:
+      if constexpr (!EXACT) return launch_tile<FORM, EXACT, 128, 128, 2, 4, 4>(g, p.splits, st);
+      return hipErrorInvalidValue;
     case kT128Pair: return launch_tile<FORM, EXACT, 128, 128, 2, 2, 2>(g, p.splits, st);
+    case kT128Sets:
+      if constexpr (EXACT) return launch_tile<FORM, EXACT, 128, 128, 2, 2, 2, 2>(g, p.splits, st);
+      return hipErrorInvalidValue;
+    case kT64Sets: return launch_tile<FORM, EXACT, 64, 64, 2, 2, 4, 2>(g, p.splits, st);
     default: return launch_tile<FORM, EXACT, 64, 64, 2, 2, 4>(g, p.splits, st);
   }
 }

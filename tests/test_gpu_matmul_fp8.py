@@ -87,7 +87,20 @@ LARGER = [("forward", False, 1, 16, 2176), ("forward", True, 1, 16, 2432), ("for
           ("weight_grad", False, 2738, 2832, 896), ("weight_grad", True, 1722, 2448, 128),
           ("weight_grad", True, 2718, 736, 2304), ("weight_grad", False, 2370, 1744, 128),
           ("weight_grad", True, 2933, 3008, 1408), ("weight_grad", True, 4852, 3424, 384),
-          ("weight_grad", False, 1176, 6992, 1408), ("weight_grad", False, 1, 16, 2688)]
+          ("weight_grad", False, 1176, 6992, 1408), ("weight_grad", False, 1, 16, 2688),
+          ("forward", False, 1, 16, 5120), ("forward", False, 67, 4992, 5120), ("forward", False, 69, 4080, 2432),
+          ("forward", False, 772, 5920, 768), ("forward", True, 1, 16, 4864), ("forward", True, 132, 752, 3584),
+          ("forward", True, 133, 5504, 2816), ("forward", True, 3443, 2528, 896), ("forward", True, 68, 4560, 3200),
+          ("forward", True, 71, 4224, 3968), ("input_grad", False, 199, 4368, 4992),
+          ("input_grad", False, 21, 2128, 3584), ("input_grad", False, 2375, 1680, 896),
+          ("input_grad", True, 1283, 6256, 384), ("input_grad", True, 3074, 2816, 896),
+          ("input_grad", True, 44, 3936, 2048), ("input_grad", True, 65, 4448, 3968),
+          ("input_grad", True, 65, 5024, 3200), ("weight_grad", False, 12, 5040, 2688),
+          ("weight_grad", False, 8366, 80, 4224), ("weight_grad", True, 147, 1200, 2048),
+          ("weight_grad", True, 65, 4336, 3584), ("weight_grad", True, 66, 4144, 3968),
+          # two sets of wavefronts, the last slice a single K block
+          ("input_grad", False, 25, 2272, 4736), ("forward", True, 65, 2736, 5248), ("weight_grad", False, 28, 2000, 5504),
+          ("weight_grad", True, 384, 336, 4736), ("input_grad", True, 186, 704, 4736)]
 
 
 @pytest.mark.parametrize("case", LARGER, ids=lambda c: "-".join(map(str, c)))
