@@ -128,11 +128,15 @@ template <int L>
 __device__ __forceinline__ uint32_t max_of(uint32_t v) {
   return reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
 }
+// (as integers of the same order: a float maximum would quiet each operand first.  A NaN is the largest or ignored: what
+// uses the maximum of a row with one has no number anyway.)
 template <int L>
 __device__ __forceinline__ float max_of(float v) {
-  return __uint_as_float(reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
-  }));
+  const int32_t b = __float_as_int(v);
+  const uint32_t m = reduce<L>((uint32_t)(b ^ ((b >> 31) & 0x7FFFFFFF)),
+                               [](uint32_t a, uint32_t b) { return (uint32_t)max((int32_t)a, (int32_t)b); });
+  const int32_t r = (int32_t)m;
+  return __int_as_float(r ^ ((r >> 31) & 0x7FFFFFFF));
 }
 template <int L>
 __device__ __forceinline__ float sum_of(float v) {
@@ -246,8 +250,6 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
 #pragma unroll
     for (int j = 0; j < CPL; ++j) bias[j] = j < left ? 0.0f : kNegInf;
   }
-  // this lane's predecessors in its token, as bits of the ballot's half
-  const uint32_t before = L == 64 ? 0u : ((1u << lane) - 1u) << (wl & (32 - L));
   __syncthreads();
   const int64_t per_block = threads / L;
   for (int64_t t0 = (int64_t)blockIdx.x * per_block + wave * kTokens; t0 < a.T; t0 += (int64_t)gridDim.x * per_block) {
@@ -270,7 +272,7 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
 #pragma unroll
         for (int j = 0; j < CPL; ++j) s[j] = exp_of(l[j] - top);
         total = sum_of<L>(sum_run<CPL>(s));
-        total = total == 0.0f ? 0.0f : 1.0f / total;   // 0: every expert masked
+        total = total == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(total);   // (1 ulp) 0: every expert masked
       } else {
 #pragma unroll
         for (int j = 0; j < CPL; ++j) s[j] = sigmoid_of(l[j]);
@@ -347,21 +349,17 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
 #pragma unroll
       for (int q = 1; q < kLists; ++q) head = max(head, key[q][0]);
       const uint32_t best = max_of<L>(head);
-      if (L == 64 ? best == kOut : __ballot(best != kOut) == 0) break;
-      const uint64_t at = __ballot(head == best && best != kOut);
-      bool mine;
-      if constexpr (L == 64) {
-        mine = wl == __builtin_ctzll(at);
-      } else {
-        const uint32_t half = wl < 32 ? (uint32_t)at : (uint32_t)(at >> 32);
-        mine = head == best && best != kOut && (half & before) == 0;
-      }
-      if (mine) {   // the first list whose head it is
+      // of the lanes that have it the token's lowest: the lowest set bit in each L bits (a field with its top bit set
+      // less one, without a borrow from the next)
+      const uint64_t at = __builtin_amdgcn_ballot_w64(head == best) & __builtin_amdgcn_ballot_w64(best != kOut);
+      constexpr uint64_t kLow = L == 16 ? 0x0001000100010001ull : L == 32 ? 0x0000000100000001ull : 1ull;
+      const uint64_t lowest = at & ~((at | kLow << (L - 1)) - kLow);
+      if (__builtin_amdgcn_inverse_ballot_w64(lowest)) {   // the first list whose head it is
         bool found = false;
         uint32_t j = 0;
 #pragma unroll
         for (int q = 0; q < kLists; ++q) {
-          const bool here = !found && key[q][0] == best;
+          const bool here = !found && (q == kLists - 1 || key[q][0] == best);
           found = found || here;
           j = here ? order[q] & 0xFFu : j;
           order[q] = here ? order[q] >> 8 : order[q];
@@ -374,14 +372,18 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
     __builtin_amdgcn_wave_barrier();
     // the picks' gates, from their logits again
     constexpr int kHalves = L == 16 ? 2 : 1;   // 16 lanes hold up to 32 picks
+    const int halves = kHalves == 2 && K > L ? 2 : 1;
     float g[kHalves], v[kHalves];
     int e[kHalves];
     float most = kNegInf;
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      e[h] = lane + L * h < K ? won[wave][slot][lane + L * h] : -1;
+      e[h] = -1;
       v[h] = kNegInf;
-      if constexpr (CPL <= 4) {   // from the lane that has it
+      g[h] = 0.0f;
+      if (h >= halves) continue;
+      if (lane + L * h < K) e[h] = won[wave][slot][lane + L * h];
+      if constexpr (L == 64 && CPL <= 4) {   // from the lane that has it: sooner, though more instructions
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
           const float o = __shfl(l[j], max(e[h], 0) / CPL, L);
@@ -398,23 +400,25 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
     }
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
-      if constexpr (SOFTMAX)   // (total is NaN where a NaN or an infinity leaves the row without a number)
-        g[h] = a.renorm ? (total != total ? total : exp_of(v[h] - most)) : exp_of(v[h] - top) * total;
-      else
+      if (h >= halves) continue;
+      if constexpr (SOFTMAX) {   // (total is NaN where a NaN or an infinity leaves the row without a number)
+        g[h] = exp_of(v[h] - (a.renorm ? most : top));
+        g[h] = a.renorm ? (total != total ? total : g[h]) : g[h] * total;
+      } else {
         g[h] = sigmoid_of(v[h]);
+      }
       if (e[h] < 0) g[h] = 0.0f;
     }
     if (a.renorm) {   // (picks are 32 at most: two runs of 16 lanes, or one of 32)
-      float part[kHalves];
+      float sum = sum_of<kHalves == 2 ? 16 : 32>(g[0]);
+      if (halves == 2) sum += sum_of<16>(g[kHalves - 1]);
 #pragma unroll
-      for (int h = 0; h < kHalves; ++h) part[h] = sum_of<kHalves == 2 ? 16 : 32>(g[h]);
-      const float sum = sum_run<kHalves>(part);
-#pragma unroll
-      for (int h = 0; h < kHalves; ++h) g[h] = sum == 0.0f ? 0.0f : g[h] / sum;
+      for (int h = 0; h < kHalves; ++h)
+        if (h < halves) g[h] = sum == 0.0f ? 0.0f : g[h] / sum;
     }
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
-      if (real && lane + L * h < K) {
+      if (h < halves && real && lane + L * h < K) {
         a.idx[t * K + lane + L * h] = e[h];
         a.gate[t * K + lane + L * h] = a.scale * g[h];
         if (e[h] >= 0) atomicAdd(&hist[e[h]], 1);
