@@ -15,8 +15,9 @@
 // L lanes hold a token, CPL neighbouring experts each (one load of up to 64 bytes), in lists of four sorted by key: a
 // round of the selection is the largest head over the lanes and one pop, and equal keys leave in index order (lowest
 // lane, lowest list, stable sort).  What bounds it is instructions, not bytes (a 64-lane round costs 30 for one token, a
-// 16-lane one 60 for four): T=16384, 256 experts in 8 groups: 19.4 us with 64 lanes, 10.4 with 16, 13.8 with 8; T=32768,
-// 64 experts: 19.5, 7.4 and 8.2; one token of 256 experts 4.4 with 64 and 5.6 with 16.
+// 16-lane one 50 for four): T=16384, 256 experts in 8 groups: 15.5 us with 64 lanes, 9.8 with 16; T=32768, 64 experts:
+// 16.6 and 6.2; one token of 256 experts 3.9 and 5.0.  Fewer lanes (8, 4) lose what they save in rounds to their longer
+// runs.
 #include "moe_internal.h"
 
 namespace moe {
@@ -572,9 +573,9 @@ __global__ void __launch_bounds__(kBwdThreads) gate_bwd_kernel(GateBwdArgs a) {
 }
 
 // How a call's tokens lie on lanes: 16 lanes a token (32 above 256 experts), or 64 for groups that do not fall on a power
-// of two of whole lanes, and for up to four tokens, where a token's own time counts (one token, 256 experts: 4.4 us
-// against 5.6).  Sums do not depend on it, so a token's gates are the same in every batch.  Workgroups are small while
-// kMaxBlocks of them hold every token, and so reach more CUs (T=4096, 256 experts: 8.9 us against 13.1).
+// of two of whole lanes, and for up to four tokens, where a token's own time counts (one token, 256 experts: 3.9 us
+// against 5.0).  Sums do not depend on it, so a token's gates are the same in every batch.  Workgroups are small while
+// kMaxBlocks of them hold every token, and so reach more CUs (T=4096, 256 experts: 8.8 us against 12.6).
 struct GateLanes {
   int lanes, cpl;
   int per;     // lanes of a group, 0 where groups are not whole lanes
@@ -600,8 +601,7 @@ template <typename TL, bool SOFTMAX>
 hipError_t gate_forward_t(const GateArgs& a, const GateLanes& g, int lanes_log2, unsigned grid, hipStream_t st) {
 #define MOE_GATE_CASE(C, L)                                                                                            \
   case L * 100 + C:                                                                                                    \
-    hipLaunchKernelGGL((gate_kernel<C, L, TL, SOFTMAX>), dim3(grid), dim3(g.waves * 64), 0, st, a, g.per, lanes_log2);      \
-    break
+    return launch_kernel(gate_kernel<C, L, TL, SOFTMAX>, dim3(grid), dim3(g.waves * 64), 0, st, a, g.per, lanes_log2)
   switch (g.lanes * 100 + g.cpl) {
     MOE_GATE_CASE(1, 16);
     MOE_GATE_CASE(2, 16);
@@ -613,10 +613,9 @@ hipError_t gate_forward_t(const GateArgs& a, const GateLanes& g, int lanes_log2,
     MOE_GATE_CASE(2, 64);
     MOE_GATE_CASE(4, 64);
     MOE_GATE_CASE(8, 64);
-    default: return hipErrorInvalidValue;
   }
 #undef MOE_GATE_CASE
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 template <int L, typename TL, bool SOFTMAX, bool DENSE>
@@ -625,13 +624,13 @@ hipError_t gate_backward_t(const GateBwdArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(a.T, per_block), 4096);
   const size_t lds = (size_t)per_block * ((a.N + 3) / 4) * 16;   // at most 32 KB
 #define MOE_GATE_CASE(C) \
-  hipLaunchKernelGGL((gate_bwd_kernel<L, C, TL, SOFTMAX, DENSE>), dim3(grid), dim3(kBwdThreads), lds, st, a)
+  return launch_kernel(gate_bwd_kernel<L, C, TL, SOFTMAX, DENSE>, dim3(grid), dim3(kBwdThreads), lds, st, a)
   if (a.N <= 4 * L) MOE_GATE_CASE(1);
-  else if (a.N <= 8 * L) MOE_GATE_CASE(2);
-  else if (L == 32 || a.N <= 16 * L) MOE_GATE_CASE(4);   // (512 experts at most)
-  else if constexpr (L == 16) MOE_GATE_CASE(8);
+  if (a.N <= 8 * L) MOE_GATE_CASE(2);
+  if (L == 32 || a.N <= 16 * L) MOE_GATE_CASE(4);   // (512 experts at most)
+  if constexpr (L == 16) MOE_GATE_CASE(8);
 #undef MOE_GATE_CASE
-  return hipGetLastError();
+  return hipErrorInvalidValue;
 }
 
 template <typename TL>
@@ -657,8 +656,7 @@ hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float
                        int32_t* load, int32_t* counts, hipStream_t st) {
   if (c.tokens == 0) {
     if (!load) return hipSuccess;
-    hipLaunchKernelGGL(gate_zero_kernel, dim3((unsigned)ceil_div(c.n_routed, 256)), dim3(256), 0, st, load, c.n_routed);
-    return hipGetLastError();
+    return launch_kernel(gate_zero_kernel, dim3((unsigned)ceil_div(c.n_routed, 256)), dim3(256), 0, st, load, c.n_routed);
   }
   const unsigned grid = (unsigned)gate_blocks(c);
   const GateArgs a{logits, c.logits_ld ? c.logits_ld : c.n_routed, bias, c.tokens, c.n_routed, c.top_k, c.n_groups,
@@ -676,9 +674,8 @@ hipError_t launch_gate(const moe_gate_config& c, const void* logits, const float
     err = f32 ? gate_forward_t<float, false>(a, g, lanes_log2, grid, st)
               : gate_forward_t<uint16_t, false>(a, g, lanes_log2, grid, st);
   if (err != hipSuccess || !load || grid == 1) return err;
-  hipLaunchKernelGGL(gate_load_kernel, dim3((unsigned)ceil_div(c.n_routed, 64)), dim3(kWaves * 64), 0, st, counts, (int)grid,
+  return launch_kernel(gate_load_kernel, dim3((unsigned)ceil_div(c.n_routed, 64)), dim3(kWaves * 64), 0, st, counts, (int)grid,
                      c.n_routed, load);
-  return hipGetLastError();
 }
 
 hipError_t launch_gate_backward(const moe_gate_config& c, const void* logits, const int32_t* idx, const float* d_gate,

@@ -666,7 +666,7 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
   const int kb = s.k / kBK;
   Plan best{rows, 0, kT64Pair, 1, kb, 0.0f};
   if (s.form == MOE_FP8_FORWARD && (rows <= 16 || (rows <= 32 && s.k <= 2048))) {
-    // straight from memory (1 x 4096 x 7168: 7.3 us against 11 with the best tile; 17 x 1024 x 1024: 6.2 against 7.6)
+    // straight from memory (1 x 4096 x 7168: 7.3 us against 10.6 with the best tile; 17 x 1024 x 1024: 4.4 against 5.9)
     best.rows_mb = rows <= 16 ? 1 : 2;
     best.us = 5.0f + (float)s.n * s.k / 1e7f;
     return best;
@@ -726,8 +726,7 @@ hipError_t launch_tile(const MatmulArgs& g, int splits, hipStream_t st) {
   // an XCD's 32 CUs take neighbouring tiles; fewer at a time where there are not enough for every XCD
   const int chunk = (int)std::min<int64_t>(32, ceil_div(total, kXcds));
   const int64_t grid = ceil_div(total, kXcds * chunk) * (kXcds * chunk);
-  hipLaunchKernelGGL(kern, dim3((unsigned)grid), dim3(SETS * S::kThreads), SETS * S::kLds, st, g, (int)MT, (int)NT, splits, chunk);
-  return hipGetLastError();
+  return launch_kernel(kern, dim3((unsigned)grid), dim3(SETS * S::kThreads), SETS * S::kLds, st, g, (int)MT, (int)NT, splits, chunk);
 }
 
 template <int MB, bool EXACT>
@@ -736,17 +735,14 @@ hipError_t launch_rows(const MatmulArgs& g, hipStream_t st) {
   const int each = (int)ceil_div(g.k / kBK, kRowWaves);   // K blocks of a wavefront: all in flight at once if they fit
   if constexpr (MB == 1) {
     if (each > 4) {
-      hipLaunchKernelGGL((matmul_rows_kernel<1, 8, EXACT>), grid, block, 0, st, g);
-      return hipGetLastError();
+      return launch_kernel(matmul_rows_kernel<1, 8, EXACT>, grid, block, 0, st, g);
     }
     if (each > 2) {
-      hipLaunchKernelGGL((matmul_rows_kernel<1, 4, EXACT>), grid, block, 0, st, g);
-      return hipGetLastError();
+      return launch_kernel(matmul_rows_kernel<1, 4, EXACT>, grid, block, 0, st, g);
     }
   }
   // (two blocks of rows come with k <= 2048 only: no wavefront has more than two K blocks)
-  hipLaunchKernelGGL((matmul_rows_kernel<MB, 2, EXACT>), grid, block, 0, st, g);
-  return hipGetLastError();
+  return launch_kernel(matmul_rows_kernel<MB, 2, EXACT>, grid, block, 0, st, g);
 }
 
 template <int FORM, bool EXACT>
@@ -816,9 +812,8 @@ hipError_t launch_matmul_fp8(const moe_matmul_shape& s, const uint8_t* a, const 
                                                     : launch_product<MOE_FP8_WEIGHT_GRAD>(g, p, st);
     if (err == hipSuccess && p.splits > 1) {
       const int64_t quads = (int64_t)p.rows * s.n / 4;
-      hipLaunchKernelGGL(matmul_join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(quads, 256), 4096)), dim3(256), 0, st,
-                         g, p.splits);
-      err = hipGetLastError();
+      err = launch_kernel(matmul_join_kernel, dim3((unsigned)std::min<int64_t>(ceil_div(quads, 256), 4096)), dim3(256), 0, st,
+                          g, p.splits);
     }
     if (err != hipSuccess) return err;
     row += p.rows;
@@ -827,9 +822,8 @@ hipError_t launch_matmul_fp8(const moe_matmul_shape& s, const uint8_t* a, const 
 }
 
 hipError_t launch_quantize_act_t(int rows, int cols, const void* x, uint8_t* codes, float* scales, hipStream_t st) {
-  hipLaunchKernelGGL(quant_act_t_kernel, dim3((unsigned)ceil_div(rows, 128), (unsigned)ceil_div(cols, 64)), dim3(256), 0, st,
+  return launch_kernel(quant_act_t_kernel, dim3((unsigned)ceil_div(rows, 128), (unsigned)ceil_div(cols, 64)), dim3(256), 0, st,
                      static_cast<const uint16_t*>(x), rows, cols, codes, scales);
-  return hipGetLastError();
 }
 
 }  // namespace moe

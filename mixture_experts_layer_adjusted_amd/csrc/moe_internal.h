@@ -25,6 +25,18 @@ constexpr int kMaxShared = 64;
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 inline size_t align_up(size_t a, size_t b) { return (a + b - 1) / b * b; }
 
+// A kernel's launch, for operators of a few microseconds: the <<<>>> syntax first puts grid and stream on a stack of the
+// runtime's and takes them off again (2.91 us of host time a launch against 2.76).
+template <typename T>
+struct SameType { using type = T; };
+template <typename... P>
+hipError_t launch_kernel(void (*kernel)(P...), dim3 grid, dim3 block, size_t lds, hipStream_t st,
+                         typename SameType<P>::type... p) {
+  void* args[] = {&p...};
+  (void)hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, block, args, lds, st);
+  return hipGetLastError();
+}
+
 // Byte offsets of every buffer inside the caller's workspace.
 struct WorkspacePlan {
   // routing

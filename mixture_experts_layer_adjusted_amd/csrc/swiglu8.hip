@@ -176,19 +176,17 @@ hipError_t launch_swiglu8_forward(int64_t rows, const int32_t* row_end, int I, c
                                   float* scales, hipStream_t st) {
   const int64_t units = rows * (I / 128);
   if (units == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu8_fwd_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, st,
+  return launch_kernel(swiglu8_fwd_kernel, dim3(blocks_for(units)), dim3(kThreads), 0, st,
                      static_cast<const uint16_t*>(ab), rows, row_end, I, static_cast<uint16_t*>(h), codes, scales);
-  return hipGetLastError();
 }
 
 hipError_t launch_swiglu8_backward(int64_t rows, int I, const void* dh, const int8_t* codes, const float* scales,
                                    void* dab, void* h, hipStream_t st) {
   const int64_t units = rows * (I / 128);
   if (units == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu8_bwd_kernel<false>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
+  return launch_kernel(swiglu8_bwd_kernel<false>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
                      static_cast<const uint16_t*>(dh), codes, scales, rows, I, static_cast<uint16_t*>(dab),
                      static_cast<uint16_t*>(h), Swiglu8Rows{});
-  return hipGetLastError();
 }
 
 hipError_t launch_swiglu_bwd_saved8(const int8_t* codes, const float* scales, const void* dhu, const float* row_gate,
@@ -196,10 +194,9 @@ hipError_t launch_swiglu_bwd_saved8(const int8_t* codes, const float* scales, co
                                     void* h, float* dg_part, hipStream_t st) {
   const int64_t units = max_rows * (I / 128);
   if (units == 0) return hipSuccess;
-  hipLaunchKernelGGL(swiglu8_bwd_kernel<true>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
+  return launch_kernel(swiglu8_bwd_kernel<true>, dim3(blocks_for(units)), dim3(kThreads), 0, st,
                      static_cast<const uint16_t*>(dhu), codes, scales, max_rows, I, static_cast<uint16_t*>(dab),
                      static_cast<uint16_t*>(h), Swiglu8Rows{row_end, row_gate, row_token, dg_part});
-  return hipGetLastError();
 }
 
 }  // namespace moe
