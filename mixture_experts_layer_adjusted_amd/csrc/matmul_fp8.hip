@@ -155,14 +155,16 @@ struct TileShape {
   static constexpr int kMB = BM / WM / 16, kNB = BN / WN / 16;
   static constexpr int kADma = BM / 8 / kWaves, kBDma = BN / 8 / kWaves;   // 1 KB loads of a wavefront per stage
   static constexpr int kDataBytes = (BM + BN) * kBK;
-  static constexpr int kSpan = ROWS && STAGES == 3 ? 2 : 4;                 // K blocks whose scales are loaded together
+  // K blocks whose scales are loaded together (forward 8192 x 4096 x 7168: 219 us with 4, 215 with 8; the input gradient
+  // 192 x 3024 x 2176 the other way round, 10.2 and 10.4; the weight gradient's two vectors leave no room for more)
+  static constexpr int kSpan = FORM == MOE_FP8_FORWARD ? 8 : ROWS && STAGES == 3 ? 2 : 4;
   static constexpr int kPart = 64 / kSpan;                                  // rows of one scale load
   static constexpr int kAScale = BM * kSpan * 4;                            // a's scales of kSpan K blocks
   static constexpr int kBScale = ROWS ? BN * kSpan * 4 : 256;               // b's: rows, or up to 16 column blocks
   static constexpr int kScales = STAGES * kDataBytes;                        // where they start
-  static constexpr int kUnread = kScales + 3 * (kAScale + kBScale);          // where the L2 prefetch goes
+  static constexpr int kUnread = kScales + 3 * (kAScale + kBScale);          // where loads go that nothing reads
   static constexpr bool kPrefetch = STAGES == 2 && BM == 256 && !KN;
-  static constexpr int kLds = kUnread + (kPrefetch ? kWaves * 256 : 0);
+  static constexpr int kLds = kUnread + (kPrefetch ? kWaves * 256 : 256);
   static_assert(BM % 64 == 0 && BM / 64 + (ROWS ? BN / 64 : 1) <= kWaves, "one scale load of a wavefront per stage");
   static_assert(STAGES - 1 <= kSpan, "three spans of scales hold all that is in use");
   static_assert(kADma * 8 * kWaves == BM && kBDma * 8 * kWaves == BN, "whole loads");
@@ -178,6 +180,8 @@ struct TileShape {
 // Scales: a row's are neighbours along K, rows are far apart, and a load costs by the cache lines it touches (64 rows
 // a load kept the address unit busy 183 cycles, 29 a load of codes).  So a load takes several K blocks (a span) of fewer
 // rows, one load of a wavefront per stage, a span ahead, into one of three spans in LDS: [kPart rows][K block][row].
+// Wavefronts without a share load one word, which costs the address unit next to nothing (repeating another's share
+// took 4 to 10% of small tiles' time: 1000 x 2816 x 2048 15.4 us -> 14.7).
 //
 // L2: with two stages, what misses L2 is late (all hits: 199 us against 237 at 8192 x 4096 x 7168).  Of the tiles an XCD
 // works on at a time, eight share a's rows and four b's, so each asks for an eighth and a quarter of the lines of the
@@ -236,16 +240,18 @@ __global__ void __launch_bounds__(WM * WN * 64 * SETS) matmul_tile_kernel(Matmul
   }
   // scales: in the load of stage s, lane (kb, r) takes K block kb and row r of part (s mod kSpan) BM / 64 + w of the span
   // after s's; w: the wavefront among the first BM / 64 (a's rows) or the next (b's rows, or all the span's column blocks
-  // in each load).  The others repeat a's, so that every wavefront has the same loads in flight.
+  // in each load).  The others load one word into LDS that nothing reads, so that every wavefront has the same loads in
+  // flight.
   constexpr int kAW = BM / 64, kBW = ROWS ? BN / 64 : 1;
-  const bool for_a = wave < kAW || wave >= kAW + kBW, for_rows = for_a || ROWS;
+  const bool idle = wave >= kAW + kBW, for_a = wave < kAW || idle, for_rows = for_a || ROWS;
   const int s_wave = for_a ? wave % kAW : wave - kAW;
-  const int s_step = for_a ? kAW : ROWS ? kBW : 0;        // parts of one stage's loads
+  const int s_step = idle ? 0 : for_a ? kAW : ROWS ? kBW : 0;        // parts of one stage's loads
   const int s_row = (for_rows ? s_wave * kPart : n0 / kBK) + lane % kPart;
   const int s_last = for_a ? g.m - 1 - m0 : ROWS ? g.n - 1 - n0 : g.nblk - 1;
-  const uint32_t s_rowstep = KN && !for_a ? 1 : (uint32_t)KB, s_kstep = KN && !for_a ? (uint32_t)g.nblk : 1;
-  uint8_t* const s_dst = (for_a ? ascales : bscales) + (for_rows ? s_wave * 256 : 0);
-  const int s_span = for_a ? S::kAScale : S::kBScale;
+  const uint32_t s_rowstep = idle ? 0 : KN && !for_a ? 1 : (uint32_t)KB;
+  const uint32_t s_kstep = idle ? 0 : KN && !for_a ? (uint32_t)g.nblk : 1;
+  uint8_t* const s_dst = idle ? lds + S::kUnread : (for_a ? ascales : bscales) + (for_rows ? s_wave * 256 : 0);
+  const int s_span = idle ? 0 : for_a ? S::kAScale : S::kBScale;
   const uint8_t* abase = g.a + (int64_t)m0 * g.lda;
   const uint8_t* bbase = KN ? g.b + n0 : g.b + (int64_t)n0 * g.ldb;
   const __amdgpu_buffer_rsrc_t abuf =
@@ -358,7 +364,7 @@ __global__ void __launch_bounds__(WM * WN * 64 * SETS) matmul_tile_kernel(Matmul
   auto read_rows = [&](int kt, int i) {   // row block i's fragment and scale
     const uint8_t* st = lds + kt % STAGES * S::kDataBytes;
     next = frag_at(st + xr + i * 16 * kBK + c0, st + xr + i * 16 * kBK + c1);
-    sa_next = scale_at(ascales, S::kAScale, kt, mrow + 16 * i)[l16];
+    sa_next = scale_at(ascales, S::kAScale, kt, mrow + 16 * i)[kPart < 16 ? l16 / kPart * 64 + l16 % kPart : l16];
   };
   // Group h of K block kt from `now`; `then` receives the start of the group after it.  Pieces of kUnit blocks: a
   // piece's instructions, then the fold of the piece kLag before it, whose results are there by then, in this order (left
@@ -641,16 +647,16 @@ __global__ void __launch_bounds__(256) quant_act_t_kernel(const uint16_t* __rest
 
 // The tiles (Sets: two sets of wavefronts, each on half of the K blocks), and for bf16 and for fp32 outputs what a launch
 // of one takes apart from its K blocks and what a K block takes with every CU at work (us; 0: not built), fitted to
-// 138 shapes from 16 to 9000 rows with up to 8 slices: the choice is 1% slower than the best of them on average.
+// 138 shapes from 16 to 9000 rows with up to 8 slices; on 60 others the choice is 2% slower than the best on average.
 enum Tile { kT256, kT128x256, kT128, kT128Pair, kT128Sets, kT64Pair, kT64Sets, kTiles };
 struct TileCost {
   int bm, bn, per_cu;   // workgroups of a CU at a time
   float base, step, base_f32, step_f32;
 };
 constexpr TileCost kCost[kTiles] = {{256, 256, 1, 6.8f, 1.59f, 9.9f, 3.19f}, {128, 256, 1, 5.9f, 1.08f, 0.0f, 0.0f},
-                                    {128, 128, 1, 5.1f, 0.65f, 0.0f, 0.0f},  {128, 128, 2, 4.5f, 1.44f, 4.8f, 1.88f},
-                                    {128, 128, 1, 0.0f, 0.0f, 5.8f, 1.18f},  {64, 64, 2, 4.4f, 0.51f, 3.2f, 1.10f},
-                                    {64, 64, 1, 5.0f, 0.25f, 4.5f, 0.55f}};
+                                    {128, 128, 1, 5.1f, 0.62f, 0.0f, 0.0f},  {128, 128, 2, 4.5f, 1.44f, 4.8f, 1.88f},
+                                    {128, 128, 1, 0.0f, 0.0f, 5.8f, 1.18f},  {64, 64, 2, 4.4f, 0.49f, 3.2f, 1.08f},
+                                    {64, 64, 1, 4.8f, 0.23f, 4.5f, 0.52f}};
 
 struct Plan {
   int rows;            // rows of a that the plan covers (from the first)
@@ -660,8 +666,9 @@ struct Plan {
   float us;
 };
 
-// The plan for `rows` rows in one kernel (and the join): rounds of tiles over the CUs, a chip that is not full being up
-// to 22% faster (38% where a CU has one workgroup in place of two), and for slices 2.3 us and their sums' way to memory and back.  kb / slices is 2 at least.
+// The plan for `rows` rows in one kernel (and the join): rounds of tiles over the CUs (1.5 us for the start of each after
+// the first), a chip that is not full being up to 22% faster (38% where a CU has one workgroup in place of two), and for
+// slices 2.3 us and their sums' way to memory and back.  kb / slices is 2 at least.
 Plan plan_one(const moe_matmul_shape& s, int rows) {
   const int kb = s.k / kBK;
   Plan best{rows, 0, kT64Pair, 1, kb, 0.0f};
@@ -677,9 +684,7 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
     const TileCost& c = kCost[i];
     const float step = f32 ? c.step_f32 : c.step;
     if (step == 0.0f) continue;
-    // (two sets gain least in a bf16 forward, which is nearest to memory: 77 x 7168 x 2048 8.9 us without, 9.4 with;
-    // with 31 K blocks, 308 x 1680, 13.2 and 11.4)
-    const float base = f32 ? c.base_f32 : i == kT64Sets && s.form == MOE_FP8_FORWARD ? c.base + 2.0f : c.base;
+    const float base = f32 ? c.base_f32 : c.base;
     const float faster = c.per_cu == 2 ? 0.38f : 0.22f;
     const int64_t tiles = ceil_div(rows, c.bm) * ceil_div(s.n, c.bn);
     for (int want = 1; want <= 16 && (want == 1 || want * 2 <= kb); ++want) {
@@ -687,7 +692,8 @@ Plan plan_one(const moe_matmul_shape& s, int rows) {
       if (splits != want) continue;
       const int64_t total = tiles * splits, at_once = 256 * c.per_cu;
       const float fill = total < at_once ? (float)total / at_once : 1.0f;
-      float us = base + (float)ceil_div(total, at_once) * per * step * (1.0f - faster * (1.0f - fill));
+      const float rounds = (float)ceil_div(total, at_once);
+      float us = base + 1.5f * (rounds - 1.0f) + rounds * per * step * (1.0f - faster * (1.0f - fill));
       if (splits > 1) us += 2.3f + (float)splits * rows * s.n * 8 / 4.2e6f;
       if (best.us == 0.0f || us < best.us)
         best = Plan{rows, 0, (Tile)i, splits, per, us};

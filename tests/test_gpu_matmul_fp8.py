@@ -98,6 +98,10 @@ LARGER = [("forward", False, 1, 16, 2176), ("forward", True, 1, 16, 2432), ("for
           ("input_grad", True, 65, 5024, 3200), ("weight_grad", False, 12, 5040, 2688),
           ("weight_grad", False, 8366, 80, 4224), ("weight_grad", True, 147, 1200, 2048),
           ("weight_grad", True, 65, 4336, 3584), ("weight_grad", True, 66, 4144, 3968),
+          ("forward", False, 198, 4112, 4992), ("forward", False, 845, 4688, 896), ("forward", False, 17, 400, 3200),
+          ("forward", True, 66, 4112, 3712), ("input_grad", True, 65, 4592, 3584),
+          ("forward", False, 475, 4192, 256), ("forward", False, 1000, 2816, 1024), ("input_grad", False, 8687, 208, 256),
+          ("weight_grad", False, 540, 3696, 256),
           # two sets of wavefronts, the last slice a single K block
           ("input_grad", False, 25, 2272, 4736), ("forward", True, 65, 2736, 5248), ("weight_grad", False, 28, 2000, 5504),
           ("weight_grad", True, 384, 336, 4736), ("input_grad", True, 186, 704, 4736)]
