@@ -287,10 +287,9 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
             continue;
           }
           const int i = 4 * q + j;
-          float c = SOFTMAX ? fmaf(s[i], total, bias[i]) : s[i] + bias[i];
-          c = l[i] == kNegInf ? kNegInf : c;   // (scores are finite: a bias of -inf leaves -inf too)
+          const float c = SOFTMAX ? fmaf(s[i], total, bias[i]) : s[i] + bias[i];
           const uint32_t k = key_of(c);
-          key[q][j] = c == kNegInf ? kOut : k;
+          key[q][j] = l[i] == kNegInf || bias[i] == kNegInf ? kOut : k;   // (not by c: a NaN score's is a NaN)
         }
     }
     if (limited && per == 0) {
