@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
     for (int h = 0; h < kHalves; ++h)
       if (h < halves && real && lane + L * h < K) {
         a.idx[t * K + lane + L * h] = e[h];
-        a.gate[t * K + lane + L * h] = a.scale * g[h];
+        a.gate[t * K + lane + L * h] = e[h] >= 0 ? a.scale * g[h] : 0.0f;   // (an empty place's share of a NaN sum is one)
         if (e[h] >= 0) atomicAdd(&hist[e[h]], 1);
       }
     __builtin_amdgcn_wave_barrier();

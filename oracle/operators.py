@@ -69,7 +69,7 @@ def gate_values(s, idx, renorm=True, scale=1.0):
     sel = np.where(on, np.take_along_axis(s, np.where(on, idx, 0), 1), 0.0)
     if renorm:
         total = sel.sum(axis=1, keepdims=True)
-        sel = sel / np.where(total == 0, 1, total)
+        sel = np.where(on, sel / np.where(total == 0, 1, total), 0.0)
     return scale * sel
 
 

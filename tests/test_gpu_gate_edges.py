@@ -60,3 +60,14 @@ def test_a_nan_or_an_infinity_opens_no_expert_out_of_service(T, N, G, softmax):
         assert clear[:4].all() and np.array_equal(got[clear], want[clear])
         assert not np.isneginf(bias[got[got >= 0]]).any()
         assert np.array_equal(load.cpu().numpy(), np.bincount(got[got >= 0], minlength=N))
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("softmax", [False, True], ids=["sigmoid", "softmax"])
+def test_an_empty_place_beside_a_nan_has_gate_zero(softmax, renorm):
+    for T, N in ((4, 200), (5, 30), (5, 400)):
+        l = torch.full((T, N), -INF, device="cuda")
+        l[:, 7], l[:, 9] = 0.5, NAN
+        _, idx, gate, _ = run(l, None, 5, softmax, renorm=renorm)
+        assert idx.tolist() == [[7, 9, -1, -1, -1]] * T
+        assert (gate[:, 2:] == 0).all() and torch.isnan(gate[:, 1]).all()

@@ -88,3 +88,10 @@ def test_swiglu8_backward_against_differences():
         e = np.zeros_like(ab)
         e[r, c] = step
         assert abs(((P.swiglu(ab + e) - P.swiglu(ab - e)) * dh).sum() / (2 * step) - d_ab[r, c]) < 1e-8
+
+
+def test_gate_of_an_empty_place_beside_a_nan():
+    l = np.array([[0.5, np.nan, -np.inf, -np.inf]])
+    for softmax in (False, True):
+        idx, g, _, _ = P.gate(l, None, 3, softmax)
+        assert idx.tolist() == [[0, 1, -1]] and np.isnan(g[0, 1]) and g[0, 2] == 0
