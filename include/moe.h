@@ -339,7 +339,10 @@ moe_status moe_gate_workspace_size(const moe_gate_config* config, size_t* bytes)
  *   expert_load [N]     int32 out, or NULL: picks of each expert
  * An expert whose logit or bias is -inf is not eligible; a token whose logits are all -inf (a
  * padding row) picks nothing.  A NaN score ranks below every number, and its gates are NaN.  Scores,
- * sums and gates are fp32.  T == 0 writes expert_load = 0.
+ * sums and gates are fp32, scores and gates below 2^-126 may be 0.  Only a softmax without a bias (or
+ * with entries +0 and -inf alone) ranks experts and groups by the logits, so that scores too small for
+ * fp32 keep their order; other keys that are equal in fp32 count as ties.  T == 0 writes
+ * expert_load = 0.
  * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512 or top_k > 32:
  * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE if workspace_bytes is too small. */
 moe_status moe_gate(const moe_gate_config* config, const void* logits, const float* bias, int32_t* topk_idx,

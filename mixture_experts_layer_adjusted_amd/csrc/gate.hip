@@ -3,6 +3,7 @@
 // For a token's logits l[0..N), a bias b (or none) and K picks:
 //   s_i = 1 / (1 + exp(-l_i))   or   s_i = exp(l_i) / sum_j exp(l_j);
 //   c_i = s_i + b_i ranks the experts; l_i = -inf or b_i = -inf takes expert i out;
+//   (a softmax whose b_i are all 0, or -inf, ranks by l_i: the same order, which exp(l_i) below 2^-126 would lose)
 //   with G groups of N / G neighbouring experts, only the TG groups with the largest score (the largest c,
 //   or the sum of the two largest) stay; the K largest c left are the picks, equal ones by index;
 //   g_k = scale s_k / sum of the picked s, or scale s_k.
@@ -172,9 +173,11 @@ struct GateArgs {
 };
 
 // Bits of the groups that stay open.  keys: the token's keys in LDS.  2^p lanes work on a group (as many as
-// leave a lane set for every group), each on every 2^p-th expert; their two largest join by shuffles.  A
-// group's score counts numbers only: a NaN or an absent second adds nothing.
-__device__ __forceinline__ uint64_t open_groups(const uint32_t* keys, const GateArgs& a, int lane, int lanes_log2) {
+// leave a lane set for every group), each on every 2^p-th expert; their two largest join by shuffles.
+// score_pair: the key of a group's score from those of its two largest, where both count.
+template <typename Score>
+__device__ __forceinline__ uint64_t open_groups(const uint32_t* keys, const GateArgs& a, int lane, int lanes_log2,
+                                                Score score_pair) {
   const int gs = a.N / a.G, per = 1 << lanes_log2;
   const int g = lane >> lanes_log2;
   uint32_t k1 = kOut, k2 = kOut;
@@ -190,8 +193,7 @@ __device__ __forceinline__ uint64_t open_groups(const uint32_t* keys, const Gate
     k2 = max(max(k2, o2), min(k1, o1));
     k1 = max(k1, o1);
   }
-  uint32_t score = k1;
-  if (a.top2 && k2 > kNanKey) score = key_of(score_of(k1) + score_of(k2));
+  const uint32_t score = a.top2 ? score_pair(k1, k2) : k1;
   // the rank of the lane's group: groups above it, or equal to it and before it
   int rank = 0;
   for (int h = 0; h < a.G; ++h) {
@@ -206,8 +208,9 @@ __device__ __forceinline__ uint64_t open_groups(const uint32_t* keys, const Gate
 
 // Whether the lane's group stays open, groups being `per` whole lanes: the lanes' two largest join over the group, and
 // the group's rank counts the groups above it, or equal to it and before it.  Scores as in open_groups.
-template <int L>
-__device__ __forceinline__ bool group_open(uint32_t k1, uint32_t k2, const GateArgs& a, int lane, int per) {
+template <int L, typename Score>
+__device__ __forceinline__ bool group_open(uint32_t k1, uint32_t k2, const GateArgs& a, int lane, int per,
+                                           Score score_pair) {
   auto join = [&](uint32_t o1, uint32_t o2) {
     k2 = max(max(k2, o2), min(k1, o1));
     k1 = max(k1, o1);
@@ -218,8 +221,7 @@ __device__ __forceinline__ bool group_open(uint32_t k1, uint32_t k2, const GateA
   if (per >= 16) join(turned<0x140>(k1), turned<0x140>(k2));    // row_mirror
   if (L >= 32 && per >= 32) join(__shfl_xor(k1, 16, 64), __shfl_xor(k2, 16, 64));
   if (L >= 64 && per >= 64) join(__shfl_xor(k1, 32, 64), __shfl_xor(k2, 32, 64));
-  uint32_t score = k1;
-  if (a.top2 && k2 > kNanKey) score = key_of(score_of(k1) + score_of(k2));
+  const uint32_t score = a.top2 ? score_pair(k1, k2) : k1;
   const int g = lane / per;
   int rank = 0;
   for (int h = 0; h < a.G; ++h) {
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
     float total = 0.0f, top = 0.0f;      // softmax: the row's sum and maximum
     float l[CPL];
     load_run<CPL>(row + first, left, l);
+    bool by_logit = false;
     {
       float s[CPL];
       if constexpr (SOFTMAX) {
@@ -278,6 +281,18 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
 #pragma unroll
         for (int j = 0; j < CPL; ++j) s[j] = sigmoid_of(l[j]);
       }
+      // the biases, from here on unknown to the compiler: it would wait for them before the logits are asked for, and keep
+      // a mask for each of their comparisons
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) asm volatile("" : "+v"(bias[j]));
+      float factor = 1.0f;   // of what ranks the experts: the scores before their division by the sum, or the logits
+      if constexpr (SOFTMAX) {
+        bool none = true;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) none = none && __builtin_amdgcn_classf(bias[j], 0x044);   // +0 or -inf: then no key is -0
+        by_logit = __builtin_amdgcn_ballot_w64(!none) == 0;   // (a wavefront sees all the biases)
+        factor = by_logit ? fmaf(total, 0.0f, 1.0f) : total;   // (a row without a number has none of either)
+      }
 #pragma unroll
       for (int q = 0; q < kLists; ++q)
 #pragma unroll
@@ -287,18 +302,27 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
             continue;
           }
           const int i = 4 * q + j;
-          const float c = SOFTMAX ? fmaf(s[i], total, bias[i]) : s[i] + bias[i];
+          const float c = SOFTMAX ? fmaf(by_logit ? l[i] : s[i], factor, bias[i]) : s[i] + bias[i];
           const uint32_t k = key_of(c);
           key[q][j] = l[i] == kNegInf || bias[i] == kNegInf ? kOut : k;   // (not by c: a NaN score's is a NaN)
         }
     }
+    // The key of a group's score, the sum of its two largest.  It counts numbers only: a NaN or an absent second adds
+    // nothing.  By logits, of exp(l1 - top) + exp(l2 - top) the logarithm.
+    auto score_pair = [&](uint32_t k1, uint32_t k2) {
+      if (SOFTMAX && by_logit) {
+        const float l1 = score_of(k1), x = k2 > kNanKey ? exp_of(score_of(k2) - l1) : 0.0f;
+        return k1 > kNanKey ? key_of(fmaf(__builtin_amdgcn_logf(1.0f + x), 0.693147182f, l1 - top)) : k1;
+      }
+      return k2 > kNanKey ? key_of(score_of(k1) + score_of(k2)) : k1;
+    };
     if (limited && per == 0) {
       if constexpr (L == 64) {
 #pragma unroll
         for (int j = 0; j < CPL; ++j)
           if (j < left) keys[wave][first + j] = key[j / 4][j % 4];
         __builtin_amdgcn_wave_barrier();   // LDS operations of one wavefront take effect in program order
-        const uint64_t open = open_groups(keys[wave], a, lane, lanes_log2);
+        const uint64_t open = open_groups(keys[wave], a, lane, lanes_log2, score_pair);
         __builtin_amdgcn_wave_barrier();
         const float inv = (float)a.G / (float)N;   // (small integers: half a step in, the quotient is exact enough)
 #pragma unroll
@@ -335,7 +359,7 @@ __global__ void __launch_bounds__(kWaves * 64) gate_kernel(GateArgs a, int per, 
         k2 = max(max(k2, kLen > 1 ? key[q][1] : kOut), min(k1, key[q][0]));
         k1 = max(k1, key[q][0]);
       }
-      if (!group_open<L>(k1, k2, a, lane, per)) {
+      if (!group_open<L>(k1, k2, a, lane, per, score_pair)) {
 #pragma unroll
         for (int q = 0; q < kLists; ++q)
 #pragma unroll

@@ -71,3 +71,34 @@ def test_an_empty_place_beside_a_nan_has_gate_zero(softmax, renorm):
         _, idx, gate, _ = run(l, None, 5, softmax, renorm=renorm)
         assert idx.tolist() == [[7, 9, -1, -1, -1]] * T
         assert (gate[:, 2:] == 0).all() and torch.isnan(gate[:, 1]).all()
+
+
+# (tokens, experts, groups) and the step between neighbouring logits of a row: the last ones are 500 below the first
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T,N,G,step", [(40, 48, 1, 8), (40, 64, 4, 8), (40, 63, 9, 8), (40, 256, 8, 2), (4, 128, 4, 4),
+                                        (4, 256, 1, 2), (40, 500, 5, 1)])
+def test_softmax_picks_among_scores_too_small_for_fp32(T, N, G, step, bf16):
+    """Without a bias (none, or zeros) the order is that of the logits, exp(-90) and exp(-91) told apart."""
+    if bf16 and step == 1:
+        pytest.skip("more integers than bf16 holds")
+    K = 9
+    rng = np.random.default_rng(N)
+    l = (step * (np.argsort(rng.random((T, N)), axis=1) - N // 2)).astype(np.float32)
+    l[0] = 0
+    l[0, [N // 2, N // 3]] = 95, 5         # the rest ties at 0
+    x = torch.from_numpy(l).cuda()
+    x = x.bfloat16() if bf16 else x
+    assert np.array_equal(x.float().cpu().numpy(), l)
+    zeros = np.zeros(N, np.float32)
+    out = zeros.copy()
+    out[[1, N // 2 + 1, N - 1]] = -INF
+    for bias in (None, zeros, out):
+        b = None if bias is None else torch.from_numpy(bias).cuda()
+        for top2 in (False, True) if G > 1 else (False,):
+            for renorm in (False, True):
+                TG = (G + 1) // 2
+                cfg, idx, gate, load = run(x, b, K, True, G, TG, top2, renorm)
+                want, gates, cnt, _ = P.gate(l, bias, K, True, G, TG, top2, renorm)
+                assert np.array_equal(idx.cpu().numpy(), want) and np.array_equal(load.cpu().numpy(), cnt)
+                # (differences of these logits are exact; a score below 2^-126 may be 0)
+                assert (np.abs(gate.cpu().numpy() - gates) <= 5e-6 * gates + 2.0 ** -126).all()
