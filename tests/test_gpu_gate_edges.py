@@ -102,3 +102,34 @@ def test_softmax_picks_among_scores_too_small_for_fp32(T, N, G, step, bf16):
                 assert np.array_equal(idx.cpu().numpy(), want) and np.array_equal(load.cpu().numpy(), cnt)
                 # (differences of these logits are exact; a score below 2^-126 may be 0)
                 assert (np.abs(gate.cpu().numpy() - gates) <= 5e-6 * gates + 2.0 ** -126).all()
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("softmax", [False, True], ids=["sigmoid", "softmax"])
+@pytest.mark.parametrize("N,K", [(40, 6), (256, 8), (500, 20)])
+def test_gates_and_gradients_of_large_logits(N, K, softmax, bf16):
+    """Logits of up to 80: saturated sigmoids, and softmax rows that one expert has to itself.  A sigmoid keeps its own
+    5e-6; a softmax's argument is rounded by up to 2^-24 of 160 besides (1e-5), and its gates may underflow."""
+    T = 60
+    g = torch.Generator("cuda").manual_seed(N + K)
+    l = 160 * torch.rand(T, N, device="cuda", generator=g) - 80
+    l[:8] = -60 - 20 * torch.rand(8, N, device="cuda", generator=g)     # rows of small sigmoids alone
+    l[8:16] = 20 + 60 * torch.rand(8, N, device="cuda", generator=g)    # and of saturated ones
+    l = l.bfloat16() if bf16 else l
+    bias = 0.1 * torch.randn(N, device="cuda", generator=g)
+    dg = torch.randn(T, K, device="cuda", generator=g)
+    host = l.float().cpu().numpy()
+    for b in (None, bias):
+        for renorm in (False, True):
+            cfg, idx, gate, _ = run(l, b, K, softmax, renorm=renorm, scale=2.0)
+            got = idx.cpu().numpy()
+            assert (got >= 0).all() and all(len(set(r)) == K for r in got.tolist())
+            gates = P.gate_values(P.gate_scores(host, softmax), got, renorm, 2.0)
+            tol = (1.5e-5 if softmax else 5e-6) * gates + 2.0 ** -124
+            assert (np.abs(gate.cpu().numpy() - gates) <= tol).all()
+            d = torch.full_like(l, NAN)
+            moe.moe_gate_backward(cfg, l, idx, dg, d)
+            ref = P.gate_backward(host, got, dg.cpu().numpy(), softmax, renorm, 2.0)
+            tol = (3e-5 if softmax else 1e-5) * 2.0 * dg.abs().amax(dim=1, keepdim=True).cpu().numpy()
+            tol = tol + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+            assert (np.abs(d.float().cpu().numpy() - ref) <= tol).all()
