@@ -1038,7 +1038,8 @@ moe_status moe_swiglu_forward8(int32_t rows, int32_t inter, const void* ab, void
   if (rows < 0 || inter < 0) return MOE_ERR_INVALID_ARG;
   if (inter % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)rows * inter == 0) return MOE_OK;
-  if (!ab || !saved || !scales || h == ab || saved == ab || !aligned16(ab, h, saved)) return MOE_ERR_INVALID_ARG;
+  if (!ab || !saved || !scales || h == ab || saved == ab || h == saved || !aligned16(ab, h, saved))
+    return MOE_ERR_INVALID_ARG;
   return hip_status(launch_swiglu8_forward(rows, nullptr, inter, ab, h, saved, scales, stream));
 }
 

@@ -116,6 +116,13 @@ def test_quantize_act_t_and_swiglu8():
     assert b(4, 128, P[0], P[1], P[2], P[1], P[4]) == INVALID and b(4, 128, P[0], P[1], P[2], P[3], P[0]) == INVALID
 
 
+def test_swiglu8_outputs_in_one_place():
+    """The codes and h may not share a buffer (both are written, by different lanes)."""
+    assert lib.moe_swiglu_forward8(4, 128, P[0], P[1], P[1], P[3], None) == INVALID
+    assert lib.moe_swiglu_backward8(4, 128, P[0], P[1], P[2], P[3], P[3], None) == INVALID
+    assert lib.moe_swiglu_backward8(4, 128, P[0], P[1], P[2], P[3], P[1], None) == INVALID
+
+
 def test_layer_under_a_given_router():
     sb = moe.make_shape(300, 256, 16, 4, 1, 128, moe.MOE_DTYPE_BF16)
     s32 = moe.make_shape(300, 256, 16, 4, 1, 128, moe.MOE_DTYPE_F32)
