@@ -285,9 +285,10 @@ moe_status moe_prepare_weights(const moe_shape* shape, const moe_weights* logica
 
 /* FP8 weight preparation (核心概念, FP8 item: 128x128 block scaling): quantises a stack of
  * n_mats bf16 matrices [rows, cols] into E4M3FN codes [n_mats, rows, cols] and fp32 scales
- * [n_mats, rows/128, cols/128]: scale = amax/448 (1 for an all-zero block), code =
+ * [n_mats, ceil(rows/128), ceil(cols/128)]: scale = amax/448 (1 for an all-zero block), code =
  * round-to-nearest-even E4M3FN of fp32(x / scale), saturating at 448.
- * rows and cols must be multiples of 128. */
+ * rows and cols must be multiples of 16; the last blocks may be smaller than 128 (moe_matmul_fp8
+ * takes them, the layer needs whole ones). */
 moe_status moe_quantize_weights(int32_t n_mats, int32_t rows, int32_t cols, const void* w_bf16,
                                 uint8_t* codes, float* scales, hipStream_t stream);
 

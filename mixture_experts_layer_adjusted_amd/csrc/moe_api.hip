@@ -860,7 +860,7 @@ moe_status moe_update_bias(int32_t n_routed, int64_t total_assignments, const in
 moe_status moe_quantize_weights(int32_t n_mats, int32_t rows, int32_t cols, const void* w_bf16, uint8_t* codes,
                                 float* scales, hipStream_t stream) {
   if (n_mats < 0 || rows < 0 || cols < 0) return MOE_ERR_INVALID_ARG;
-  if (rows % 128 != 0 || cols % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (rows % 16 != 0 || cols % 16 != 0) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)n_mats * rows * cols == 0) return MOE_OK;
   if (!w_bf16 || !codes || !scales) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_quantize_weights(n_mats, rows, cols, w_bf16, codes, scales, stream));

@@ -1,5 +1,5 @@
-"""The FP8 quantisers beside each other, on the GPU: the transposing one gives what the plain one gives for the
-transposed matrix, to the bit."""
+"""The FP8 quantisers on the GPU: the transposing one gives what the plain one gives for the transposed matrix, to the
+bit; weights in 16s are quantised as if filled up with zeros."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +40,49 @@ def test_transposed_codes_are_those_of_the_transpose(rows, cols):
     assert torch.equal(s, s2)
     number = (q2 & 0x7F) != 0x7F                 # (a NaN's sign says nothing)
     assert torch.equal(number, (q & 0x7F) != 0x7F) and torch.equal(q[number], q2[number])
+
+
+@pytest.mark.parametrize("n,rows,cols", [(1, 16, 128), (2, 144, 256), (3, 288, 400), (1, 128, 16), (1, 2320, 384)])
+def test_weights_whose_last_blocks_are_smaller(n, rows, cols):
+    """A block's codes and scale are those of the same block filled up with zeros."""
+    g = torch.Generator("cuda").manual_seed(rows)
+    w = torch.randn(n, rows, cols, device="cuda", generator=g).bfloat16()
+    rb, cb = -(-rows // 128), -(-cols // 128)
+    q = torch.full((n, rows, cols), 0x55, dtype=torch.uint8, device="cuda")
+    s = torch.full((n, rb, cb), 7.0, device="cuda")
+    moe.moe_quantize_weights(n, rows, cols, w, q, s)
+    full = torch.zeros(n, rb * 128, cb * 128, dtype=torch.bfloat16, device="cuda")
+    full[:, :rows, :cols] = w
+    q2, s2 = torch.empty_like(full, dtype=torch.uint8), torch.empty_like(s)
+    moe.moe_quantize_weights(n, rb * 128, cb * 128, full, q2, s2)
+    assert torch.equal(s, s2) and torch.equal(q, q2[:, :rows, :cols])
+
+
+def test_product_with_quantised_weights_of_odd_size():
+    """Forward and input gradient of a layer whose 144 outputs do not fill their blocks, from the quantisers to the
+    product: against float64 of what the codes stand for (fp32 outputs: (k + 64) 2^-24 of the products' magnitudes)."""
+    T, n, d = 70, 144, 256
+    g = torch.Generator("cuda").manual_seed(2)
+    w = (torch.randn(n, d, device="cuda", generator=g) * torch.linspace(0.1, 9, n, device="cuda")[:, None]).bfloat16()
+    q = torch.empty(n, d, dtype=torch.float8_e4m3fn, device="cuda")
+    s = torch.empty(2, 2, device="cuda")
+    moe.moe_quantize_weights(1, n, d, w, q, s)
+    wide = q.double() * s.double().repeat_interleave(128, 0)[:n].repeat_interleave(128, 1)
+    assert ((wide - w.double()).norm() <= 0.05 * w.double().norm()).item()     # (E4M3: 2.6% of a normal value)
+    x, xs = quantized(torch.randn(T, d, device="cuda", generator=g).bfloat16())
+    out = torch.empty(T, n, device="cuda")
+    shape = moe.make_matmul_shape(T, n, d, moe.MOE_FP8_FORWARD, moe.MOE_DTYPE_F32)
+    ws = torch.empty(max(1, moe.moe_matmul_fp8_workspace_size(shape)), dtype=torch.uint8, device="cuda")
+    moe.moe_matmul_fp8(shape, x, xs, q, s, out, ws)
+    a = x.view(torch.float8_e4m3fn).double() * xs.double().repeat_interleave(128, 1)
+    y = wide.t().contiguous()
+    assert ((out.double() - a @ y).abs() <= (d + 64) * 2.0 ** -24 * (a.abs() @ y.abs())).all()
+    # the input gradient contracts over a stored matrix's rows, here 256 of them, and has its 144 columns
+    w2 = w.t().contiguous()
+    q2, s2 = torch.empty(d, n, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(2, 2, device="cuda")
+    moe.moe_quantize_weights(1, d, n, w2, q2, s2)
+    wide = q2.double() * s2.double().repeat_interleave(128, 0).repeat_interleave(128, 1)[:, :n]
+    shape = moe.make_matmul_shape(T, n, d, moe.MOE_FP8_INPUT_GRAD, moe.MOE_DTYPE_F32)
+    ws = torch.empty(max(1, moe.moe_matmul_fp8_workspace_size(shape)), dtype=torch.uint8, device="cuda")
+    moe.moe_matmul_fp8(shape, x, xs, q2, s2, out, ws)
+    assert ((out.double() - a @ wide).abs() <= (d + 64) * 2.0 ** -24 * (a.abs() @ wide.abs())).all()

@@ -116,6 +116,13 @@ def test_quantize_act_t_and_swiglu8():
     assert b(4, 128, P[0], P[1], P[2], P[1], P[4]) == INVALID and b(4, 128, P[0], P[1], P[2], P[3], P[0]) == INVALID
 
 
+def test_weights_in_16s_can_be_quantised():
+    """Every n that moe_matmul_fp8 takes."""
+    w = lambda n, r, c: lib.moe_quantize_weights(n, r, c, None, None, None, None)  # noqa: E731
+    assert w(0, 144, 256) == OK and w(0, 128, 16) == OK
+    assert w(1, 144, 256) == INVALID and w(1, 136, 128) == UNSUPPORTED and w(1, 128, 24) == UNSUPPORTED
+
+
 def test_swiglu8_outputs_in_one_place():
     """The codes and h may not share a buffer (both are written, by different lanes)."""
     assert lib.moe_swiglu_forward8(4, 128, P[0], P[1], P[1], P[3], None) == INVALID
