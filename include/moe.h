@@ -344,7 +344,7 @@ moe_status moe_gate_workspace_size(const moe_gate_config* config, size_t* bytes)
  * with entries +0 and -inf alone) ranks experts and groups by the logits, so that scores too small for
  * fp32 keep their order; other keys that are equal in fp32 count as ties.  T == 0 writes
  * expert_load = 0.
- * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512 or top_k > 32:
+ * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512, top_k > 32 or tokens * top_k >= 2^31:
  * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE if workspace_bytes is too small. */
 moe_status moe_gate(const moe_gate_config* config, const void* logits, const float* bias, int32_t* topk_idx,
                     float* topk_gate, int32_t* expert_load, void* workspace, size_t workspace_bytes,
