@@ -433,7 +433,10 @@ moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, con
  *
  * moe_saved8_size: bytes of the buffer that moe_forward_train8 writes (about half of
  * moe_saved_inputs_size: int8 codes and a scale per 128 values of every row's a and b, as
- * moe_swiglu_forward8 keeps them).  moe_train8_workspace_size: bytes of its workspace. */
+ * moe_swiglu_forward8 keeps them).  moe_train8_workspace_size: bytes of its workspace.  The gate/up
+ * products leave a and b in bf16 there, and a second pass packs them: where 2 * inter > hidden they
+ * do not fit into the place of the down products, and the workspace is larger than
+ * moe_workspace_size by moe_saved_inputs_size. */
 moe_status moe_saved8_size(const moe_shape* shape, size_t* bytes);
 moe_status moe_train8_workspace_size(const moe_shape* shape, size_t* bytes);
 
