@@ -401,8 +401,10 @@ moe_status moe_matmul_fp8(const moe_matmul_shape* shape, const uint8_t* a, const
 /* The operands of a weight gradient: x [rows, cols] bf16 transposed and quantised in runs of 128 rows:
  *   codes  [cols, R]      E4M3FN, R = rows rounded up to 128, rows past the last as zeros
  *   scales [cols, R/128]  fp32
- * the codes and scales that moe_quantize_act gives for the transpose: scale = amax/448 (1 for a run of
- * zeros), code = round-to-nearest-even E4M3FN of fp32(x / scale), saturating at 448.  cols must be a multiple of 8 (MOE_ERR_UNSUPPORTED), x and codes
+ * scale = amax * fp32(1/448) (1 for a run of zeros), code = round-to-nearest-even E4M3FN of
+ * fp32(x / scale), saturating at 448.  moe_quantize_act's scale is the quotient amax/448: for the
+ * transposed matrix its scales are up to one unit in the last place apart, and where they are a value
+ * near a rounding tie may have the neighbouring code.  cols must be a multiple of 8 (MOE_ERR_UNSUPPORTED), x and codes
  * 16-byte aligned (MOE_ERR_INVALID_ARG). */
 moe_status moe_quantize_act_t(int32_t rows, int32_t cols, const void* x_bf16, uint8_t* codes, float* scales,
                               hipStream_t stream);

@@ -115,11 +115,11 @@ def matmul_fp8(form, a, a_scale, b, b_scale):
 
 
 def run_scales(x, largest):
-    """fp32 scales of the runs of 128 along the rows: amax / largest, 1 for a run of zeros, NaN for a run that is not
-    finite.  (8-bit integers, whose largest is 127: amax times fp32(1 / 127).)"""
+    """fp32 scales of the runs of 128 along the rows: amax times fp32(1 / largest), 1 for a run of zeros, NaN for a
+    run that is not finite."""
     v = np.asarray(x, np.float32).reshape(x.shape[0], -1, BLOCK)
     amax = np.abs(v).max(axis=2)
-    scale = amax * (np.float32(1) / np.float32(127)) if largest == 127 else amax / np.float32(largest)
+    scale = (amax * (np.float32(1) / np.float32(largest))).astype(np.float32)
     scale = np.where(amax == 0, np.float32(1), scale)
     return np.where(np.isfinite(v).all(axis=2), scale, np.float32(np.nan))
 
