@@ -493,8 +493,8 @@ struct GateBwdArgs {
 
 // L lanes a token (16, or 32 for more than 16 picks).  The picks' lanes work out the gradients and put them into the
 // token's row in LDS, zero otherwise, from where it leaves in runs of four.  DENSE (a softmax whose gates are not
-// renormalised): every expert has one; C runs of four a lane.  Bound by memory: T=16384, 256 experts, 6.4 us for 26 MB,
-// dense 7.8 us for 35 MB.
+// renormalised): every expert has one; C runs of four a lane.  Bound by memory: T=16384, 256 experts, 6.4 to
+// 7.9 us for 26 MB, dense 7.8 us for 35 MB.
 constexpr int kBwdThreads = 256, kBwdWaves = kBwdThreads / 64;
 template <int L, int C, typename TL, bool SOFTMAX, bool DENSE>
 __global__ void __launch_bounds__(kBwdThreads) gate_bwd_kernel(GateBwdArgs a) {

@@ -13,7 +13,7 @@
 // row and run, the sum of dh H before the gate (its share of the gate's gradient).
 //
 // 16 lanes share one run of 128 features of a row, 8 features a lane: 16-byte loads and stores, the run's amax by
-// four row rotations.  Bound by memory: 32768 x 2048, forward 100 to 112 us for 541 MB, backward 116 to 121 us for 675 MB.
+// four row rotations.  Bound by memory: 32768 x 2048, forward 100 to 114 us for 541 MB, backward 116 to 121 us for 675 MB.
 #include "moe_internal.h"
 
 namespace moe {
