@@ -462,6 +462,133 @@ moe_status moe_backward_gates(const moe_shape* shape, const void* u, const moe_w
                               const moe_weight_grads* dw, void* workspace, size_t workspace_bytes,
                               hipStream_t stream);
 
+/* ---- The residual's addition and the norm before a layer -------------------------------------
+ * h = x + residual, and its root-mean-square norm y = h / sqrt(mean(h^2) + eps) * weight, as bf16 or
+ * fp32 and as the E4M3 codes that moe_matmul_fp8 takes. */
+typedef struct moe_norm_shape {
+  int32_t rows, cols;   /* rows >= 0; cols >= 8, a multiple of 8 (of 128 with codes), at most 32768 */
+  int32_t dtype;        /* MOE_DTYPE_F32 or MOE_DTYPE_BF16: x, residual, sum, y and their gradients */
+  float eps;            /* >= 0, finite */
+  int64_t x_ld;         /* elements between rows of x, residual, sum, h, d_sum and d_x; 0: cols */
+  int64_t y_ld;         /* elements between rows of y and d_y; 0: cols (both multiples of 8) */
+} moe_norm_shape;
+
+/* Bytes of device workspace that moe_norm_backward needs for `shape` (moe_norm_forward needs none). */
+moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
+
+/*   x         [rows, cols]
+ *   residual  [rows, cols], or NULL (h = x)
+ *   weight    [cols]  fp32
+ *   sum       [rows, cols] out: h, rounded to the type, which is what the norm is taken of; may be x or
+ *             residual itself; NULL: not kept.  NULL without a residual
+ *   y         [rows, cols] out, or NULL
+ *   codes     [rows, cols] out: E4M3FN, and scales [rows, cols/128] fp32: scale = amax/448 of the run
+ *             of 128 (1 for zeros), code = round-to-nearest-even E4M3FN of fp32(y / scale), from y
+ *             before its rounding to the type; both or neither NULL.  y or codes is needed
+ *   rstd      [rows] fp32 out: 1 / sqrt(mean(h^2) + eps), for moe_norm_backward; may be NULL
+ * Squares and sums are fp32: a row whose sum of squares passes 3.4e38 has rstd 0, and a row of zeros
+ * under eps = 0 is NaN.  A row's results do not depend on the other rows.  No buffer is another's, but for sum as above;
+ * x_ld and y_ld are multiples of 8, and all pointers but rstd and scales multiples of 16.
+ * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, a negative size, ld < cols, buffers in
+ * place of one another), MOE_ERR_UNSUPPORTED (other limits). */
+moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const void* residual, const float* weight,
+                            void* sum, void* y, uint8_t* codes, float* scales, float* rstd, hipStream_t stream);
+
+/* The gradient, from h (sum, or x without a residual) and rstd of moe_norm_forward.  With u = h rstd and
+ * g = d_y weight,
+ *   d_x       [rows, cols] out: rstd (g - u mean(g u)) + d_sum, the gradient of x and of residual alike;
+ *             may be d_sum itself
+ *   d_weight  [cols] fp32 out: the rows' sum of d_y u; NULL: not computed, and no workspace needed
+ *   d_y       [rows, cols]; d_sum [rows, cols]: the gradient that reaches `sum` from behind, or NULL
+ * rows == 0 gives d_weight zeros.  Errors as moe_norm_forward, MOE_ERR_WORKSPACE. */
+moe_status moe_norm_backward(const moe_norm_shape* shape, const void* d_y, const void* d_sum, const void* h,
+                             const float* weight, const float* rstd, void* d_x, float* d_weight, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream);
+
+/* ---- Balance loss of a router --------------------------------------------------------------------
+ * For callers who route with moe_gate or by themselves: for each sequence of L tokens,
+ *   p_t = softmax(l_t), or s_t / sum s_t with the sigmoid;   n_i = picks of expert i
+ *   loss = alpha sum_i (N n_i / (K L)) (sum_t p_{t,i} / L)
+ * (moe_route_balance's statistic), and its gradient with the picks held fixed.  A pick is an entry
+ * of topk_idx in [0, N); a token without one is padding: it is not in L and has no gradient. */
+typedef struct moe_balance_config {
+  int32_t tokens;        /* T >= 0 */
+  int32_t n_routed;      /* N: 1 to 512 */
+  int32_t top_k;         /* K: 1 to min(N, 32); tokens * top_k < 2^31 */
+  int32_t logits_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 (logits and their gradient) */
+  int32_t score;         /* moe_score */
+  int32_t n_seqs;        /* S >= 1 */
+  float alpha;           /* finite */
+  int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
+} moe_balance_config;
+
+/* Bytes of device workspace that moe_balance_loss needs for `config`. */
+moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* bytes);
+
+/*   logits      [T, N]  fp32 or bf16 (an expert at -inf has p = 0)
+ *   topk_idx    [T, K]  int32
+ *   seq_start   [S + 1] int32: sequence s is the tokens [seq_start[s], seq_start[s+1]), ascending, within
+ *               [0, T], empty ones allowed; tokens outside belong to no sequence.  NULL: one sequence,
+ *               all tokens (n_seqs == 1)
+ *   loss        [S]     fp32 out (0 for a sequence without tokens)
+ *   counts      [S, N]  int32 out: n_i
+ *   seq_tokens  [S]     int32 out: L
+ *   prob_sum    [S, N]  fp32 out, or NULL: sum_t p_{t,i}.  With counts, seq_tokens and prob_sum added up
+ *               over the ranks of a job, the loss of the whole batch is the formula above, and
+ *               moe_balance_backward takes the sums
+ * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512, top_k > 32 or tokens * top_k >= 2^31:
+ * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE. */
+moe_status moe_balance_loss(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
+                            const int32_t* seq_start, float* loss, int32_t* counts, int32_t* seq_tokens, float* prob_sum,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/* The gradient with respect to the logits:
+ *   logits, topk_idx, seq_start, counts, seq_tokens   as above
+ *   d_loss    [S]    fp32 dL/dloss
+ *   d_logits  [T, N] out, rows d_logits_ld apart (0: n_routed): fp32 or bf16 (rounded once).  accumulate
+ *             zero: every element written; non-zero: added to what is there (moe_gate_backward's), and rows without a
+ *             gradient are left as they are.  May not alias logits
+ * Errors as moe_balance_loss. */
+moe_status moe_balance_backward(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
+                                const int32_t* seq_start, const int32_t* counts, const int32_t* seq_tokens,
+                                const float* d_loss, void* d_logits, int64_t d_logits_ld, int32_t accumulate,
+                                hipStream_t stream);
+
+/* ---- Low-rank adapters of many requests ------------------------------------------------------------
+ * Beside a projection that all requests share (moe_matmul_fp8, or a library's): row t belongs to a
+ * request whose adapter is e = row_adapter[t], and
+ *   out_t = base_t + scale_e B_e (A_e x_t),
+ * the contraction over A_e's first ranks[e] rows.  Rows may come in any order; those of one adapter side by side
+ * (prompts) cost least.  For serving: there is no gradient. */
+typedef struct moe_adapter_shape {
+  int32_t rows;               /* T >= 0 */
+  int32_t in_cols, out_cols;  /* 8 to 2^20, multiples of 8 */
+  int32_t n_adapters;         /* n >= 1 */
+  int32_t rank;               /* r: rows of each A, columns of each B; 8 to 128, a multiple of 8 */
+  int32_t out_dtype;          /* MOE_DTYPE_BF16 or MOE_DTYPE_F32: base and out */
+  int64_t x_ld, base_ld, out_ld;   /* elements between rows; 0: dense; multiples of 8 */
+} moe_adapter_shape;
+
+/* Bytes of device workspace that moe_adapters needs for `shape`. */
+moe_status moe_adapters_workspace_size(const moe_adapter_shape* shape, size_t* bytes);
+
+/*   x            [T, in]     bf16
+ *   row_adapter  [T]         int32; outside [0, n): the row has no adapter and out is base
+ *   a            [n, r, in]  bf16;   b [n, out, r] bf16
+ *   scale        [n]         fp32
+ *   ranks        [n]         int32, 0 to r (others: the nearer of the two), what a and b hold from
+ *                            there on is not used; NULL: r for all
+ *   base         [T, out]    bf16 or fp32, or NULL (zeros); out may be base itself (equal strides)
+ *   out          [T, out]    the same type
+ * Sums are fp32 and the low-rank values keep 16 bits of their fp32 sums under a bf16 output, 24 under an fp32
+ * one.  A row's result is its own alone (an infinity or NaN in another row or adapter does not reach it).
+ * Errors: MOE_ERR_INVALID_ARG (null pointers, pointers that are not multiples of 16 (row_adapter, scale and
+ * ranks: of 4), strides below the row length, out in place of another operand), MOE_ERR_UNSUPPORTED
+ * (other limits), MOE_ERR_WORKSPACE. */
+moe_status moe_adapters(const moe_adapter_shape* shape, const void* x, const int32_t* row_adapter, const void* a,
+                        const void* b, const float* scale, const int32_t* ranks, const void* base, void* out,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static description of a status code (never NULL). */
 const char* moe_status_string(int32_t status);
 

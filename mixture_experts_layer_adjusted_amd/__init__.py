@@ -14,7 +14,10 @@ from .binding import (MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_FP8_B128, MOE_FOR
                       MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, GateConfig, MatmulShape, make_gate_config,
                       make_matmul_shape, moe_gate, moe_gate_backward, moe_gate_workspace_size, moe_matmul_fp8,
                       moe_matmul_fp8_workspace_size, moe_quantize_act_t, moe_swiglu_backward8, moe_swiglu_forward8,
-                      moe_backward_gates, moe_forward_train8, moe_saved8_size, moe_train8_workspace_size)
+                      moe_backward_gates, moe_forward_train8, moe_saved8_size, moe_train8_workspace_size,
+                      AdapterShape, BalanceConfig, NormShape, make_adapter_shape, make_balance_config, make_norm_shape,
+                      moe_adapters, moe_adapters_workspace_size, moe_balance_backward, moe_balance_loss,
+                      moe_balance_workspace_size, moe_norm_backward, moe_norm_forward, moe_norm_workspace_size)
 
 __all__ = ["MOE_DTYPE_BF16", "MOE_DTYPE_F32", "MOE_DTYPE_FP8_B128", "MOE_FORWARD_EVENTS", "MoeError", "Shape",
            "WeightGrads", "Weights", "make_shape", "make_weight_grads", "make_weights", "moe_backward",
@@ -27,4 +30,7 @@ __all__ = ["MOE_DTYPE_BF16", "MOE_DTYPE_F32", "MOE_DTYPE_FP8_B128", "MOE_FORWARD
            "MOE_SCORE_SIGMOID", "MOE_SCORE_SOFTMAX", "GateConfig", "MatmulShape", "make_gate_config",
            "make_matmul_shape", "moe_gate", "moe_gate_backward", "moe_gate_workspace_size", "moe_matmul_fp8",
            "moe_matmul_fp8_workspace_size", "moe_quantize_act_t", "moe_swiglu_backward8", "moe_swiglu_forward8",
-           "moe_backward_gates", "moe_forward_train8", "moe_saved8_size", "moe_train8_workspace_size"]
+           "moe_backward_gates", "moe_forward_train8", "moe_saved8_size", "moe_train8_workspace_size",
+           "AdapterShape", "BalanceConfig", "NormShape", "make_adapter_shape", "make_balance_config", "make_norm_shape",
+           "moe_adapters", "moe_adapters_workspace_size", "moe_balance_backward", "moe_balance_loss",
+           "moe_balance_workspace_size", "moe_norm_backward", "moe_norm_forward", "moe_norm_workspace_size"]

@@ -61,6 +61,21 @@ class MatmulShape(ctypes.Structure):
         (n, ctypes.c_int64) for n in ("lda", "ldb", "ldo")]
 
 
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x_ld", ctypes.c_int64), ("y_ld", ctypes.c_int64)]
+
+
+class BalanceConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_routed", "top_k", "logits_dtype", "score", "n_seqs")] + [
+        ("alpha", ctypes.c_float), ("logits_ld", ctypes.c_int64)]
+
+
+class AdapterShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("rows", "in_cols", "out_cols", "n_adapters", "rank", "out_dtype")] + [
+        (n, ctypes.c_int64) for n in ("x_ld", "base_ld", "out_ld")]
+
+
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built; run __graft_entry__.build() (hipcc, gfx950)")
 _lib = ctypes.CDLL(LIB_PATH)
@@ -104,6 +119,14 @@ _SIG = {
                            ctypes.c_size_t, _P],
     "moe_backward_gates": [ctypes.POINTER(Shape), _P, ctypes.POINTER(Weights), _P, _P, _P, ctypes.c_size_t, _P, _P, _P,
                            ctypes.POINTER(WeightGrads), _P, ctypes.c_size_t, _P],
+    "moe_norm_workspace_size": [ctypes.POINTER(NormShape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_norm_forward": [ctypes.POINTER(NormShape), _P, _P, _P, _P, _P, _P, _P, _P, _P],
+    "moe_norm_backward": [ctypes.POINTER(NormShape), _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_balance_workspace_size": [ctypes.POINTER(BalanceConfig), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_balance_loss": [ctypes.POINTER(BalanceConfig), _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+    "moe_balance_backward": [ctypes.POINTER(BalanceConfig), _P, _P, _P, _P, _P, _P, _P, ctypes.c_int64, ctypes.c_int32, _P],
+    "moe_adapters_workspace_size": [ctypes.POINTER(AdapterShape), ctypes.POINTER(ctypes.c_size_t)],
+    "moe_adapters": [ctypes.POINTER(AdapterShape), _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
     "moe_status_string": [ctypes.c_int32],
 }
 for _name, _args in _SIG.items():
@@ -356,6 +379,69 @@ def moe_backward_gates(shape, u, weights: Weights, topk_idx, topk_gate, saved8, 
         ctypes.byref(shape), _addr(u), ctypes.byref(weights), _addr(topk_idx), _addr(topk_gate), _addr(saved8),
         _nbytes(saved8), _addr(dout), _addr(du), _addr(d_gate), ctypes.byref(weight_grads), _addr(workspace),
         _nbytes(workspace), _stream(stream)))
+
+
+def make_norm_shape(rows, cols, dtype, eps, x_ld=0, y_ld=0) -> NormShape:
+    return NormShape(rows, cols, dtype, eps, x_ld, y_ld)
+
+
+def moe_norm_workspace_size(shape: NormShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_norm_workspace_size", _lib.moe_norm_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_norm_forward(shape, x, residual, weight, sum=None, y=None, codes=None, scales=None, rstd=None, stream=None):
+    _check("moe_norm_forward", _lib.moe_norm_forward(
+        ctypes.byref(shape), _addr(x), _addr(residual), _addr(weight), _addr(sum), _addr(y), _addr(codes), _addr(scales),
+        _addr(rstd), _stream(stream)))
+
+
+def moe_norm_backward(shape, d_y, d_sum, h, weight, rstd, d_x, d_weight=None, workspace=None, stream=None):
+    _check("moe_norm_backward", _lib.moe_norm_backward(
+        ctypes.byref(shape), _addr(d_y), _addr(d_sum), _addr(h), _addr(weight), _addr(rstd), _addr(d_x), _addr(d_weight),
+        _addr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def make_balance_config(tokens, n_routed, top_k, logits_dtype, score, n_seqs=1, alpha=1e-4, logits_ld=0) -> BalanceConfig:
+    return BalanceConfig(tokens, n_routed, top_k, logits_dtype, score, n_seqs, alpha, logits_ld)
+
+
+def moe_balance_workspace_size(config: BalanceConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_balance_workspace_size", _lib.moe_balance_workspace_size(ctypes.byref(config), ctypes.byref(n)))
+    return n.value
+
+
+def moe_balance_loss(config, logits, topk_idx, seq_start, loss, counts, seq_tokens, prob_sum, workspace, stream=None):
+    """seq_start: None for one sequence; prob_sum may be None."""
+    _check("moe_balance_loss", _lib.moe_balance_loss(
+        ctypes.byref(config), _addr(logits), _addr(topk_idx), _addr(seq_start), _addr(loss), _addr(counts),
+        _addr(seq_tokens), _addr(prob_sum), _addr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_balance_backward(config, logits, topk_idx, seq_start, counts, seq_tokens, d_loss, d_logits, d_logits_ld=0,
+                         accumulate=False, stream=None):
+    _check("moe_balance_backward", _lib.moe_balance_backward(
+        ctypes.byref(config), _addr(logits), _addr(topk_idx), _addr(seq_start), _addr(counts), _addr(seq_tokens),
+        _addr(d_loss), _addr(d_logits), d_logits_ld, accumulate, _stream(stream)))
+
+
+def make_adapter_shape(rows, in_cols, out_cols, n_adapters, rank, out_dtype, x_ld=0, base_ld=0, out_ld=0) -> AdapterShape:
+    return AdapterShape(rows, in_cols, out_cols, n_adapters, rank, out_dtype, x_ld, base_ld, out_ld)
+
+
+def moe_adapters_workspace_size(shape: AdapterShape) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_adapters_workspace_size", _lib.moe_adapters_workspace_size(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def moe_adapters(shape, x, row_adapter, a, b, scale, ranks, base, out, workspace, stream=None):
+    """ranks: None where every adapter has the whole rank; base: None for zeros, or out itself."""
+    _check("moe_adapters", _lib.moe_adapters(
+        ctypes.byref(shape), _addr(x), _addr(row_adapter), _addr(a), _addr(b), _addr(scale), _addr(ranks), _addr(base),
+        _addr(out), _addr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def moe_status_string(status: int) -> str:

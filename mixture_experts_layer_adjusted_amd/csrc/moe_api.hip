@@ -1054,6 +1054,152 @@ moe_status moe_swiglu_backward8(int32_t rows, int32_t inter, const void* dh, con
   return hip_status(launch_swiglu8_backward(rows, inter, dh, saved, scales, d_ab, h, stream));
 }
 
+static moe_status check_norm(const moe_norm_shape* s) {
+  if (!s || s->rows < 0 || s->cols < 1) return MOE_ERR_INVALID_ARG;
+  if (s->dtype != MOE_DTYPE_F32 && s->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (!(s->eps >= 0.0f) || !std::isfinite(s->eps)) return MOE_ERR_INVALID_ARG;
+  if ((s->x_ld != 0 && s->x_ld < s->cols) || (s->y_ld != 0 && s->y_ld < s->cols)) return MOE_ERR_INVALID_ARG;
+  if (s->cols % 8 != 0 || s->cols > 32768 || s->x_ld % 8 != 0 || s->y_ld % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes) {
+  moe_status rc = check_norm(shape);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = norm_workspace(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const void* residual, const float* weight,
+                            void* sum, void* y, uint8_t* codes, float* scales, float* rstd, hipStream_t stream) {
+  moe_status rc = check_norm(shape);
+  if (rc != MOE_OK) return rc;
+  if (codes && shape->cols % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (shape->rows == 0) return MOE_OK;
+  if (!x || !weight || (!y && !codes) || !codes != !scales || (sum && !residual)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x, residual, weight, sum, y, codes)) return MOE_ERR_INVALID_ARG;
+  const void* in[] = {x, residual, weight, sum};
+  const void* out[] = {y, codes, scales, rstd};
+  for (int i = 0; i < 4; ++i) {
+    for (const void* p : in)
+      if (out[i] && out[i] == p) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i] && out[i] == out[j]) return MOE_ERR_INVALID_ARG;
+  }
+  if (sum == weight) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_norm_forward(*shape, x, residual, weight, sum, y, codes, scales, rstd, stream));
+}
+
+moe_status moe_norm_backward(const moe_norm_shape* shape, const void* d_y, const void* d_sum, const void* h,
+                             const float* weight, const float* rstd, void* d_x, float* d_weight, void* workspace,
+                             size_t workspace_bytes, hipStream_t stream) {
+  moe_status rc = check_norm(shape);
+  if (rc != MOE_OK) return rc;
+  if (shape->rows == 0) return d_weight ? hip_status(launch_norm_backward(*shape, d_y, d_sum, h, weight, rstd, d_x, d_weight,
+                                                                          nullptr, stream))
+                                        : MOE_OK;
+  if (!d_y || !h || !weight || !rstd || !d_x) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_y, d_sum, h, weight, d_x, workspace)) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {d_y, h, static_cast<const void*>(weight), static_cast<const void*>(rstd)})
+    if (d_x == p || d_weight == p || (workspace && workspace == p)) return MOE_ERR_INVALID_ARG;
+  if (d_weight && (d_weight == d_x || d_weight == d_sum)) return MOE_ERR_INVALID_ARG;
+  const size_t need = d_weight ? norm_workspace(*shape) : 0;
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || workspace == d_x || workspace == d_sum || workspace == d_weight)) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_norm_backward(*shape, d_y, d_sum, h, weight, rstd, d_x, d_weight, static_cast<float*>(workspace),
+                                         stream));
+}
+
+static moe_status check_balance(const moe_balance_config* c) {
+  if (!c) return MOE_ERR_INVALID_ARG;
+  if (c->tokens < 0 || c->n_routed < 1 || c->top_k < 1 || c->top_k > c->n_routed || c->n_seqs < 1)
+    return MOE_ERR_INVALID_ARG;
+  if (c->logits_dtype != MOE_DTYPE_F32 && c->logits_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if (c->score != MOE_SCORE_SIGMOID && c->score != MOE_SCORE_SOFTMAX) return MOE_ERR_INVALID_ARG;
+  if (!std::isfinite(c->alpha)) return MOE_ERR_INVALID_ARG;
+  if (c->logits_ld != 0 && c->logits_ld < c->n_routed) return MOE_ERR_INVALID_ARG;
+  if (c->n_routed > kMaxRouted || c->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)c->tokens * c->top_k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* bytes) {
+  moe_status rc = check_balance(config);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = balance_workspace(*config);
+  return MOE_OK;
+}
+
+moe_status moe_balance_loss(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
+                            const int32_t* seq_start, float* loss, int32_t* counts, int32_t* seq_tokens, float* prob_sum,
+                            void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status rc = check_balance(config);
+  if (rc != MOE_OK) return rc;
+  if (!loss || !counts || !seq_tokens || (!seq_start && config->n_seqs != 1)) return MOE_ERR_INVALID_ARG;
+  if (config->tokens > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
+  const size_t need = balance_workspace(*config);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && (!workspace || !aligned16(workspace))) return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_balance_loss(*config, logits, topk_idx, seq_start, loss, counts, seq_tokens, prob_sum,
+                                        static_cast<float*>(workspace), stream));
+}
+
+moe_status moe_balance_backward(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
+                                const int32_t* seq_start, const int32_t* counts, const int32_t* seq_tokens,
+                                const float* d_loss, void* d_logits, int64_t d_logits_ld, int32_t accumulate,
+                                hipStream_t stream) {
+  moe_status rc = check_balance(config);
+  if (rc != MOE_OK) return rc;
+  if (d_logits_ld != 0 && d_logits_ld < config->n_routed) return MOE_ERR_INVALID_ARG;
+  if (!seq_start && config->n_seqs != 1) return MOE_ERR_INVALID_ARG;
+  if (config->tokens == 0) return MOE_OK;
+  if (!logits || !topk_idx || !counts || !seq_tokens || !d_loss || !d_logits || d_logits == logits)
+    return MOE_ERR_INVALID_ARG;
+  return hip_status(launch_balance_backward(*config, logits, topk_idx, seq_start, counts, seq_tokens, d_loss, d_logits,
+                                            d_logits_ld, accumulate != 0, stream));
+}
+
+static moe_status check_adapters(const moe_adapter_shape* s) {
+  if (!s || s->rows < 0 || s->in_cols < 1 || s->out_cols < 1 || s->n_adapters < 1 || s->rank < 1) return MOE_ERR_INVALID_ARG;
+  if (s->out_dtype != MOE_DTYPE_F32 && s->out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
+  if ((s->x_ld != 0 && s->x_ld < s->in_cols) || (s->base_ld != 0 && s->base_ld < s->out_cols) ||
+      (s->out_ld != 0 && s->out_ld < s->out_cols))
+    return MOE_ERR_INVALID_ARG;
+  if (s->in_cols % 8 != 0 || s->out_cols % 8 != 0 || s->rank % 8 != 0 || s->rank > 128) return MOE_ERR_UNSUPPORTED;
+  if (s->in_cols > (1 << 20) || s->out_cols > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (s->x_ld % 8 != 0 || s->base_ld % 8 != 0 || s->out_ld % 8 != 0) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_adapters_workspace_size(const moe_adapter_shape* shape, size_t* bytes) {
+  moe_status rc = check_adapters(shape);
+  if (rc != MOE_OK) return rc;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = adapters_workspace(*shape);
+  return MOE_OK;
+}
+
+moe_status moe_adapters(const moe_adapter_shape* shape, const void* x, const int32_t* row_adapter, const void* a,
+                        const void* b, const float* scale, const int32_t* ranks, const void* base, void* out,
+                        void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  moe_status rc = check_adapters(shape);
+  if (rc != MOE_OK) return rc;
+  if (shape->rows == 0) return MOE_OK;
+  if (!x || !row_adapter || !a || !b || !scale || !out || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x, a, b, base, out, workspace)) return MOE_ERR_INVALID_ARG;
+  if (out == x || out == a || out == b || out == workspace) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {static_cast<const void*>(row_adapter), static_cast<const void*>(scale), static_cast<const void*>(ranks)})
+    if (out == p || workspace == p) return MOE_ERR_INVALID_ARG;
+  const int64_t base_ld = shape->base_ld ? shape->base_ld : shape->out_cols;
+  const int64_t out_ld = shape->out_ld ? shape->out_ld : shape->out_cols;
+  if (out == base && base_ld != out_ld) return MOE_ERR_INVALID_ARG;
+  if (workspace_bytes < adapters_workspace(*shape)) return MOE_ERR_WORKSPACE;
+  return hip_status(launch_adapters(*shape, x, row_adapter, a, b, scale, ranks, base, out, static_cast<float*>(workspace),
+                                    stream));
+}
+
 const char* moe_status_string(int32_t status) {
   switch (status) {
     case MOE_OK: return "ok";

@@ -254,4 +254,27 @@ hipError_t launch_swiglu_bwd_saved8(const int8_t* codes, const float* scales, co
                                     const int32_t* row_token, const int32_t* row_end, int64_t max_rows, int I, void* dab,
                                     void* h, float* dg_part, hipStream_t st);
 
+// residual addition and root-mean-square norm (norm.hip); parts: the workspace
+size_t norm_workspace(const moe_norm_shape& s);
+hipError_t launch_norm_forward(const moe_norm_shape& s, const void* x, const void* residual, const float* weight, void* sum,
+                               void* y, uint8_t* codes, float* scales, float* rstd, hipStream_t st);
+hipError_t launch_norm_backward(const moe_norm_shape& s, const void* d_y, const void* d_sum, const void* h,
+                                const float* weight, const float* rstd, void* d_x, float* d_weight, float* parts,
+                                hipStream_t st);
+
+// balance loss from logits (balance.hip); places: the workspace; prob_sum may be null
+size_t balance_workspace(const moe_balance_config& c);
+hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
+                               float* loss, int32_t* counts, int32_t* tokens, float* prob_sum, float* places,
+                               hipStream_t st);
+hipError_t launch_balance_backward(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
+                                   const int32_t* counts, const int32_t* tokens, const float* d_loss, void* d_logits,
+                                   int64_t d_ld, bool add, hipStream_t st);
+
+// low-rank adapters (adapters.hip); low: the workspace
+size_t adapters_workspace(const moe_adapter_shape& s);
+hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int32_t* row_adapter, const void* a, const void* b,
+                           const float* scale, const int32_t* ranks, const void* base, void* out, float* low,
+                           hipStream_t st);
+
 }  // namespace moe
