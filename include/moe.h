@@ -566,7 +566,7 @@ typedef struct moe_adapter_shape {
   int32_t n_adapters;         /* n >= 1 */
   int32_t rank;               /* r: rows of each A, columns of each B; 8 to 128, a multiple of 8 */
   int32_t out_dtype;          /* MOE_DTYPE_BF16 or MOE_DTYPE_F32: base and out */
-  int64_t x_ld, base_ld, out_ld;   /* elements between rows; 0: dense; multiples of 8 */
+  int64_t x_ld, base_ld, out_ld;   /* elements between rows; 0: dense; multiples of 8, x_ld below 2^24 */
 } moe_adapter_shape;
 
 /* Bytes of device workspace that moe_adapters needs for `shape`. */

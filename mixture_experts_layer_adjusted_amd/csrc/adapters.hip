@@ -22,7 +22,9 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 16;        // rows of a tile
+constexpr int kStep = 64;        // values of a wavefront's step along the first product's contraction
 constexpr int kCols = 64;        // output columns of a wavefront at a time
+constexpr int kLeadRows = 128;   // rows at most where workgroups go by adapters
 
 struct AdapterArgs {
   const uint16_t* x;
@@ -65,49 +67,139 @@ __device__ __forceinline__ void for_adapters(int mine, F f) {
   }
 }
 
-// The first product, transposed: ranks are the matrix instruction's rows, tokens its columns, so that a lane holds four
-// neighbouring ranks of one token.  RT tiles of 16 ranks.  A workgroup's wavefronts take every fourth run of 32.
-template <int RT>
-__global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
-  __shared__ float place[kWaves][kRows][RT * 16 + 4];
-  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
-  const int64_t t0 = (int64_t)blockIdx.x * kRows, t = t0 + col;
-  const int begin = blockIdx.y * g.per_split, end = min(g.in, begin + g.per_split);
-  const int mine = adapter_of(g, t);
-  const uint16_t* x = g.x + (mine >= 0 ? t : 0) * g.x_ld;
-  f32x4 kept[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  for_adapters(mine, [&](int e) {
-    const int rank = rank_of(g, e);
-    const uint16_t* a = g.a + ((int64_t)e * g.r + col) * g.in;
-    f32x4 acc[RT];
-#pragma unroll
-    for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-    for (int k0 = begin + 32 * wave; k0 < end; k0 += 32 * kWaves) {
-      const int k = k0 + 8 * quad;
-      const bool in = k < end;
-      const bf16x8 xv = in && mine == e ? vector_at(x + k) : no_values();
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-        acc[j] = mfma(in && 16 * j + col < rank ? vector_at(a + (int64_t)16 * j * g.in + k) : no_values(), xv, acc[j]);
-    }
-    if (mine == e) {
-#pragma unroll
-      for (int j = 0; j < RT; ++j) kept[j] = acc[j];
-    }
-  });
-#pragma unroll
-  for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4*>(&place[wave][col][16 * j + 4 * quad]) = kept[j];
+// The rows of a workgroup that goes by adapters: blockIdx.x is a row, and if it is the first one with its adapter
+// (or the first without one) the workgroup takes all rows that have the same; otherwise there are none.
+struct LeadRows {
+  uint64_t match[kLeadRows / 64];
+  uint8_t row[kLeadRows];
+};
+__device__ __forceinline__ int lead_rows(const AdapterArgs& g, LeadRows& l) {
+  const int i = threadIdx.x, first = blockIdx.x;
+  const int e = adapter_of(g, first);
+  const bool same = i < kLeadRows && i < g.rows && adapter_of(g, i) == e;
+  const uint64_t m = __ballot(same);
+  if (i < kLeadRows && (i & 63) == 0) l.match[i >> 6] = m;
   __syncthreads();
-  for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
-    const int row = i / (RT * 4), c = i % (RT * 4) * 4;
-    if (t0 + row >= g.rows) continue;
-    f32x4 s = *reinterpret_cast<f32x4*>(&place[0][row][c]);
+  int count = 0, before = 0;
+  bool earlier = false;
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(&place[w][row][c]);
-    *reinterpret_cast<f32x4*>(g.low + ((int64_t)blockIdx.y * g.rows + t0 + row) * (RT * 16) + c) = s;
+  for (int w = 0; w < kLeadRows / 64; ++w) {
+    const uint64_t mask = l.match[w];
+    if (w < first >> 6) earlier |= mask != 0;
+    if (w == first >> 6) earlier |= (mask & ((uint64_t(1) << (first & 63)) - 1)) != 0;
+    if (w < i >> 6) before += __popcll(mask);
+    count += __popcll(mask);
+  }
+  if (earlier) return 0;
+  if (same) l.row[before + __popcll(m & ((uint64_t(1) << (i & 63)) - 1))] = (uint8_t)i;
+  __syncthreads();
+  return count;
+}
+
+// The operands of one step of the first product: 64 values along the contraction, two of the instruction's
+template <int RT>
+struct LowStep {
+  bf16x8 x[2], a[2][RT];
+};
+
+// The first product, transposed: ranks are the matrix instruction's rows, tokens its columns, so that a lane holds four
+// neighbouring ranks of one token.  RT tiles of 16 ranks.  A workgroup's wavefronts take every fourth run of 64.
+template <int RT, bool LEAD>
+__global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
+  constexpr int kAhead = RT == 1 ? 4 : RT == 2 ? 2 : 1;   // steps whose operands are in flight
+  __shared__ float place[kWaves][kRows][RT * 16 + 4];
+  __shared__ LeadRows lead;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int begin = blockIdx.y * g.per_split, end = min(g.in, begin + g.per_split);
+  int count = kRows;
+  if constexpr (LEAD) {
+    if (adapter_of(g, blockIdx.x) < 0) return;
+    count = lead_rows(g, lead);
+  }
+  for (int group = 0; group < count; group += kRows) {
+    int64_t t;
+    if constexpr (LEAD) t = group + col < count ? lead.row[group + col] : g.rows;
+    else t = (int64_t)blockIdx.x * kRows + col;
+    const int mine = adapter_of(g, t);
+    // (32-bit offsets from the first row of the tile, or of all)
+    const uint16_t* x = g.x + (LEAD ? 0 : (int64_t)blockIdx.x * kRows * g.x_ld);
+    const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
+    f32x4 kept[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for_adapters(mine, [&](int e) {
+      const int rank = rank_of(g, e);
+      if (rank == 0) return;
+      const uint16_t* a = g.a + (int64_t)e * g.r * g.in;
+      uint32_t row[RT];   // of A; rows past the rank repeat the last one, their sums are dropped
+#pragma unroll
+      for (int j = 0; j < RT; ++j) row[j] = (uint32_t)min(16 * j + col, rank - 1) * (uint32_t)g.in;
+      f32x4 acc[RT];
+#pragma unroll
+      for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      LowStep<RT> step[kAhead];
+      auto load = [&](LowStep<RT>& s, int k0) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k = k0 + 32 * h + 8 * quad;
+          s.x[h] = vector_at(x + (at + k));
+#pragma unroll
+          for (int j = 0; j < RT; ++j) s.a[h][j] = vector_at(a + (row[j] + k));
+        }
+      };
+      auto multiply = [&](const LowStep<RT>& s) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int j = 0; j < RT; ++j) acc[j] = mfma(s.a[h][j], s.x[h], acc[j]);
+      };
+      constexpr int kStride = kStep * kWaves;
+      const int first = begin + kStep * wave, last = end - kStep;   // last: where a whole step can begin
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d)
+        if (first + d * kStride <= last) load(step[d], first + d * kStride);
+      int k0 = first;
+      for (; k0 <= last; k0 += kAhead * kStride) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          const int k = k0 + d * kStride;
+          if (k <= last) multiply(step[d]);
+          if (k + kAhead * kStride <= last) load(step[d], k + kAhead * kStride);
+        }
+      }
+      const int tail = first + (last >= first ? (last - first) / kStride + 1 : 0) * kStride;
+      if (tail < end) {   // the contraction ends inside this step
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t k = tail + 32 * h + 8 * quad;
+          const bool in = (int)k < end;
+          const bf16x8 xv = in ? vector_at(x + (at + k)) : no_values();
+#pragma unroll
+          for (int j = 0; j < RT; ++j) acc[j] = mfma(in ? vector_at(a + (row[j] + k)) : no_values(), xv, acc[j]);
+        }
+      }
+      if (mine == e) {
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) kept[j][i] = 16 * j + 4 * quad + i < rank ? acc[j][i] : 0.0f;
+      }
+    });
+    if (LEAD && group > 0) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4*>(&place[wave][col][16 * j + 4 * quad]) = kept[j];
+    __syncthreads();
+    for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
+      const int row = i / (RT * 4), c = i % (RT * 4) * 4;
+      int64_t to;
+      if constexpr (LEAD) to = group + row < count ? lead.row[group + row] : g.rows;
+      else to = (int64_t)blockIdx.x * kRows + row;
+      if (to >= g.rows) continue;
+      f32x4 s = *reinterpret_cast<f32x4*>(&place[0][row][c]);
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(&place[w][row][c]);
+      *reinterpret_cast<f32x4*>(g.low + ((int64_t)blockIdx.y * g.rows + to) * (RT * 16) + c) = s;
+    }
   }
 }
 
@@ -124,135 +216,183 @@ __device__ __forceinline__ bf16x8 part_of(float (&v)[8]) {
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
+// Eight values of base, as they lie in memory
+template <typename T>
+struct alignas(16) Raw8 {
+  T v[8];
+};
+__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)r.v[i] << 16);
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = r.v[i];
+}
+
 // The second product, transposed as well: output columns are the instruction's rows, in an order that leaves a lane 16
 // neighbouring columns of its token (row m of tile j is column 16 (m / 4) + 4 j + m % 4 of the wavefront's 64).
 // PARTS bf16 parts of the low-rank values.  RT == 1: one run of 32 holds two parts.
-template <int RT, int PARTS, typename T>
+template <int RT, int PARTS, typename T, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
-  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = threadIdx.x >> 6;
-  const int64_t t = (int64_t)blockIdx.x * kRows + col;
-  const int mine = adapter_of(g, t);
-  bf16x8 low[kSteps];
-  {
-    const float factor = mine >= 0 ? g.scale[mine] : 0.0f;
+  constexpr int kQuads = kRows * RT * 4;                            // groups of four low-rank values of a tile
+  constexpr int kShare = kThreads / kQuads > 1 ? kThreads / kQuads : 1;   // threads that share one's slices
+  constexpr int kBatch = 8;                                         // slices loaded at once
+  __shared__ float place[kShare][kRows][RT * 16 + 4];
+  __shared__ LeadRows lead;
+  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int first = blockIdx.y * g.per_block + kCols * wave, end = min(g.outs, (int)(blockIdx.y + 1) * g.per_block);
+  int count = kRows;
+  if constexpr (LEAD) count = lead_rows(g, lead);
+  for (int group = 0; group < count; group += kRows) {
+    auto row_of = [&](int i) -> int64_t {
+      if constexpr (LEAD) return group + i < count ? lead.row[group + i] : g.rows;
+      else return (int64_t)blockIdx.x * kRows + i;
+    };
+    const int64_t t = row_of(col);
+    const int mine = adapter_of(g, t);
+    const bool any = __ballot(mine >= 0) != 0;
+    auto load_base = [&](Raw8<T> (&v)[2], int c0) {
 #pragma unroll
-    for (int run = 0; run < kRuns; ++run) {
-      const int rank = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
-      float v[8];
+      for (int h = 0; h < 2; ++h) {
+        const int c = c0 + 16 * quad + 8 * h;
+        const bool in = g.base && c0 < end && t < g.rows && c < g.outs;
+        v[h] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(g.base) + t * g.base_ld + c) : Raw8<T>{};
+      }
+    };
+    Raw8<T> base[2];
+    load_base(base, first);
+    bf16x8 low[kSteps];
+    if (any) {   // (the wavefronts of a workgroup have the same rows)
+      if (LEAD && group > 0) __syncthreads();
+      // the slices' sums, slices shared out among threads and loaded in batches
+      for (int i = threadIdx.x; i < kQuads * kShare; i += kThreads) {
+        const int row = i % kQuads / (RT * 4), c = i % (RT * 4) * 4, share = i / kQuads;
+        const int64_t from = row_of(row);
+        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (from < g.rows) {
+          const float* p = g.low + from * (RT * 16) + c;
+          for (int s0 = share; s0 < g.splits; s0 += kShare * kBatch) {
+            f32x4 v[kBatch];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      if (mine >= 0) {
-        const float* p = g.low + t * (RT * 16) + rank;
-        for (int s = 0; s < g.splits; ++s) {
-          float u[8];
-          load8(p + (int64_t)s * g.rows * (RT * 16), u);
+            for (int b = 0; b < kBatch; ++b)
+              v[b] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + b * kShare, g.splits - 1) * g.rows * (RT * 16));
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] += u[i];
+            for (int b = 0; b < kBatch; ++b) sum += s0 + b * kShare < g.splits ? v[b] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] *= factor;
+        *reinterpret_cast<f32x4*>(&place[share][row][c]) = sum;
       }
-      if constexpr (RT == 1) {
-        bf16x8 part[2 * kSteps];
+      __syncthreads();
+      const float factor = mine >= 0 ? g.scale[mine] : 0.0f;
 #pragma unroll
-        for (int p = 0; p < 2 * kSteps; ++p) part[p] = p < PARTS ? part_of(v) : no_values();
+      for (int run = 0; run < kRuns; ++run) {
+        const int rank = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
+        float v[8];
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) low[s] = quad < 2 ? part[2 * s] : part[2 * s + 1];
-      } else {
+        for (int i = 0; i < 8; ++i) {
+          v[i] = place[0][col][rank + i];
 #pragma unroll
-        for (int p = 0; p < PARTS; ++p) low[p * kRuns + run] = part_of(v);
+          for (int w = 1; w < kShare; ++w) v[i] += place[w][col][rank + i];
+          v[i] = mine >= 0 ? v[i] * factor : 0.0f;
+        }
+        if constexpr (RT == 1) {
+#pragma unroll
+          for (int s = 0; s < kSteps; ++s) {   // the lower half of the lanes has one part, the upper half the next
+            const bf16x8 even = part_of(v), odd = 2 * s + 1 < PARTS ? part_of(v) : no_values();
+            low[s] = quad < 2 ? even : odd;
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < PARTS; ++p) low[p * kRuns + run] = part_of(v);
+        }
       }
     }
-  }
-  const int first = blockIdx.y * g.per_block, end = min(g.outs, first + g.per_block);
-  for (int c0 = first + kCols * wave; c0 < end; c0 += kCols * kWaves) {
-    const int c = c0 + 16 * quad;   // the lane's 16 columns
-    float was[16];
+    for (int c0 = first; c0 < end; c0 += kCols * kWaves) {
+      f32x4 kept[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-      if (g.base && t < g.rows && c + 8 * h < g.outs) {
-        load8(static_cast<const T*>(g.base) + t * g.base_ld + c + 8 * h, v);
-      } else {
+      for (int j = 0; j < 4; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      Raw8<T> next[2];
+      load_base(next, c0 + kCols * kWaves);
+      for_adapters(mine, [&](int e) {
+        const int rank = rank_of(g, e);
+        const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
+        bf16x8 bv[4][kRuns];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      }
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t bc = (uint32_t)min(c0 + 16 * (col >> 2) + 4 * j + (col & 3), g.outs - 1) * (uint32_t)g.r;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) was[8 * h + i] = v[i];
-    }
-    f32x4 kept[4];
+          for (int run = 0; run < kRuns; ++run) {
+            const int k = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
+            bv[j][run] = vector_at(b + (bc + (uint32_t)min(k, g.r - 8)));
+          }
+        }
+        if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
 #pragma unroll
-    for (int j = 0; j < 4; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for_adapters(mine, [&](int e) {
-      const int rank = rank_of(g, e);
-      f32x4 acc[4];
+          for (int run = 0; run < kRuns; ++run) {
+            const int left = rank - (RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int bc = c0 + 16 * (col >> 2) + 4 * j + (col & 3);
-        const uint16_t* b = g.b + ((int64_t)e * g.outs + bc) * g.r;
-        acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        bf16x8 bv[kRuns];
+            for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int run = 0; run < kRuns; ++run) {
-          const int k = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
-          bv[run] = bc < g.outs && k < rank ? vector_at(b + k) : no_values();
-          if (k < rank && k + 8 > rank) {   // the rank ends inside: what is behind it does not count, whatever it holds
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (k + i >= rank) bv[run][i] = (__bf16)0.0f;
+              for (int i = 0; i < 8; ++i)
+                if (i >= left) bv[j][run][i] = (__bf16)0.0f;
           }
         }
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) acc[j] = mfma(bv[RT == 1 ? 0 : s % kRuns], low[s], acc[j]);
-      }
-      if (mine == e) {
+        for (int j = 0; j < 4; ++j) {
+          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) kept[j] = acc[j];
-      }
-    });
-    if (t >= g.rows) continue;
+          for (int s = 0; s < kSteps; ++s) acc = mfma(bv[j][RT == 1 ? 0 : s % kRuns], low[s], acc);
+          if (mine == e) kept[j] = acc;
+        }
+      });
+      const int c = c0 + 16 * quad;   // the lane's 16 columns
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (c + 8 * h >= g.outs) continue;
-      float v[8];
+      for (int h = 0; h < 2; ++h) {
+        if (t >= g.rows || c + 8 * h >= g.outs) continue;
+        float v[8];
+        T* to = static_cast<T*>(g.out) + t * g.out_ld + c + 8 * h;
+        unpack8(base[h], v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {   // (a row without an adapter keeps its base to the sign of a zero)
-        const float d = kept[2 * h + i / 4][i % 4];
-        v[i] = mine >= 0 ? was[8 * h + i] + d : was[8 * h + i];
+        for (int i = 0; i < 8; ++i)   // (a row without an adapter keeps its base to the sign of a zero)
+          v[i] = mine >= 0 ? v[i] + kept[2 * h + i / 4][i % 4] : v[i];
+        store8(to, v);
+        base[h] = next[h];
       }
-      store8(static_cast<T*>(g.out) + t * g.out_ld + c + 8 * h, v);
     }
   }
 }
 
 struct AdapterPlan {
   int tiles16;                   // RT
+  bool lead;                     // workgroups go by adapters
   int splits, per_split, per_block;
 };
 
-// Slices of the first product: some 512 workgroups, each of 256 values at least.
 AdapterPlan plan_of(const moe_adapter_shape& s) {
   AdapterPlan p;
   p.tiles16 = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : s.rank <= 64 ? 4 : 8;
-  const int64_t tiles = ceil_div(s.rows, kRows);
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(512, std::max<int64_t>(1, tiles)), ceil_div(s.in_cols, 256)));
-  p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), 128) * 128);
+  p.lead = s.rows <= kLeadRows;
+  const int64_t tiles = std::max<int64_t>(1, ceil_div(s.rows, kRows)), run = kStep * kWaves;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));
+  p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
-  int64_t blocks = ceil_div(1024, std::max<int64_t>(1, tiles));
+  const int64_t blocks = ceil_div(2048, tiles);
   p.per_block = (int)(ceil_div(ceil_div(s.out_cols, blocks), kCols * kWaves) * kCols * kWaves);
   return p;
 }
 
-template <int RT>
+template <int RT, bool LEAD>
 hipError_t run_t(const AdapterArgs& g, int out_dtype, hipStream_t st) {
-  const unsigned tiles = (unsigned)ceil_div(g.rows, kRows);
-  const hipError_t err = launch_kernel(adapters_low_kernel<RT>, dim3(tiles, (unsigned)g.splits), dim3(kThreads), 0, st, g);
+  const unsigned tiles = (unsigned)(LEAD ? g.rows : ceil_div(g.rows, kRows));
+  const hipError_t err = launch_kernel(adapters_low_kernel<RT, LEAD>, dim3(tiles, (unsigned)g.splits), dim3(kThreads), 0, st, g);
   if (err != hipSuccess) return err;
   const dim3 grid(tiles, (unsigned)ceil_div(g.outs, g.per_block));
-  return out_dtype == MOE_DTYPE_F32 ? launch_kernel(adapters_out_kernel<RT, 3, float>, grid, dim3(kThreads), 0, st, g)
-                                    : launch_kernel(adapters_out_kernel<RT, 2, uint16_t>, grid, dim3(kThreads), 0, st, g);
+  return out_dtype == MOE_DTYPE_F32
+             ? launch_kernel(adapters_out_kernel<RT, 3, float, LEAD>, grid, dim3(kThreads), 0, st, g)
+             : launch_kernel(adapters_out_kernel<RT, 2, uint16_t, LEAD>, grid, dim3(kThreads), 0, st, g);
 }
 
 }  // namespace
@@ -287,10 +427,10 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       p.per_split,
                       p.per_block};
   switch (p.tiles16) {
-    case 1: return run_t<1>(g, s.out_dtype, st);
-    case 2: return run_t<2>(g, s.out_dtype, st);
-    case 4: return run_t<4>(g, s.out_dtype, st);
-    default: return run_t<8>(g, s.out_dtype, st);
+    case 1: return p.lead ? run_t<1, true>(g, s.out_dtype, st) : run_t<1, false>(g, s.out_dtype, st);
+    case 2: return p.lead ? run_t<2, true>(g, s.out_dtype, st) : run_t<2, false>(g, s.out_dtype, st);
+    case 4: return p.lead ? run_t<4, true>(g, s.out_dtype, st) : run_t<4, false>(g, s.out_dtype, st);
+    default: return p.lead ? run_t<8, true>(g, s.out_dtype, st) : run_t<8, false>(g, s.out_dtype, st);
   }
 }
 

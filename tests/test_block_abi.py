@@ -131,7 +131,7 @@ def adapters(**kw):
     (dict(out_ld=504), INVALID), (dict(in_cols=252), UNSUPPORTED), (dict(out_cols=500), UNSUPPORTED),
     (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(in_cols=(1 << 20) + 8), UNSUPPORTED),
     (dict(out_cols=(1 << 20) + 8), UNSUPPORTED), (dict(x_ld=260), UNSUPPORTED), (dict(base_ld=516), UNSUPPORTED),
-    (dict(out_ld=513), UNSUPPORTED), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
+    (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
 ])
 def test_adapter_limits(kw, status):
     s, n = adapters(**kw), ctypes.c_size_t(0)
