@@ -18,7 +18,6 @@ namespace moe {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 16;        // rows of a tile
@@ -214,20 +213,6 @@ __device__ __forceinline__ bf16x8 part_of(float (&v)[8]) {
     v[2 * i + 1] = fabsf(hi) < __builtin_inff() ? v[2 * i + 1] - hi : 0.0f;
   }
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
-}
-
-// Eight values of base, as they lie in memory
-template <typename T>
-struct alignas(16) Raw8 {
-  T v[8];
-};
-__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)r.v[i] << 16);
-}
-__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = r.v[i];
 }
 
 // The second product, transposed as well: output columns are the instruction's rows, in an order that leaves a lane 16

@@ -22,6 +22,8 @@
 namespace moe {
 namespace {
 
+constexpr int kParts = 256;   // workgroups of a backward pass at most, one a CU
+
 struct NormArgs {
   const void *x, *residual;
   const float* weight;
@@ -76,67 +78,62 @@ __device__ __forceinline__ float run_amax(const float (&v)[8]) {
   return fmaxf(m, __uint_as_float(turned<0x121>(__float_as_uint(m))));
 }
 
-// V vectors of eight a lane; WAVE: a row to a wavefront
-template <typename T, int V, bool WAVE>
-__global__ void __launch_bounds__(WAVE ? 256 : 1024) norm_fwd_kernel(NormArgs a) {
+// V vectors of eight a lane; MOST: threads of a workgroup at most, 64: a row to a wavefront.  One row each: rows that a
+// workgroup goes through with the next one's values on their way measured 5.1 TB/s against 5.6 (16384 x 7168).
+template <typename T, int V, int MOST>
+__global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormArgs a) {
+  constexpr bool WAVE = MOST == 64;
   __shared__ float place[2][16];
   const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int per = WAVE ? blockDim.x >> 6 : 1;   // rows of the workgroup at a time
-  const int first = WAVE ? threadIdx.x >> 6 : 0;
-  const float n = (float)a.cols;
-  int at = 0;
-  for (int64_t r = (int64_t)blockIdx.x * per + first; r < a.rows; r += (int64_t)gridDim.x * per, at ^= 1) {
-    const T* x = static_cast<const T*>(a.x) + r * a.x_ld;
-    float h[V][8];
+  const int64_t r = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  if (r >= a.rows) return;
+  Raw8<T> x[V], res[V];
+  float w[V][8], h[V][8], part[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * lanes + lane) * 8;
-      if (c < a.cols) load8(x + c, h[j]);
-      else
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * lanes + lane) * 8;
+    const bool in = c < a.cols;
+    x[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.x) + r * a.x_ld + c) : Raw8<T>{};
+    if (a.residual)
+      res[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.residual) + r * a.x_ld + c) : Raw8<T>{};
+  }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] = 0.0f;
-    }
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * lanes + lane) * 8;
+    if (c < a.cols) load8(a.weight + c, w[j]);
+  }
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    unpack8(x[j], h[j]);
     if (a.residual) {
-      const T* res = static_cast<const T*>(a.residual) + r * a.x_ld;
+      float v[8];
+      unpack8(res[j], v);
 #pragma unroll
-      for (int j = 0; j < V; ++j) {
-        const int c = (j * lanes + lane) * 8;
-        float v[8];
-        if (c < a.cols) {
-          load8(res + c, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[j][i] += v[i];
-          round8<T>(h[j]);
-        }
-      }
+      for (int i = 0; i < 8; ++i) h[j][i] += v[i];
+      round8<T>(h[j]);
     }
-    float part[V];
+    float sq[8];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      float sq[8];
+    for (int i = 0; i < 8; ++i) sq[i] = h[j][i] * h[j][i];
+    part[j] = sum_run<8>(sq);
+  }
+  const float rstd = 1.0f / sqrtf(row_sum<WAVE>(sum_run<V>(part), place, 0) / (float)a.cols + a.eps);
+  if (a.rstd && lane == 0) a.rstd[r] = rstd;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sq[i] = h[j][i] * h[j][i];
-      part[j] = sum_run<8>(sq);
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<WAVE>(sum_run<V>(part), place, at) / n + a.eps);
-    if (a.rstd && lane == 0) a.rstd[r] = rstd;
+  for (int j = 0; j < V; ++j) {
+    const int c = (j * lanes + lane) * 8;
+    const bool in = c < a.cols;   // (with codes: of the 16 lanes of a run all or none)
+    if (!in) continue;
+    if (a.sum) store8(static_cast<T*>(a.sum) + r * a.x_ld + c, h[j]);
+    float y[8];
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const int c = (j * lanes + lane) * 8;
-      const bool in = c < a.cols;   // (with codes: of the 16 lanes of a run all or none)
-      if (!in) continue;
-      if (a.sum) store8(static_cast<T*>(a.sum) + r * a.x_ld + c, h[j]);
-      float w[8], y[8];
-      load8(a.weight + c, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = h[j][i] * rstd * w[i];
-      if (a.y) store8(static_cast<T*>(a.y) + r * a.y_ld + c, y);
-      if (a.codes) {
-        const float amax = run_amax(y);
-        const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
-        *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = e4m3_codes8(y, scale);
-        if ((lane & 15) == 0) a.scales[r * (a.cols / 128) + c / 128] = scale;
-      }
+    for (int i = 0; i < 8; ++i) y[i] = h[j][i] * rstd * w[j][i];
+    if (a.y) store8(static_cast<T*>(a.y) + r * a.y_ld + c, y);
+    if (a.codes) {
+      const float amax = run_amax(y);
+      const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = e4m3_codes8(y, scale);
+      if ((lane & 15) == 0) a.scales[r * (a.cols / 128) + c / 128] = scale;
     }
   }
 }
@@ -145,48 +142,74 @@ struct NormBwdArgs {
   const void *d_y, *d_sum, *h;
   const float *weight, *rstd;
   void* d_x;
-  float* parts;   // [gridDim.x * rows at a time, cols], or null
+  float* parts;   // [gridDim.x, cols], or null
   int64_t rows, x_ld, y_ld;
   int cols;
 };
 
-template <typename T, int V, bool WAVE>
-__global__ void __launch_bounds__(WAVE ? 256 : 1024) norm_bwd_kernel(NormBwdArgs a) {
+// kAhead: a workgroup goes through its rows with the next one's values on their way, which lets one workgroup a CU reach what
+// the memory gives (16384 x 7168, bf16: 169 us with 256 workgroups, 5.6 TB/s; 183 with 512; 230 with one row each).  Where
+// the registers do not hold both rows, they are loaded one after the other.
+template <typename T, int V, int MOST>
+__global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormBwdArgs a) {
+  constexpr bool WAVE = MOST == 64, kAhead = MOST == 512 || (WAVE && V * sizeof(T) <= 8);
   __shared__ float place[2][16];
   const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int per = WAVE ? blockDim.x >> 6 : 1;
   const int first = WAVE ? threadIdx.x >> 6 : 0;
+  const int64_t step = (int64_t)gridDim.x * per;
   const float n = (float)a.cols;
-  float dw[V][8];
-#pragma unroll
-  for (int j = 0; j < V; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-  int at = 0;
-  for (int64_t r = (int64_t)blockIdx.x * per + first; r < a.rows; r += (int64_t)gridDim.x * per, at ^= 1) {
-    const T* h = static_cast<const T*>(a.h) + r * a.x_ld;
-    const T* d_y = static_cast<const T*>(a.d_y) + r * a.y_ld;
-    const float rstd = a.rstd[r];
-    float u[V][8], g[V][8], part[V];
+  float dw[V][8], w[V][8];
+  Raw8<T> h[V], d_y[V], d_sum[V];
+  float next_rstd = 0.0f;
+  auto load = [&](int64_t r) {
+    next_rstd = a.rstd[r];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       const int c = (j * lanes + lane) * 8;
-      part[j] = 0.0f;
-      if (c < a.cols) {
-        float w[8], p[8];
-        load8(h + c, u[j]);
-        load8(d_y + c, g[j]);
-        load8(a.weight + c, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          u[j][i] *= rstd;
-          dw[j][i] = fmaf(g[j][i], u[j][i], dw[j][i]);
-          g[j][i] *= w[i];
-          p[i] = g[j][i] * u[j][i];
-        }
-        part[j] = sum_run<8>(p);
-      }
+      const bool in = c < a.cols;
+      h[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.h) + r * a.x_ld + c) : Raw8<T>{};
+      d_y[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.d_y) + r * a.y_ld + c) : Raw8<T>{};
+      d_sum[j] = in && a.d_sum ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.d_sum) + r * a.x_ld + c) : Raw8<T>{};
     }
+  };
+  int64_t r = (int64_t)blockIdx.x * per + first;
+  if (kAhead && r < a.rows) load(r);
+  auto weights = [&](int j) {
+    const int c = (j * lanes + lane) * 8;
+    if (c < a.cols) load8(a.weight + c, w[j]);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[j][i] = 0.0f;
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
+    if constexpr (kAhead) weights(j);
+  }
+  for (int at = 0; r < a.rows; r += step, at ^= 1) {
+    if constexpr (!kAhead) load(r);
+    const float rstd = next_rstd;
+    float u[V][8], g[V][8], part[V];
+    Raw8<T> behind[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      float p[8];
+      if constexpr (!kAhead) weights(j);
+      unpack8(h[j], u[j]);
+      unpack8(d_y[j], g[j]);
+      behind[j] = d_sum[j];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        u[j][i] *= rstd;
+        dw[j][i] = fmaf(g[j][i], u[j][i], dw[j][i]);
+        g[j][i] *= w[j][i];
+        p[i] = g[j][i] * u[j][i];
+      }
+      part[j] = sum_run<8>(p);
+    }
+    if (kAhead && r + step < a.rows) load(r + step);
     const float mean = row_sum<WAVE>(sum_run<V>(part), place, at) / n;
     T* d_x = static_cast<T*>(a.d_x) + r * a.x_ld;
 #pragma unroll
@@ -194,35 +217,54 @@ __global__ void __launch_bounds__(WAVE ? 256 : 1024) norm_bwd_kernel(NormBwdArgs
       const int c = (j * lanes + lane) * 8;
       if (c >= a.cols) continue;
       float d[8];
-      if (a.d_sum) load8(static_cast<const T*>(a.d_sum) + r * a.x_ld + c, d);
-      else
-#pragma unroll
-        for (int i = 0; i < 8; ++i) d[i] = 0.0f;
+      unpack8(behind[j], d);
 #pragma unroll
       for (int i = 0; i < 8; ++i) d[i] += rstd * (g[j][i] - u[j][i] * mean);
       store8(d_x + c, d);
     }
   }
   if (!a.parts) return;
-  float* mine = a.parts + ((int64_t)blockIdx.x * per + first) * a.cols;
+  float* mine = a.parts + (int64_t)blockIdx.x * a.cols;
+  if constexpr (WAVE) {   // the four wavefronts' sums, in their order
+    __shared__ float sums[4][V * 512];
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = (j * lanes + lane) * 8;
-    if (c < a.cols) store8(mine + c, dw[j]);
+    for (int j = 0; j < V; ++j) store8(&sums[first][(j * 64 + lane) * 8], dw[j]);
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < a.cols; c += 1024) {
+      f32x4 v = *reinterpret_cast<f32x4*>(&sums[0][c]);
+#pragma unroll
+      for (int w = 1; w < 4; ++w) v += *reinterpret_cast<f32x4*>(&sums[w][c]);
+      *reinterpret_cast<f32x4*>(mine + c) = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int c = (j * lanes + lane) * 8;
+      if (c < a.cols) store8(mine + c, dw[j]);
+    }
   }
 }
 
-// d_weight from `count` rows of partial sums: 64 columns a workgroup, its 16 wavefronts every 16th row
+// d_weight from `count` rows of partial sums: 16 columns a workgroup, 64 threads a column, every 64th row a thread
 __global__ void __launch_bounds__(1024) norm_join_kernel(const float* __restrict__ parts, int count, int cols,
                                                          float* __restrict__ d_weight) {
-  __shared__ float place[16][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 64 + lane;
+  __shared__ float place[16][16];
+  constexpr int kBatch = 8;   // rows loaded at once
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, c = blockIdx.x * 16 + (lane & 15);
+  const int at = wave * 4 + (lane >> 4);
   float s = 0.0f;
-  if (c < cols)
-    for (int p = wave; p < count; p += 16) s += parts[(int64_t)p * cols + c];
-  place[wave][lane] = s;
+  for (int p0 = at; p0 < count; p0 += 64 * kBatch) {
+    float v[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) v[b] = parts[(int64_t)min(p0 + 64 * b, count - 1) * cols + min(c, cols - 1)];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) s += p0 + 64 * b < count ? v[b] : 0.0f;
+  }
+  s += __shfl_xor(s, 16, 64);
+  s += __shfl_xor(s, 32, 64);
+  if (lane < 16) place[wave][lane] = s;
   __syncthreads();
-  if (wave != 0 || c >= cols) return;
+  if (threadIdx.x >= 16 || c >= cols) return;
   float v[16];
 #pragma unroll
   for (int w = 0; w < 16; ++w) v[w] = place[w][lane];
@@ -234,56 +276,59 @@ __global__ void norm_zero_kernel(float* __restrict__ p, int n) {
   if (i < n) p[i] = 0.0f;
 }
 
-// How a row lies on lanes: wavefronts of a row, vectors of eight a lane.  By the row's length alone.
+// How a row lies on lanes: a wavefront up to 2048 values, a workgroup of up to 512 threads up to 8192, of up to 1024
+// beyond; vectors of eight a lane.  By the row's length alone.
 struct NormLanes {
-  int vectors;
-  bool wave;
+  int vectors, most;
   unsigned threads;   // of a workgroup
   int per;            // rows of a workgroup at a time
 };
 NormLanes lanes_of(int cols) {
   const int vecs = cols / 8;
-  if (vecs <= 64) return {1, true, 256, 4};
-  if (vecs <= 128) return {2, true, 256, 4};
-  if (vecs <= 256) return {4, true, 256, 4};
+  if (vecs <= 256) return {vecs <= 64 ? 1 : vecs <= 128 ? 2 : 4, 64, 256, 4};
   const int v = vecs <= 2048 ? 2 : 4;
-  return {v, false, (unsigned)(64 * ceil_div(vecs, 64 * v)), 1};
+  return {v, vecs <= 1024 ? 512 : 1024, (unsigned)(64 * ceil_div(vecs, 64 * v)), 1};
 }
 
-// Workgroups of a backward pass, each with its own sums of the weight's gradient: as many as keep those sums near 16 MB
-int64_t norm_blocks(const NormLanes& l, int64_t rows, int cols) {
-  const int64_t most = std::max<int64_t>(256, std::min<int64_t>(4096, (int64_t(1) << 22) / cols));
-  return std::min<int64_t>(ceil_div(rows, l.per), most / l.per);
+// f(vectors, most) as integral constants
+template <typename F>
+hipError_t with_lanes(const NormLanes& l, F f) {
+  using std::integral_constant;
+  if (l.most == 64) {
+    if (l.vectors == 1) return f(integral_constant<int, 1>{}, integral_constant<int, 64>{});
+    if (l.vectors == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 64>{});
+    return f(integral_constant<int, 4>{}, integral_constant<int, 64>{});
+  }
+  if (l.most == 512) return f(integral_constant<int, 2>{}, integral_constant<int, 512>{});
+  if (l.vectors == 2) return f(integral_constant<int, 2>{}, integral_constant<int, 1024>{});
+  return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
+}
+
+// Workgroups of a backward pass, each with its own sums of the weight's gradient
+int64_t norm_blocks(const NormLanes& l, int64_t rows) {
+  return std::min<int64_t>(ceil_div(rows, l.per), kParts);
 }
 
 template <typename T>
 hipError_t norm_forward_t(const NormLanes& l, const NormArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(a.rows, l.per), 1 << 20);
-  if (l.wave) {
-    if (l.vectors == 1) return launch_kernel(norm_fwd_kernel<T, 1, true>, dim3(grid), dim3(l.threads), 0, st, a);
-    if (l.vectors == 2) return launch_kernel(norm_fwd_kernel<T, 2, true>, dim3(grid), dim3(l.threads), 0, st, a);
-    return launch_kernel(norm_fwd_kernel<T, 4, true>, dim3(grid), dim3(l.threads), 0, st, a);
-  }
-  if (l.vectors == 2) return launch_kernel(norm_fwd_kernel<T, 2, false>, dim3(grid), dim3(l.threads), 0, st, a);
-  return launch_kernel(norm_fwd_kernel<T, 4, false>, dim3(grid), dim3(l.threads), 0, st, a);
+  const unsigned grid = (unsigned)ceil_div(a.rows, l.per);
+  return with_lanes(l, [&](auto v, auto most) {
+    return launch_kernel(norm_fwd_kernel<T, decltype(v)::value, decltype(most)::value>, dim3(grid), dim3(l.threads), 0, st, a);
+  });
 }
 
 template <typename T>
 hipError_t norm_backward_t(const NormLanes& l, const NormBwdArgs& a, unsigned grid, hipStream_t st) {
-  if (l.wave) {
-    if (l.vectors == 1) return launch_kernel(norm_bwd_kernel<T, 1, true>, dim3(grid), dim3(l.threads), 0, st, a);
-    if (l.vectors == 2) return launch_kernel(norm_bwd_kernel<T, 2, true>, dim3(grid), dim3(l.threads), 0, st, a);
-    return launch_kernel(norm_bwd_kernel<T, 4, true>, dim3(grid), dim3(l.threads), 0, st, a);
-  }
-  if (l.vectors == 2) return launch_kernel(norm_bwd_kernel<T, 2, false>, dim3(grid), dim3(l.threads), 0, st, a);
-  return launch_kernel(norm_bwd_kernel<T, 4, false>, dim3(grid), dim3(l.threads), 0, st, a);
+  return with_lanes(l, [&](auto v, auto most) {
+    return launch_kernel(norm_bwd_kernel<T, decltype(v)::value, decltype(most)::value>, dim3(grid), dim3(l.threads), 0, st, a);
+  });
 }
 
 }  // namespace
 
 size_t norm_workspace(const moe_norm_shape& s) {
   const NormLanes l = lanes_of(s.cols);
-  return (size_t)(norm_blocks(l, s.rows, s.cols) * l.per) * s.cols * 4;
+  return (size_t)norm_blocks(l, s.rows) * s.cols * 4;
 }
 
 hipError_t launch_norm_forward(const moe_norm_shape& s, const void* x, const void* residual, const float* weight, void* sum,
@@ -300,14 +345,14 @@ hipError_t launch_norm_backward(const moe_norm_shape& s, const void* d_y, const 
   if (s.rows == 0)
     return launch_kernel(norm_zero_kernel, dim3((unsigned)ceil_div(s.cols, 256)), dim3(256), 0, st, d_weight, s.cols);
   const NormLanes l = lanes_of(s.cols);
-  const unsigned grid = (unsigned)norm_blocks(l, s.rows, s.cols);
+  const unsigned grid = (unsigned)norm_blocks(l, s.rows);
   const NormBwdArgs a{d_y, d_sum, h, weight, rstd, d_x, d_weight ? parts : nullptr, s.rows, s.x_ld ? s.x_ld : s.cols,
                       s.y_ld ? s.y_ld : s.cols, s.cols};
   const hipError_t err =
       s.dtype == MOE_DTYPE_F32 ? norm_backward_t<float>(l, a, grid, st) : norm_backward_t<uint16_t>(l, a, grid, st);
   if (err != hipSuccess || !d_weight) return err;
-  return launch_kernel(norm_join_kernel, dim3((unsigned)ceil_div(s.cols, 64)), dim3(1024), 0, st, parts,
-                       (int)grid * l.per, s.cols, d_weight);
+  return launch_kernel(norm_join_kernel, dim3((unsigned)ceil_div(s.cols, 16)), dim3(1024), 0, st, parts,
+                       (int)grid, s.cols, d_weight);
 }
 
 }  // namespace moe

@@ -4,8 +4,8 @@ The sum is one fp32 addition and one rounding: compared bit for bit.  rstd is fp
 6 + 16 roundings behind a square's (8 values, 4 vectors, 64 lanes, 16 wavefronts) and is halved by the root; division and root
 add three: under 20 of 2^-24, and 2^-19 is asked.  y has two products more and its type's rounding (bf16 2^-8).  A code is within half a step (2^-4 of
 the value, 2^-10 of the scale below 2^-6 of it) and y's fp32 error.  dh is a difference, so its error counts
-against its terms; d_weight sums at most D rows one after another (16 MB of partial sums: D rows a workgroup, then the
-workgroups): (2^-18 + D 2^-24) of its terms."""
+against its terms; d_weight has D additions one after another, the rows of a workgroup and the workgroups:
+(2^-18 + D 2^-24) of its terms."""
 import numpy as np
 import pytest
 
@@ -69,10 +69,9 @@ def check_codes(out, y_ref):
     assert (np.abs(got - v) <= (2.0 ** -4 + 2.0 ** -17) * np.abs(v) + 2.0 ** -10 * s[:, :, None]).all()
 
 
-def depth(rows, cols):
-    """Rows that one thread sums at most, and workgroups whose sums one wavefront adds up."""
-    parts = max(256, min(4096, (1 << 22) // cols)) - 3
-    return -(-rows // parts) + min(rows + 3, parts + 3) // 16 + 8
+def depth(rows):
+    """Additions one after another: the rows of one of 256 workgroups, its wavefronts, the workgroups."""
+    return -(-rows // 256) + 3 + 4 + 16
 
 
 CASES = [(1, 8, "bf16"), (1, 7168, "bf16"), (3, 128, "f32"), (5, 520, "bf16"), (77, 2048, "bf16"), (9, 2056, "f32"),
@@ -104,7 +103,7 @@ def test_against_float64(rows, cols, stream, residual):
     size += np.abs(np_(d_s)) if residual else 0
     assert (np.abs(np_(d_x) - ref) <= half * np.abs(ref) + 2.0 ** -17 * size).all()
     size = np.abs(np_(d_y) * u).sum(axis=0)
-    assert (np.abs(np_(d_w) - ref_w) <= (2.0 ** -18 + depth(rows, cols) * 2.0 ** -24) * size).all()
+    assert (np.abs(np_(d_w) - ref_w) <= (2.0 ** -18 + depth(rows) * 2.0 ** -24) * size).all()
 
 
 def test_codes_are_the_quantisers():
