@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
       for (int h = 0; h < 2; ++h) {
         const int c = c0 + 16 * quad + 8 * h;
         const bool in = g.base && c0 < end && t < g.rows && c < g.outs;
-        v[h] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(g.base) + t * g.base_ld + c) : Raw8<T>{};
+        v[h] = in ? raw_at(static_cast<const T*>(g.base) + t * g.base_ld + c) : Raw8<T>{};
       }
     };
     Raw8<T> base[2];

@@ -8,8 +8,8 @@
 // The gradient holds the picks, and so f, fixed.  With c_i = d_loss alpha f_i / L and D = sum_i p_i c_i:
 //   softmax  dl_i = p_i (c_i - D);   sigmoid  dl_i = p_i (1 - s_i) (c_i - D).
 //
-// Sequences lie one behind the other and may begin anywhere.  16 lanes hold a token, each runs of four neighbouring
-// experts.  A workgroup takes a chunk of tokens and writes its sums of p and its counts once for every sequence that it
+// Sequences lie one behind the other and may begin anywhere.  16 lanes hold a token (32 above 128 experts, 64 above 256),
+// each one or two runs of four neighbouring experts.  A workgroup takes a chunk of tokens and writes its sums of p and its counts once for every sequence that it
 // meets: chunk c and sequence s have the place c + s, which no other pair has (from one pair to the next, at least one of
 // the two grows).  A second kernel adds up the places of each sequence, in order: no floating-point atomics.
 #include "lanes.h"
@@ -18,13 +18,14 @@
 namespace moe {
 namespace {
 
-constexpr int kLanes = 16, kTokens = 64 / kLanes;             // lanes of a token, tokens of a wavefront at a time
 constexpr int kPartWaves = 16, kPartThreads = 64 * kPartWaves;  // of a workgroup of the forward pass
 constexpr int kWaves = 4, kThreads = 64 * kWaves;             // of a workgroup of the backward pass
-constexpr int kJoinThreads = 1024;
+constexpr int kJoinThreads = 1024;                            // of the second kernel
+constexpr int kPlaces = 256;                                  // places for the whole batch, or so
 
-// the places' layout: N sums of p (fp32), N counts, the number of tokens
-__host__ __device__ inline int64_t place_words(int n) { return 2 * (int64_t)n + 4; }
+// the places' layout: sums of p (fp32), counts, the number of tokens, columns rounded up to fours
+__host__ __device__ inline int place_cols(int n) { return (n + 3) & ~3; }
+__host__ __device__ inline int place_words(int n) { return 2 * place_cols(n) + 4; }
 
 struct BalanceArgs {
   const void* logits;
@@ -67,14 +68,14 @@ __device__ __forceinline__ int64_t piece_end(const BalanceArgs& a, int s, int64_
 // The token's p, and for the sigmoid 1 - s; C runs of four a lane.  Where no logit of the token is positive the sigmoid's
 // shares come from exp(l - largest l) / (1 + exp(l)): they keep their value where every s is below 2^-126.  Reciprocals are the
 // instruction's, one unit in the last place.
-template <int C, bool SOFTMAX>
+template <int L, int C, bool SOFTMAX>
 __device__ __forceinline__ void shares(float (&l)[C][4], float (&rest)[C][4]) {
   float top = kNegInf;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = fmaxf(top, l[c][j]);
-  top = max_of<kLanes>(top);
+  top = max_of<L>(top);
   if (top == kNegInf) top = 0.0f;
   float part[C];
 #pragma unroll
@@ -93,7 +94,7 @@ __device__ __forceinline__ void shares(float (&l)[C][4], float (&rest)[C][4]) {
     }
     part[c] = sum_run<4>(l[c]);
   }
-  const float sum = sum_of<kLanes>(sum_run<C>(part));
+  const float sum = sum_of<L>(sum_run<C>(part));
   const float r = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -101,11 +102,11 @@ __device__ __forceinline__ void shares(float (&l)[C][4], float (&rest)[C][4]) {
     for (int j = 0; j < 4; ++j) l[c][j] *= r;
 }
 
-template <int C, typename TL>
+template <int L, int C, typename TL>
 __device__ __forceinline__ void load_token(const TL* row, int N, int lane, float (&l)[C][4]) {
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int first = 4 * (c * kLanes + lane);
+    const int first = 4 * (c * L + lane);
     if (first < N) load_run<4>(row + first, N - first, l[c]);
     else
 #pragma unroll
@@ -113,26 +114,37 @@ __device__ __forceinline__ void load_token(const TL* row, int N, int lane, float
   }
 }
 
-// the sum over the four tokens of a wavefront
+// the sum over the tokens of a wavefront
+template <int L>
 __device__ __forceinline__ float slots_sum(float v) {
-  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-  const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+  if constexpr (L == 16) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+  }
+  if constexpr (L <= 32) {
+    const auto q = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(q[0]) + __uint_as_float(q[1]);
+  }
+  return v;
 }
 
-// chunk: tokens of a workgroup, in blocks of 64 that lie in registers together
-template <int C, typename TL, bool SOFTMAX>
-__global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs a, int chunk, float* __restrict__ places,
-                                                                    int32_t* __restrict__ tickets) {
+// the token's entries of topk_idx that the lane holds, -1 behind the last (at most 32 picks: two of 16 lanes)
+template <int L>
+constexpr int kPicks = L == 16 ? 2 : 1;
+template <int L>
+__device__ __forceinline__ void load_picks(const BalanceArgs& a, int64_t t, int lane, int (&pick)[kPicks<L>]) {
+#pragma unroll
+  for (int h = 0; h < kPicks<L>; ++h) pick[h] = lane + h * L < a.K ? a.idx[t * a.K + lane + h * L] : -1;
+}
+
+// L lanes a token.  chunk: tokens of a workgroup, in blocks that lie in registers together
+template <int L, int C, typename TL, bool SOFTMAX>
+__global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs a, int chunk, float* __restrict__ places) {
   extern __shared__ float lds[];   // [kPartWaves][N] sums, then int [N] counts, int [1] tokens
-  constexpr int kBlock = kPartWaves * kTokens;
-  const int lane = threadIdx.x & (kLanes - 1), wl = threadIdx.x & 63, slot = wl / kLanes, wave = threadIdx.x >> 6;
+  constexpr int kTokens = 64 / L, kBlock = kPartWaves * kTokens;
+  const int lane = threadIdx.x & (L - 1), slot = (threadIdx.x & 63) / L, wave = threadIdx.x >> 6;
   const int64_t begin = (int64_t)blockIdx.x * chunk, end = begin + chunk < a.T ? begin + chunk : a.T;
   int* counts = reinterpret_cast<int*>(lds + kPartWaves * a.N);
-  if (tickets)   // (for the second kernel)
-    for (int64_t i = (int64_t)blockIdx.x * kPartThreads + threadIdx.x; i < a.S; i += (int64_t)gridDim.x * kPartThreads) tickets[i] = 0;
-  for (int i = threadIdx.x; i < a.N + 1; i += kPartThreads) counts[i] = 0;
   float total[C][4];
 #pragma unroll
   for (int c = 0; c < C; ++c)
@@ -145,13 +157,14 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int i = 4 * (c * kLanes + lane) + j;
-        const float v = slots_sum(total[c][j]);
+        const int i = 4 * (c * L + lane) + j;
+        const float v = slots_sum<L>(total[c][j]);
         if (slot == 0 && i < a.N) lds[wave * a.N + i] = v;
         total[c][j] = 0.0f;
       }
     __syncthreads();
     float* place = places + ((int64_t)blockIdx.x + seq) * place_words(a.N);
+    const int cols = place_cols(a.N);
     for (int i = threadIdx.x; i < a.N + 1; i += kPartThreads) {
       if (i < a.N) {
         float v[kPartWaves];
@@ -159,42 +172,56 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
         for (int w = 0; w < kPartWaves; ++w) v[w] = lds[w * a.N + i];
         place[i] = sum_run<kPartWaves>(v);
       }
-      reinterpret_cast<int*>(place)[a.N + i] = counts[i];
+      reinterpret_cast<int*>(place)[i < a.N ? cols + i : 2 * cols] = counts[i];
       counts[i] = 0;
     }
     __syncthreads();
   };
+  // a block's logits and picks, on their way while the block before is worked on
+  float next[C][4];
+  int next_pick[kPicks<L>];
+  auto load = [&](int64_t block) {
+    const int64_t t = block + wave * kTokens + slot;
+    load_token<L, C>(static_cast<const TL*>(a.logits) + (t < end ? t : end - 1) * a.ld, a.N, lane, next);
+    load_picks<L>(a, t < end ? t : end - 1, lane, next_pick);
+  };
+  load(begin);
+  for (int i = threadIdx.x; i < a.N + 1; i += kPartThreads) counts[i] = 0;
+  int s = sequence_of(a, begin);
   __syncthreads();
   for (int64_t block = begin; block < end; block += kBlock) {
     const int64_t t = block + wave * kTokens + slot, stop = block + kBlock < end ? block + kBlock : end;
-    const bool in = t < stop;
     float l[C][4], rest[C][4];
-    load_token<C>(static_cast<const TL*>(a.logits) + (in ? t : block) * a.ld, a.N, lane, l);
-    int pick[2];   // (at most 32)
+    int pick[kPicks<L>];
+    bool some = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = lane + h * kLanes;
-      pick[h] = in && k < a.K ? a.idx[t * a.K + k] : -1;
-      if (pick[h] >= a.N) pick[h] = -1;
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) l[c][j] = next[c][j];
+#pragma unroll
+    for (int h = 0; h < kPicks<L>; ++h) {
+      pick[h] = next_pick[h] < a.N ? next_pick[h] : -1;
+      some |= pick[h] >= 0;
     }
-    const bool real = max_of<kLanes>((uint32_t)(pick[0] >= 0 || pick[1] >= 0)) != 0;
-    shares<C, SOFTMAX>(l, rest);
+    if (block + kBlock < end) load(block + kBlock);
+    const bool real = max_of<L>((uint32_t)some) != 0;
+    shares<L, C, SOFTMAX>(l, rest);
     for (int64_t t0 = block; t0 < stop;) {
-      const int s = sequence_of(a, t0);
+      if (t0 > begin) s = sequence_of(a, t0);
       const int64_t t1 = s < 0 ? (a.start[0] < stop ? a.start[0] : stop) : piece_end(a, s, t0, stop);
-      const bool some = s >= 0 && s < a.S;
+      const bool inside = s >= 0 && s < a.S;
       if (seq >= 0 && s != seq) {
         __syncthreads();   // (the counts of the piece before)
         leave();
       }
-      seq = some ? s : -1;
-      if (some && real && t >= t0 && t < t1) {
+      seq = inside ? s : -1;
+      if (inside && real && t >= t0 && t < t1) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
 #pragma unroll
           for (int j = 0; j < 4; ++j) total[c][j] += l[c][j];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < kPicks<L>; ++h)
           if (pick[h] >= 0) atomicAdd(&counts[pick[h]], 1);
         if (lane == 0) atomicAdd(&counts[a.N], 1);
       }
@@ -213,71 +240,109 @@ struct BalanceOut {
   float* prob_sum;   // or null
 };
 
-// A workgroup adds up 64 columns of a sequence's places, its wavefronts every so many-th place, then their sums.  The loss is a
-// sum over the columns: with several workgroups a sequence, each leaves its share and the last of them (by a ticket that the
-// first kernel cleared) adds the shares in their order.
+// One workgroup a sequence: its places added up in order, then the loss, which is a sum over all columns.  `quads` threads (a
+// power of two, 16 at least) take four columns each, groups of them every further place, eight loads at once.
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs a, int chunk, const float* __restrict__ places,
-                                                                    BalanceOut o, int32_t* tickets, float* dots) {
-  constexpr int kBatch = 8;
-  __shared__ float sums[kJoinThreads / 64][64];
-  __shared__ int counts[kJoinThreads / 64][64];
-  __shared__ int lens[kJoinThreads / 64];
-  const int s = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
-  const int i = blockIdx.y * 64 + lane, col = min(i, a.N - 1);
+                                                                    BalanceOut o, int quads) {
+  typedef float f32x4 __attribute__((ext_vector_type(4)));
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  constexpr int kBatch = 8, kMost = kJoinThreads / 64;
+  __shared__ f32x4 sums[kMost][64];
+  __shared__ i32x4 counts[kMost][64];
+  __shared__ int lens[kMost];
+  __shared__ float dots[2];
+  const int s = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, waves = blockDim.x >> 6;
+  const int cols = place_cols(a.N), words = place_words(a.N), col = min(4 * (tid & (quads - 1)), cols - 4);
+  const int group = tid / quads, groups = blockDim.x / quads;
   int64_t b = a.start ? a.start[s] : 0, e = a.start ? a.start[s + 1] : a.T;
   b = b < 0 ? 0 : b;
   e = e > a.T ? a.T : e;
-  float p = 0.0f;
-  int n = 0, len = 0;
+  f32x4 p = {0.0f, 0.0f, 0.0f, 0.0f};
+  i32x4 n = {0, 0, 0, 0};
+  int len = 0;
   if (b < e) {
-    const int64_t last = (e - 1) / chunk;
-    for (int64_t c0 = b / chunk + wave; c0 <= last; c0 += (int64_t)waves * kBatch) {
-      float v[kBatch];
-      int m[kBatch], q[kBatch];
+    const int first = (int)(b / chunk), last = (int)((e - 1) / chunk);
+    const float* at = places + (int64_t)s * words;
+    for (int c0 = first + group; c0 <= last; c0 += groups * kBatch) {
+      f32x4 v[kBatch];
+      i32x4 m[kBatch];
+      int q[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int64_t c = c0 + (int64_t)k * waves < last ? c0 + (int64_t)k * waves : last;
-        const float* place = places + (c + s) * place_words(a.N);
-        v[k] = place[col];
-        m[k] = reinterpret_cast<const int*>(place)[a.N + col];
-        q[k] = reinterpret_cast<const int*>(place)[2 * a.N];
+        const float* place = at + (int64_t)min(c0 + k * groups, last) * words;
+        v[k] = *reinterpret_cast<const f32x4*>(place + col);
+        m[k] = *reinterpret_cast<const i32x4*>(place + cols + col);
+        q[k] = reinterpret_cast<const int*>(place)[2 * cols];
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k)
-        if (c0 + (int64_t)k * waves <= last) {
+        if (c0 + k * groups <= last) {
           p += v[k];
           n += m[k];
           len += q[k];
         }
     }
   }
+  // the groups of a wavefront, then the wavefronts
+  auto over = [&](auto add) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      p[j] = __uint_as_float(add(__float_as_uint(p[j]), [](uint32_t x, uint32_t y) {
+        return __float_as_uint(__uint_as_float(x) + __uint_as_float(y));
+      }));
+      n[j] = (int)add((uint32_t)n[j], [](uint32_t x, uint32_t y) { return x + y; });
+    }
+    len = (int)add((uint32_t)len, [](uint32_t x, uint32_t y) { return x + y; });
+  };
+  if (quads < 32)
+    over([](uint32_t v, auto op) {
+      const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+      return op(r[0], r[1]);
+    });
+  if (quads < 64)
+    over([](uint32_t v, auto op) {
+      const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+      return op(r[0], r[1]);
+    });
   sums[wave][lane] = p;
   counts[wave][lane] = n;
   if (lane == 0) lens[wave] = len;
   __syncthreads();
-  if (wave != 0) return;
-  p = 0.0f;
-  n = len = 0;
-  for (int w = 0; w < waves; ++w) {
-    p += sums[w][lane];
-    n += counts[w][lane];
-    len += lens[w];
+  const int wide = quads > 64 ? quads / 64 : 1;   // wavefronts of a row of columns
+  float f = 0.0f;
+  if (tid < quads) {
+    p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    n = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kMost; ++w) {   // (all loads at once)
+      const f32x4 v = sums[w][lane];
+      const i32x4 m = counts[w][lane];
+      if (w < waves && (wide == 1 || (w & 1) == wave)) {
+        p += v;
+        n += m;
+      }
+    }
+    float term[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * tid + j;
+      term[j] = i < a.N ? (float)n[j] * p[j] : 0.0f;
+      if (i < a.N) {
+        o.counts[(int64_t)s * a.N + i] = n[j];
+        if (o.prob_sum) o.prob_sum[(int64_t)s * a.N + i] = p[j];
+      }
+    }
+    f = sum_run<4>(term);
   }
-  const bool in = i < a.N;
-  if (in) {
-    o.counts[(int64_t)s * a.N + i] = n;
-    if (o.prob_sum) o.prob_sum[(int64_t)s * a.N + i] = p;
-  }
-  float dot = sum_of<64>(in ? (float)n * p : 0.0f);
-  if (lane != 0) return;
-  if (blockIdx.y == 0) o.tokens[s] = len;
-  if (gridDim.y > 1) {
-    float* mine = dots + (int64_t)s * gridDim.y;
-    __hip_atomic_store(&mine[blockIdx.y], dot, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (__hip_atomic_fetch_add(&tickets[s], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) != (int)gridDim.y - 1) return;
-    dot = 0.0f;
-    for (unsigned k = 0; k < gridDim.y; ++k) dot += __hip_atomic_load(&mine[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  }
+  f = sum_of<64>(f);
+  if (lane == 0 && wave < 2) dots[wave] = f;
+  __syncthreads();
+  if (tid != 0) return;
+  len = 0;
+#pragma unroll
+  for (int w = 0; w < kMost; ++w) len += w < waves && (wide == 1 || (w & 1) == 0) ? lens[w] : 0;
+  const float dot = wide == 2 ? dots[0] + dots[1] : dots[0];
+  o.tokens[s] = len;
   o.loss[s] = len == 0 ? 0.0f : a.alpha * (dot / (float)len) * ((float)a.N / ((float)a.K * (float)len));
 }
 
@@ -299,14 +364,16 @@ struct BalanceBwdArgs {
   int64_t d_ld;
 };
 
-// The sequence of the token that the lane's 16 lanes hold, as sequence_of; 16 starts at once.
+// The sequence of the token that the lane's L lanes hold, as sequence_of; L starts at once.
+template <int L>
 __device__ __forceinline__ int sequence_of_lanes(const BalanceArgs& a, int64_t t) {
   if (!a.start) return 0;
-  const int lane = threadIdx.x & (kLanes - 1), shift = threadIdx.x & 63 & ~(kLanes - 1);
+  const int lane = threadIdx.x & (L - 1), shift = threadIdx.x & 63 & ~(L - 1);
   int lo = 0, hi = a.S + 1;
   while (hi > lo) {
-    const int step = (hi - lo + kLanes - 1) / kLanes, at = lo + lane * step;
-    const int c = __popc((uint32_t)(__ballot(at < hi && a.start[at] <= t) >> shift) & 0xFFFFu);
+    const int step = (hi - lo + L - 1) / L, at = lo + lane * step;
+    const uint64_t below = __ballot(at < hi && a.start[at] <= t) >> shift;
+    const int c = __popcll(L == 64 ? below : below & ((uint64_t(1) << (L & 63)) - 1));
     if (c == 0) break;
     if (step == 1) {
       lo += c;
@@ -319,39 +386,38 @@ __device__ __forceinline__ int sequence_of_lanes(const BalanceArgs& a, int64_t t
   return lo - 1;
 }
 
-// Four tokens a wavefront, each with its own sequence.
-template <int C, typename TL, bool SOFTMAX, bool ADD>
+// Every token with its own sequence.
+template <int L, int C, typename TL, bool SOFTMAX, bool ADD>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, BalanceBwdArgs w) {
-  const int lane = threadIdx.x & (kLanes - 1), slot = (threadIdx.x & 63) / kLanes, wave = threadIdx.x >> 6;
-  constexpr int kBlock = kWaves * kTokens;
+  constexpr int kTokens = 64 / L, kBlock = kWaves * kTokens;
+  const int lane = threadIdx.x & (L - 1), slot = (threadIdx.x & 63) / L, wave = threadIdx.x >> 6;
   for (int64_t t = (int64_t)blockIdx.x * kBlock + wave * kTokens + slot; t < a.T; t += (int64_t)gridDim.x * kBlock) {
     float l[C][4], rest[C][4], pull[C][4];
-    load_token<C>(static_cast<const TL*>(a.logits) + t * a.ld, a.N, lane, l);
+    int pick[kPicks<L>];
+    load_token<L, C>(static_cast<const TL*>(a.logits) + t * a.ld, a.N, lane, l);
+    load_picks<L>(a, t, lane, pick);
     bool some = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int k = lane + h * kLanes, e = k < a.K ? a.idx[t * a.K + k] : -1;
-      some |= e >= 0 && e < a.N;
-    }
-    const int s = sequence_of_lanes(a, t);
-    const bool real = s >= 0 && s < a.S && max_of<kLanes>((uint32_t)some) != 0;
-    const float len = real ? (float)w.tokens[s] : 0.0f;
-    const float each = len > 0.0f ? w.d_loss[s] * a.alpha * ((float)a.N / ((float)a.K * len)) / len : 0.0f;
-    const int32_t* n = w.counts + (real ? (int64_t)s * a.N : 0);
+    for (int h = 0; h < kPicks<L>; ++h) some |= pick[h] >= 0 && pick[h] < a.N;
+    const int s = sequence_of_lanes<L>(a, t);
+    const bool real = max_of<L>((uint32_t)some) != 0 && s >= 0 && s < a.S;
+    const int at = real ? s : 0;
+    const float len = (float)w.tokens[at], d_loss = w.d_loss[at];
+    const int32_t* n = w.counts + (int64_t)at * a.N;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int first = 4 * (c * kLanes + lane);
+      const int first = 4 * (c * L + lane);
       if (first + 4 <= a.N) {
         struct __attribute__((packed, aligned(4))) Run { int32_t v[4]; };
         const Run q = *reinterpret_cast<const Run*>(n + first);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pull[c][j] = each * (float)q.v[j];
+        for (int j = 0; j < 4; ++j) pull[c][j] = (float)q.v[j];
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pull[c][j] = first + j < a.N ? each * (float)n[first + j] : 0.0f;
+        for (int j = 0; j < 4; ++j) pull[c][j] = first + j < a.N ? (float)n[first + j] : 0.0f;
       }
     }
-    shares<C, SOFTMAX>(l, rest);
+    shares<L, C, SOFTMAX>(l, rest);
     float part[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -360,19 +426,20 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, Ba
       for (int j = 0; j < 4; ++j) q[j] = l[c][j] * pull[c][j];
       part[c] = sum_run<4>(q);
     }
-    const float dot = sum_of<kLanes>(sum_run<C>(part));
+    const float dot = sum_of<L>(sum_run<C>(part));
+    const float each = real && len > 0.0f ? d_loss * a.alpha * ((float)a.N / ((float)a.K * len)) / len : 0.0f;
     TL* row = static_cast<TL*>(w.d_logits) + t * w.d_ld;
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int first = 4 * (c * kLanes + lane);
+      const int first = 4 * (c * L + lane);
       if (first >= a.N || (ADD && !real)) continue;
       float d[4], was[4];
       if constexpr (ADD) load_run<4>(row + first, a.N - first, was);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = l[c][j] * (pull[c][j] - dot);
+        d[j] = l[c][j] * (each * (pull[c][j] - dot));
         if constexpr (!SOFTMAX) d[j] *= rest[c][j];
-        if (!real) d[j] = 0.0f;
+        if (!real) d[j] = 0.0f;   // (whatever its logits are)
         if constexpr (ADD) d[j] += was[j];
       }
       store_run4(row + first, a.N - first, d);
@@ -380,51 +447,57 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, Ba
   }
 }
 
-// Tokens of a workgroup of the forward pass: 64, or more where that would make over 1024 places
+int lanes_of(int n) { return n <= 128 ? 16 : n <= 256 ? 32 : 64; }
+
+// Tokens of a workgroup of the forward pass: whole blocks of what its wavefronts hold at once, one workgroup a CU or so (the
+// second kernel reads a place for each: T=32768, 64 experts, 512 places XX us, 256 YY)
 int chunk_of(const moe_balance_config& c) {
-  int64_t chunk = 64;
-  while (ceil_div(c.tokens, chunk) > 1024) chunk *= 2;
-  return (int)chunk;
+  const int64_t block = kPartWaves * (64 / lanes_of(c.n_routed));
+  return (int)(block * std::max<int64_t>(1, ceil_div(ceil_div(c.tokens, block), kPlaces)));
 }
 
 BalanceArgs args_of(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start) {
   return {logits, c.logits_ld ? c.logits_ld : c.n_routed, idx, start, c.tokens, c.n_routed, c.top_k, c.n_seqs, c.alpha};
 }
 
-// f(integral_constant) with the runs of four a lane that hold N experts
+// f(lanes of a token, runs of four a lane) as integral constants
 template <typename F>
-hipError_t with_runs(int n, F f) {
-  if (n <= 64) return f(std::integral_constant<int, 1>{});
-  if (n <= 128) return f(std::integral_constant<int, 2>{});
-  if (n <= 256) return f(std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 8>{});
+hipError_t with_lanes(int n, F f) {
+  using std::integral_constant;
+  if (n <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
+  if (n <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
+  if (n <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
 }
 
 template <typename TL, bool SOFTMAX>
-hipError_t part_t(const BalanceArgs& a, int chunk, float* places, int32_t* tickets, hipStream_t st) {
+hipError_t part_t(const BalanceArgs& a, int chunk, float* places, hipStream_t st) {
   const size_t lds = (size_t)(kPartWaves * a.N + a.N + 4) * 4;
-  return with_runs(a.N, [&](auto c) {
-    return launch_kernel(balance_part_kernel<decltype(c)::value, TL, SOFTMAX>, dim3((unsigned)ceil_div(a.T, chunk)),
-                         dim3(kPartThreads), lds, st, a, chunk, places, tickets);
+  return with_lanes(a.N, [&](auto l, auto c) {
+    return launch_kernel(balance_part_kernel<decltype(l)::value, decltype(c)::value, TL, SOFTMAX>,
+                         dim3((unsigned)ceil_div(a.T, chunk)), dim3(kPartThreads), lds, st, a, chunk, places);
   });
 }
 
-template <typename TL, bool SOFTMAX>
-hipError_t bwd_t(const BalanceArgs& a, const BalanceBwdArgs& w, bool add, hipStream_t st) {
-  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(a.T, kWaves * kTokens), 1 << 16);
-  return with_runs(a.N, [&](auto c) {
-    return add ? launch_kernel(balance_bwd_kernel<decltype(c)::value, TL, SOFTMAX, true>, dim3(grid), dim3(kThreads), 0, st, a, w)
-               : launch_kernel(balance_bwd_kernel<decltype(c)::value, TL, SOFTMAX, false>, dim3(grid), dim3(kThreads), 0, st, a, w);
+template <typename TL, bool SOFTMAX, bool ADD>
+hipError_t bwd_t(const BalanceArgs& a, const BalanceBwdArgs& w, hipStream_t st) {
+  const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(a.T, kWaves * (64 / lanes_of(a.N))), 1 << 16);
+  return with_lanes(a.N, [&](auto l, auto c) {
+    return launch_kernel(balance_bwd_kernel<decltype(l)::value, decltype(c)::value, TL, SOFTMAX, ADD>, dim3(grid),
+                         dim3(kThreads), 0, st, a, w);
   });
+}
+
+template <typename TL>
+hipError_t bwd_l(const BalanceArgs& a, const BalanceBwdArgs& w, bool softmax, bool add, hipStream_t st) {
+  if (softmax) return add ? bwd_t<TL, true, true>(a, w, st) : bwd_t<TL, true, false>(a, w, st);
+  return add ? bwd_t<TL, false, true>(a, w, st) : bwd_t<TL, false, false>(a, w, st);
 }
 
 }  // namespace
 
-// the workspace: places, then (more than 64 experts) a ticket and a share of the loss per 64 columns for each sequence
 size_t balance_workspace(const moe_balance_config& c) {
-  if (c.tokens == 0) return 0;
-  const size_t places = (size_t)(ceil_div(c.tokens, chunk_of(c)) + c.n_seqs) * place_words(c.n_routed) * 4;
-  return places + (c.n_routed > 64 ? (size_t)c.n_seqs * (1 + ceil_div(c.n_routed, 64)) * 4 : 0);
+  return c.tokens == 0 ? 0 : (size_t)(ceil_div(c.tokens, chunk_of(c)) + c.n_seqs) * place_words(c.n_routed) * 4;
 }
 
 hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
@@ -436,19 +509,19 @@ hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, 
     return launch_kernel(balance_zero_kernel, dim3((unsigned)ceil_div((int64_t)c.n_seqs * c.n_routed, 256)), dim3(256), 0, st,
                          o, c.n_seqs, c.n_routed);
   const int chunk = chunk_of(c);
-  float* dots = places + (ceil_div(c.tokens, chunk) + c.n_seqs) * place_words(c.n_routed);
-  int32_t* tickets = c.n_routed > 64 ? reinterpret_cast<int32_t*>(dots + c.n_seqs * ceil_div(c.n_routed, 64)) : nullptr;
   const bool f32 = c.logits_dtype == MOE_DTYPE_F32;
   hipError_t err;
   if (c.score == MOE_SCORE_SOFTMAX)
-    err = f32 ? part_t<float, true>(a, chunk, places, tickets, st) : part_t<uint16_t, true>(a, chunk, places, tickets, st);
+    err = f32 ? part_t<float, true>(a, chunk, places, st) : part_t<uint16_t, true>(a, chunk, places, st);
   else
-    err = f32 ? part_t<float, false>(a, chunk, places, tickets, st) : part_t<uint16_t, false>(a, chunk, places, tickets, st);
+    err = f32 ? part_t<float, false>(a, chunk, places, st) : part_t<uint16_t, false>(a, chunk, places, st);
   if (err != hipSuccess) return err;
-  // wavefronts: 16, or 4 where a sequence has few places
-  const unsigned threads = c.tokens / c.n_seqs >= 8 * chunk ? kJoinThreads : 256;
-  return launch_kernel(balance_join_kernel, dim3((unsigned)c.n_seqs, (unsigned)ceil_div(c.n_routed, 64)), dim3(threads), 0, st, a,
-                       chunk, places, o, tickets, dots);
+  int quads = 16;
+  while (4 * quads < c.n_routed) quads *= 2;
+  // groups of columns: about as many as an average sequence has places
+  unsigned threads = kJoinThreads;
+  while (threads > 128 && (int64_t)(threads / quads) * chunk * c.n_seqs > 2 * (int64_t)c.tokens) threads /= 2;
+  return launch_kernel(balance_join_kernel, dim3((unsigned)c.n_seqs), dim3(threads), 0, st, a, chunk, places, o, quads);
 }
 
 hipError_t launch_balance_backward(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
@@ -457,10 +530,8 @@ hipError_t launch_balance_backward(const moe_balance_config& c, const void* logi
   if (c.tokens == 0) return hipSuccess;
   const BalanceArgs a = args_of(c, logits, idx, start);
   const BalanceBwdArgs w{counts, tokens, d_loss, d_logits, d_ld ? d_ld : c.n_routed};
-  const bool f32 = c.logits_dtype == MOE_DTYPE_F32;
-  if (c.score == MOE_SCORE_SOFTMAX)
-    return f32 ? bwd_t<float, true>(a, w, add, st) : bwd_t<uint16_t, true>(a, w, add, st);
-  return f32 ? bwd_t<float, false>(a, w, add, st) : bwd_t<uint16_t, false>(a, w, add, st);
+  const bool softmax = c.score == MOE_SCORE_SOFTMAX;
+  return c.logits_dtype == MOE_DTYPE_F32 ? bwd_l<float>(a, w, softmax, add, st) : bwd_l<uint16_t>(a, w, softmax, add, st);
 }
 
 }  // namespace moe

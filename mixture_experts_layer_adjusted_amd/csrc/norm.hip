@@ -88,20 +88,21 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormA
   const int64_t r = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
   if (r >= a.rows) return;
   Raw8<T> x[V], res[V];
-  float w[V][8], h[V][8], part[V];
-#pragma unroll
-  for (int j = 0; j < V; ++j) {
+  Raw8<float> w[V];
+  float h[V][8], part[V];
+  // (lanes past the row's end load its first values, and drop them)
+  auto column = [&](int j) {
     const int c = (j * lanes + lane) * 8;
-    const bool in = c < a.cols;
-    x[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.x) + r * a.x_ld + c) : Raw8<T>{};
-    if (a.residual)
-      res[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.residual) + r * a.x_ld + c) : Raw8<T>{};
+    return c < a.cols ? c : 0;
+  };
+#pragma unroll
+  for (int j = 0; j < V; ++j) x[j] = raw_at(static_cast<const T*>(a.x) + r * a.x_ld + column(j));
+  if (a.residual) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) res[j] = raw_at(static_cast<const T*>(a.residual) + r * a.x_ld + column(j));
   }
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    const int c = (j * lanes + lane) * 8;
-    if (c < a.cols) load8(a.weight + c, w[j]);
-  }
+  for (int j = 0; j < V; ++j) w[j] = raw_at(a.weight + column(j));
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     unpack8(x[j], h[j]);
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormA
     float sq[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) sq[i] = h[j][i] * h[j][i];
-    part[j] = sum_run<8>(sq);
+    part[j] = (j * lanes + lane) * 8 < a.cols ? sum_run<8>(sq) : 0.0f;
   }
   const float rstd = 1.0f / sqrtf(row_sum<WAVE>(sum_run<V>(part), place, 0) / (float)a.cols + a.eps);
   if (a.rstd && lane == 0) a.rstd[r] = rstd;
@@ -126,8 +127,9 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormA
     if (!in) continue;
     if (a.sum) store8(static_cast<T*>(a.sum) + r * a.x_ld + c, h[j]);
     float y[8];
+    unpack8(w[j], y);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = h[j][i] * rstd * w[j][i];
+    for (int i = 0; i < 8; ++i) y[i] *= h[j][i] * rstd;
     if (a.y) store8(static_cast<T*>(a.y) + r * a.y_ld + c, y);
     if (a.codes) {
       const float amax = run_amax(y);
@@ -159,44 +161,56 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
   const int first = WAVE ? threadIdx.x >> 6 : 0;
   const int64_t step = (int64_t)gridDim.x * per;
   const float n = (float)a.cols;
-  float dw[V][8], w[V][8];
+  float dw[V][8];
+  Raw8<float> w[V];
   Raw8<T> h[V], d_y[V], d_sum[V];
   float next_rstd = 0.0f;
+  // (lanes past the row's end load its first values, and drop them)
+  auto column = [&](int j) {
+    const int c = (j * lanes + lane) * 8;
+    return c < a.cols ? c : 0;
+  };
   auto load = [&](int64_t r) {
     next_rstd = a.rstd[r];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      const int c = (j * lanes + lane) * 8;
-      const bool in = c < a.cols;
-      h[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.h) + r * a.x_ld + c) : Raw8<T>{};
-      d_y[j] = in ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.d_y) + r * a.y_ld + c) : Raw8<T>{};
-      d_sum[j] = in && a.d_sum ? *reinterpret_cast<const Raw8<T>*>(static_cast<const T*>(a.d_sum) + r * a.x_ld + c) : Raw8<T>{};
+      h[j] = raw_at(static_cast<const T*>(a.h) + r * a.x_ld + column(j));
+      d_y[j] = raw_at(static_cast<const T*>(a.d_y) + r * a.y_ld + column(j));
+    }
+    if (a.d_sum) {
+#pragma unroll
+      for (int j = 0; j < V; ++j) d_sum[j] = raw_at(static_cast<const T*>(a.d_sum) + r * a.x_ld + column(j));
     }
   };
   int64_t r = (int64_t)blockIdx.x * per + first;
   if (kAhead && r < a.rows) load(r);
-  auto weights = [&](int j) {
-    const int c = (j * lanes + lane) * 8;
-    if (c < a.cols) load8(a.weight + c, w[j]);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) w[j][i] = 0.0f;
-  };
 #pragma unroll
   for (int j = 0; j < V; ++j) {
+    d_sum[j] = a.d_sum && kAhead ? d_sum[j] : Raw8<T>{};
+    if constexpr (kAhead) w[j] = raw_at(a.weight + column(j));
 #pragma unroll
     for (int i = 0; i < 8; ++i) dw[j][i] = 0.0f;
-    if constexpr (kAhead) weights(j);
+  }
+  if constexpr (kAhead) {   // the weights are waited for here: in the loop that would wait for the next row as well
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        asm volatile("" : "+v"(w[j].q[i].x), "+v"(w[j].q[i].y), "+v"(w[j].q[i].z), "+v"(w[j].q[i].w));
   }
   for (int at = 0; r < a.rows; r += step, at ^= 1) {
-    if constexpr (!kAhead) load(r);
+    if constexpr (!kAhead) {
+      load(r);
+#pragma unroll
+      for (int j = 0; j < V; ++j) w[j] = raw_at(a.weight + column(j));
+    }
     const float rstd = next_rstd;
     float u[V][8], g[V][8], part[V];
     Raw8<T> behind[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float p[8];
-      if constexpr (!kAhead) weights(j);
+      float p[8], wv[8];
+      unpack8(w[j], wv);
       unpack8(h[j], u[j]);
       unpack8(d_y[j], g[j]);
       behind[j] = d_sum[j];
@@ -204,10 +218,10 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
       for (int i = 0; i < 8; ++i) {
         u[j][i] *= rstd;
         dw[j][i] = fmaf(g[j][i], u[j][i], dw[j][i]);
-        g[j][i] *= w[j][i];
+        g[j][i] *= wv[i];
         p[i] = g[j][i] * u[j][i];
       }
-      part[j] = sum_run<8>(p);
+      part[j] = (j * lanes + lane) * 8 < a.cols ? sum_run<8>(p) : 0.0f;
     }
     if (kAhead && r + step < a.rows) load(r + step);
     const float mean = row_sum<WAVE>(sum_run<V>(part), place, at) / n;

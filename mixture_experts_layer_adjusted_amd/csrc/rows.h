@@ -40,18 +40,33 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
 }
 
-// eight values as they lie in memory, for loads ahead of their use
+// eight values as they lie in memory, for loads ahead of their use (whole registers: 16-bit pieces would be taken apart, and
+// waited for, right behind the load)
 template <typename T>
-struct alignas(16) Raw8 {
-  T v[8];
+struct Raw8 {
+  uint4 q[sizeof(T) / 2];
 };
-__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw_at(const T* p) {
+  Raw8<T> r;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float((uint32_t)r.v[i] << 16);
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.q[0].x, r.q[0].y, r.q[0].z, r.q[0].w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
 }
 __device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = r.v[i];
+  for (int i = 0; i < 2; ++i) {
+    v[4 * i] = __uint_as_float(r.q[i].x), v[4 * i + 1] = __uint_as_float(r.q[i].y);
+    v[4 * i + 2] = __uint_as_float(r.q[i].z), v[4 * i + 3] = __uint_as_float(r.q[i].w);
+  }
 }
 
 // v rounded to the element type T (uint16_t: bf16) and back
