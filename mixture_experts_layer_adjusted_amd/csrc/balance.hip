@@ -78,22 +78,33 @@ __device__ __forceinline__ void shares(float (&l)[C][4], float (&rest)[C][4]) {
   top = max_of<L>(top);
   if (top == kNegInf) top = 0.0f;
   float part[C];
+  const bool low = top < 0.0f;
+  // some_low: a token of the wavefront has no positive logit
+  auto each = [&](auto some_low) {
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
+    for (int c = 0; c < C; ++c) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float v = l[c][j];
-      if constexpr (SOFTMAX) {
-        l[c][j] = exp_of(v - top);
-      } else {
-        const float x = exp_of(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + x);
-        const bool up = v >= 0.0f;
-        rest[c][j] = (up ? x : 1.0f) * r;
-        l[c][j] = (up ? 1.0f : top < 0.0f ? exp_of(v - top) : x) * r;
+      for (int j = 0; j < 4; ++j) {
+        const float v = l[c][j];
+        if constexpr (SOFTMAX) {
+          l[c][j] = exp_of(v - top);
+        } else {
+          const float x = exp_of(-fabsf(v)), r = __builtin_amdgcn_rcpf(1.0f + x);
+          const bool up = v >= 0.0f;
+          float part_of_s = x;
+          if constexpr (decltype(some_low)::value) {
+            const float alike = exp_of(v - top);
+            part_of_s = low ? alike : x;
+          }
+          rest[c][j] = (up ? x : 1.0f) * r;
+          l[c][j] = (up ? 1.0f : part_of_s) * r;
+        }
       }
+      part[c] = sum_run<4>(l[c]);
     }
-    part[c] = sum_run<4>(l[c]);
-  }
+  };
+  if (!SOFTMAX && __ballot(low) != 0) each(std::true_type{});
+  else each(std::false_type{});
   const float sum = sum_of<L>(sum_run<C>(part));
   const float r = sum == 0.0f ? 0.0f : __builtin_amdgcn_rcpf(sum);
 #pragma unroll
@@ -102,16 +113,53 @@ __device__ __forceinline__ void shares(float (&l)[C][4], float (&rest)[C][4]) {
     for (int j = 0; j < 4; ++j) l[c][j] *= r;
 }
 
-template <int L, int C, typename TL>
-__device__ __forceinline__ void load_token(const TL* row, int N, int lane, float (&l)[C][4]) {
+// Four neighbouring values of a row of n, from `first` on (any alignment), as they lie in memory: loads ahead of their use.
+// No lane goes round a load, lanes behind the row's end load other values of it.  WHOLE: n is a multiple of four (known to
+// the compiler: it would make four loads of one and a choice of addresses out of a branch).
+template <bool WHOLE, typename T>
+struct Four {
+  uint32_t w[WHOLE ? sizeof(T) : 4];
+};
+template <bool WHOLE, typename T>
+__device__ __forceinline__ Four<WHOLE, T> four_at(const T* row, int first, int n) {
+  Four<WHOLE, T> q;
+  if constexpr (WHOLE) {
+    struct __attribute__((packed, aligned(sizeof(T)))) Run { uint32_t w[sizeof(T)]; };
+    const Run r = *reinterpret_cast<const Run*>(row + (first < n ? first : 0));
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int first = 4 * (c * L + lane);
-    if (first < N) load_run<4>(row + first, N - first, l[c]);
-    else
+    for (int j = 0; j < (int)sizeof(T); ++j) q.w[j] = r.w[j];
+  } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) l[c][j] = kNegInf;
+    for (int j = 0; j < 4; ++j) {
+      const T* at = row + min(first + j, n - 1);
+      if constexpr (sizeof(T) == 2) q.w[j] = (uint32_t)*at << 16;
+      else q.w[j] = *reinterpret_cast<const uint32_t*>(at);
+    }
   }
+  return q;
+}
+// the values, `fill` behind the row's end
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void values(const Four<WHOLE, T>& q, int first, int n, float fill, float (&v)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (WHOLE && sizeof(T) == 2)
+      v[j] = __uint_as_float(j & 1 ? q.w[j / 2] & 0xFFFF0000u : q.w[j / 2] << 16);
+    else v[j] = __uint_as_float(q.w[j]);
+    v[j] = (WHOLE ? first : first + j) < n ? v[j] : fill;
+  }
+}
+
+// a token's logits
+template <int L, int C, bool WHOLE, typename TL>
+__device__ __forceinline__ void load_token(const TL* row, int N, int lane, Four<WHOLE, TL> (&q)[C]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) q[c] = four_at<WHOLE>(row, 4 * (c * L + lane), N);
+}
+template <int L, int C, bool WHOLE, typename TL>
+__device__ __forceinline__ void unpack_token(const Four<WHOLE, TL> (&q)[C], int N, int lane, float (&l)[C][4]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) values(q[c], 4 * (c * L + lane), N, kNegInf, l[c]);
 }
 
 // the sum over the tokens of a wavefront
@@ -138,7 +186,7 @@ __device__ __forceinline__ void load_picks(const BalanceArgs& a, int64_t t, int 
 }
 
 // L lanes a token.  chunk: tokens of a workgroup, in blocks that lie in registers together
-template <int L, int C, typename TL, bool SOFTMAX>
+template <int L, int C, bool WHOLE, typename TL, bool SOFTMAX>
 __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs a, int chunk, float* __restrict__ places) {
   extern __shared__ float lds[];   // [kPartWaves][N] sums, then int [N] counts, int [1] tokens
   constexpr int kTokens = 64 / L, kBlock = kPartWaves * kTokens;
@@ -178,11 +226,11 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
     __syncthreads();
   };
   // a block's logits and picks, on their way while the block before is worked on
-  float next[C][4];
+  Four<WHOLE, TL> next[C];
   int next_pick[kPicks<L>];
   auto load = [&](int64_t block) {
     const int64_t t = block + wave * kTokens + slot;
-    load_token<L, C>(static_cast<const TL*>(a.logits) + (t < end ? t : end - 1) * a.ld, a.N, lane, next);
+    load_token<L, C, WHOLE>(static_cast<const TL*>(a.logits) + (t < end ? t : end - 1) * a.ld, a.N, lane, next);
     load_picks<L>(a, t < end ? t : end - 1, lane, next_pick);
   };
   load(begin);
@@ -194,10 +242,7 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
     float l[C][4], rest[C][4];
     int pick[kPicks<L>];
     bool some = false;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) l[c][j] = next[c][j];
+    unpack_token<L, C, WHOLE>(next, a.N, lane, l);
 #pragma unroll
     for (int h = 0; h < kPicks<L>; ++h) {
       pick[h] = next_pick[h] < a.N ? next_pick[h] : -1;
@@ -369,11 +414,12 @@ template <int L>
 __device__ __forceinline__ int sequence_of_lanes(const BalanceArgs& a, int64_t t) {
   if (!a.start) return 0;
   const int lane = threadIdx.x & (L - 1), shift = threadIdx.x & 63 & ~(L - 1);
+  auto bits = [&](uint64_t m) { return __popcll(L == 64 ? m : (m >> shift) & ((uint64_t(1) << (L & 63)) - 1)); };
+  if (a.S < L) return bits(__ballot(a.start[min(lane, a.S)] <= t && lane <= a.S)) - 1;
   int lo = 0, hi = a.S + 1;
   while (hi > lo) {
     const int step = (hi - lo + L - 1) / L, at = lo + lane * step;
-    const uint64_t below = __ballot(at < hi && a.start[at] <= t) >> shift;
-    const int c = __popcll(L == 64 ? below : below & ((uint64_t(1) << (L & 63)) - 1));
+    const int c = bits(__ballot(at < hi && a.start[at] <= t));
     if (c == 0) break;
     if (step == 1) {
       lo += c;
@@ -387,37 +433,31 @@ __device__ __forceinline__ int sequence_of_lanes(const BalanceArgs& a, int64_t t
 }
 
 // Every token with its own sequence.
-template <int L, int C, typename TL, bool SOFTMAX, bool ADD>
+template <int L, int C, bool WHOLE, typename TL, bool SOFTMAX, bool ADD>
 __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, BalanceBwdArgs w) {
   constexpr int kTokens = 64 / L, kBlock = kWaves * kTokens;
   const int lane = threadIdx.x & (L - 1), slot = (threadIdx.x & 63) / L, wave = threadIdx.x >> 6;
   for (int64_t t = (int64_t)blockIdx.x * kBlock + wave * kTokens + slot; t < a.T; t += (int64_t)gridDim.x * kBlock) {
     float l[C][4], rest[C][4], pull[C][4];
+    Four<WHOLE, TL> raw[C];
+    Four<WHOLE, int32_t> raw_counts[C];
     int pick[kPicks<L>];
-    load_token<L, C>(static_cast<const TL*>(a.logits) + t * a.ld, a.N, lane, l);
+    load_token<L, C, WHOLE>(static_cast<const TL*>(a.logits) + t * a.ld, a.N, lane, raw);
     load_picks<L>(a, t, lane, pick);
+    const int s = sequence_of_lanes<L>(a, t), at = s < 0 ? 0 : s < a.S ? s : a.S - 1;
+    const float len = (float)w.tokens[at], d_loss = w.d_loss[at];
+#pragma unroll
+    for (int c = 0; c < C; ++c) raw_counts[c] = four_at<WHOLE>(w.counts + (int64_t)at * a.N, 4 * (c * L + lane), a.N);
     bool some = false;
 #pragma unroll
     for (int h = 0; h < kPicks<L>; ++h) some |= pick[h] >= 0 && pick[h] < a.N;
-    const int s = sequence_of_lanes<L>(a, t);
-    const bool real = max_of<L>((uint32_t)some) != 0 && s >= 0 && s < a.S;
-    const int at = real ? s : 0;
-    const float len = (float)w.tokens[at], d_loss = w.d_loss[at];
-    const int32_t* n = w.counts + (int64_t)at * a.N;
-#pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int first = 4 * (c * L + lane);
-      if (first + 4 <= a.N) {
-        struct __attribute__((packed, aligned(4))) Run { int32_t v[4]; };
-        const Run q = *reinterpret_cast<const Run*>(n + first);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pull[c][j] = (float)q.v[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) pull[c][j] = first + j < a.N ? (float)n[first + j] : 0.0f;
-      }
-    }
+    const bool real = max_of<L>((uint32_t)some) != 0 && s == at;
+    unpack_token<L, C, WHOLE>(raw, a.N, lane, l);
     shares<L, C, SOFTMAX>(l, rest);
+#pragma unroll
+    for (int c = 0; c < C; ++c)   // (behind the row's end p is 0)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pull[c][j] = (float)(int32_t)raw_counts[c].w[j];
     float part[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -432,9 +472,8 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, Ba
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int first = 4 * (c * L + lane);
-      if (first >= a.N || (ADD && !real)) continue;
       float d[4], was[4];
-      if constexpr (ADD) load_run<4>(row + first, a.N - first, was);
+      if constexpr (ADD) values(four_at<WHOLE>(row, first, a.N), first, a.N, 0.0f, was);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         d[j] = l[c][j] * (each * (pull[c][j] - dot));
@@ -442,12 +481,13 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, Ba
         if (!real) d[j] = 0.0f;   // (whatever its logits are)
         if constexpr (ADD) d[j] += was[j];
       }
-      store_run4(row + first, a.N - first, d);
+      if (first < a.N && (!ADD || real)) store_run4(row + first, WHOLE ? 4 : a.N - first, d);
     }
   }
 }
 
-int lanes_of(int n) { return n <= 128 ? 16 : n <= 256 ? 32 : 64; }
+// (any other number of experts than a multiple of four: 64 lanes whatever their number, one kernel in place of four)
+int lanes_of(int n) { return n % 4 != 0 ? 64 : n <= 128 ? 16 : n <= 256 ? 32 : 64; }
 
 // Tokens of a workgroup of the forward pass: whole blocks of what its wavefronts hold at once, one workgroup a CU or so (the
 // second kernel reads a place for each: T=32768, 64 experts, 512 places XX us, 256 YY)
@@ -460,21 +500,23 @@ BalanceArgs args_of(const moe_balance_config& c, const void* logits, const int32
   return {logits, c.logits_ld ? c.logits_ld : c.n_routed, idx, start, c.tokens, c.n_routed, c.top_k, c.n_seqs, c.alpha};
 }
 
-// f(lanes of a token, runs of four a lane) as integral constants
+// f(lanes of a token, runs of four a lane, whether runs are whole) as integral constants
 template <typename F>
 hipError_t with_lanes(int n, F f) {
+  using std::bool_constant;
   using std::integral_constant;
-  if (n <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{});
-  if (n <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{});
-  if (n <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (n % 4 != 0) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, bool_constant<false>{});
+  if (n <= 64) return f(integral_constant<int, 16>{}, integral_constant<int, 1>{}, bool_constant<true>{});
+  if (n <= 128) return f(integral_constant<int, 16>{}, integral_constant<int, 2>{}, bool_constant<true>{});
+  if (n <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{}, bool_constant<true>{});
+  return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, bool_constant<true>{});
 }
 
 template <typename TL, bool SOFTMAX>
 hipError_t part_t(const BalanceArgs& a, int chunk, float* places, hipStream_t st) {
   const size_t lds = (size_t)(kPartWaves * a.N + a.N + 4) * 4;
-  return with_lanes(a.N, [&](auto l, auto c) {
-    return launch_kernel(balance_part_kernel<decltype(l)::value, decltype(c)::value, TL, SOFTMAX>,
+  return with_lanes(a.N, [&](auto l, auto c, auto whole) {
+    return launch_kernel(balance_part_kernel<decltype(l)::value, decltype(c)::value, decltype(whole)::value, TL, SOFTMAX>,
                          dim3((unsigned)ceil_div(a.T, chunk)), dim3(kPartThreads), lds, st, a, chunk, places);
   });
 }
@@ -482,9 +524,9 @@ hipError_t part_t(const BalanceArgs& a, int chunk, float* places, hipStream_t st
 template <typename TL, bool SOFTMAX, bool ADD>
 hipError_t bwd_t(const BalanceArgs& a, const BalanceBwdArgs& w, hipStream_t st) {
   const unsigned grid = (unsigned)std::min<int64_t>(ceil_div(a.T, kWaves * (64 / lanes_of(a.N))), 1 << 16);
-  return with_lanes(a.N, [&](auto l, auto c) {
-    return launch_kernel(balance_bwd_kernel<decltype(l)::value, decltype(c)::value, TL, SOFTMAX, ADD>, dim3(grid),
-                         dim3(kThreads), 0, st, a, w);
+  return with_lanes(a.N, [&](auto l, auto c, auto whole) {
+    return launch_kernel(balance_bwd_kernel<decltype(l)::value, decltype(c)::value, decltype(whole)::value, TL, SOFTMAX, ADD>,
+                         dim3(grid), dim3(kThreads), 0, st, a, w);
   });
 }
 
