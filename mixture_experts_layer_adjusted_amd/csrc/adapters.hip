@@ -66,33 +66,30 @@ __device__ __forceinline__ void for_adapters(int mine, F f) {
   }
 }
 
-// The rows of a workgroup that goes by adapters: blockIdx.x is a row, and if it is the first one with its adapter
-// (or the first without one) the workgroup takes all rows that have the same; otherwise there are none.
+// The rows of a workgroup that goes by adapters: blockIdx.x is a row, and if it is the first one with its adapter e
+// (or the first without one) the workgroup takes all rows that have the same; otherwise there are none.  Every wavefront
+// finds them by itself: a ballot for each 64 rows, and a permutation that brings the rows of e to the lanes in front.
 struct LeadRows {
-  uint64_t match[kLeadRows / 64];
-  uint8_t row[kLeadRows];
+  int count, low, high;   // rows number 0 to 63 and 64 to 127 of e, one a lane
+  __device__ __forceinline__ int at(int i) const { return i < 64 ? __shfl(low, i, 64) : __shfl(high, i - 64, 64); }
 };
-__device__ __forceinline__ int lead_rows(const AdapterArgs& g, LeadRows& l) {
-  const int i = threadIdx.x, first = blockIdx.x;
-  const int e = adapter_of(g, first);
-  const bool same = i < kLeadRows && i < g.rows && adapter_of(g, i) == e;
-  const uint64_t m = __ballot(same);
-  if (i < kLeadRows && (i & 63) == 0) l.match[i >> 6] = m;
-  __syncthreads();
-  int count = 0, before = 0;
-  bool earlier = false;
-#pragma unroll
-  for (int w = 0; w < kLeadRows / 64; ++w) {
-    const uint64_t mask = l.match[w];
-    if (w < first >> 6) earlier |= mask != 0;
-    if (w == first >> 6) earlier |= (mask & ((uint64_t(1) << (first & 63)) - 1)) != 0;
-    if (w < i >> 6) before += __popcll(mask);
-    count += __popcll(mask);
-  }
-  if (earlier) return 0;
-  if (same) l.row[before + __popcll(m & ((uint64_t(1) << (i & 63)) - 1))] = (uint8_t)i;
-  __syncthreads();
-  return count;
+__device__ __forceinline__ int bits_below(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+__device__ __forceinline__ LeadRows lead_rows(const AdapterArgs& g, int e) {
+  const int lane = threadIdx.x & 63, first = blockIdx.x;
+  const bool is0 = lane < g.rows && adapter_of(g, lane) == e, is1 = lane + 64 < g.rows && adapter_of(g, lane + 64) == e;
+  const uint64_t m0 = __ballot(is0), m1 = __ballot(is1);
+  const uint64_t before = (uint64_t(1) << (first & 63)) - 1;
+  LeadRows l{0, 0, 0};
+  if (first < 64 ? (m0 & before) != 0 : (m0 != 0 || (m1 & before) != 0)) return l;
+  const int n0 = __popcll(m0), n1 = __popcll(m1), b0 = bits_below(m0), b1 = bits_below(m1);
+  const int to0 = is0 ? b0 : n0 + lane - b0, to1 = (n0 + (is1 ? b1 : n1 + lane - b1)) & 63;
+  const int p0 = __builtin_amdgcn_ds_permute(4 * to0, lane), p1 = __builtin_amdgcn_ds_permute(4 * to1, lane + 64);
+  l.count = n0 + n1;
+  l.low = lane < n0 ? p0 : p1;
+  l.high = p1;
+  return l;
 }
 
 // The operands of one step of the first product: 64 values along the contraction, two of the instruction's
@@ -105,21 +102,31 @@ struct LowStep {
 // neighbouring ranks of one token.  RT tiles of 16 ranks.  A workgroup's wavefronts take every fourth run of 64.
 template <int RT, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
-  constexpr int kAhead = RT == 1 ? 4 : RT == 2 ? 2 : 1;   // steps whose operands are in flight
+  constexpr int kAhead = RT == 1 ? 3 : RT <= 4 ? 2 : 1;   // steps whose operands are in flight
+  constexpr int kStride = kStep * kWaves;
   __shared__ float place[kWaves][kRows][RT * 16 + 4];
-  __shared__ LeadRows lead;
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int begin = blockIdx.y * g.per_split, end = min(g.in, begin + g.per_split);
-  int count = kRows;
+  // whole steps of the wavefront, and where a last one may end early
+  const int first = begin + kStep * wave, n = first + kStep <= end ? (end - kStep - first) / kStride + 1 : 0;
+  const int tail = first + n * kStride;
+  LeadRows rows{kRows, 0, 0};
+  int leader = -1;
   if constexpr (LEAD) {
-    if (adapter_of(g, blockIdx.x) < 0) return;
-    count = lead_rows(g, lead);
+    leader = adapter_of(g, blockIdx.x);
+    if (leader < 0) return;
+    rows = lead_rows(g, leader);
   }
-  for (int group = 0; group < count; group += kRows) {
+  for (int group = 0; group < rows.count; group += kRows) {
     int64_t t;
-    if constexpr (LEAD) t = group + col < count ? lead.row[group + col] : g.rows;
-    else t = (int64_t)blockIdx.x * kRows + col;
-    const int mine = adapter_of(g, t);
+    int mine;
+    if constexpr (LEAD) {
+      t = rows.at(min(group + col, rows.count - 1));
+      mine = group + col < rows.count ? leader : -1;
+    } else {
+      t = (int64_t)blockIdx.x * kRows + col;
+      mine = adapter_of(g, t);
+    }
     // (32-bit offsets from the first row of the tile, or of all)
     const uint16_t* x = g.x + (LEAD ? 0 : (int64_t)blockIdx.x * kRows * g.x_ld);
     const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
@@ -137,10 +144,10 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       LowStep<RT> step[kAhead];
-      auto load = [&](LowStep<RT>& s, int k0) {
+      auto load = [&](LowStep<RT>& s, int i) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t k = k0 + 32 * h + 8 * quad;
+          const uint32_t k = first + i * kStride + 32 * h + 8 * quad;
           s.x[h] = vector_at(x + (at + k));
 #pragma unroll
           for (int j = 0; j < RT; ++j) s.a[h][j] = vector_at(a + (row[j] + k));
@@ -152,21 +159,33 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
 #pragma unroll
           for (int j = 0; j < RT; ++j) acc[j] = mfma(s.a[h][j], s.x[h], acc[j]);
       };
-      constexpr int kStride = kStep * kWaves;
-      const int first = begin + kStep * wave, last = end - kStep;   // last: where a whole step can begin
+      if (n >= kAhead) {   // (no load under a condition before the last steps: each is waited for alone)
+        int i = 0;
 #pragma unroll
-      for (int d = 0; d < kAhead; ++d)
-        if (first + d * kStride <= last) load(step[d], first + d * kStride);
-      int k0 = first;
-      for (; k0 <= last; k0 += kAhead * kStride) {
+        for (int d = 0; d < kAhead; ++d) load(step[d], d);
+        for (; i + 2 * kAhead <= n; i += kAhead) {
+#pragma unroll
+          for (int d = 0; d < kAhead; ++d) {
+            multiply(step[d]);
+            load(step[d], i + d + kAhead);
+          }
+        }
 #pragma unroll
         for (int d = 0; d < kAhead; ++d) {
-          const int k = k0 + d * kStride;
-          if (k <= last) multiply(step[d]);
-          if (k + kAhead * kStride <= last) load(step[d], k + kAhead * kStride);
+          multiply(step[d]);
+          if (i + d + kAhead < n) load(step[d], i + d + kAhead);
         }
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+          if (i + d + kAhead < n) multiply(step[d]);
+      } else {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+          if (d < n) load(step[d], d);
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d)
+          if (d < n) multiply(step[d]);
       }
-      const int tail = first + (last >= first ? (last - first) / kStride + 1 : 0) * kStride;
       if (tail < end) {   // the contraction ends inside this step
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -191,13 +210,18 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
       const int row = i / (RT * 4), c = i % (RT * 4) * 4;
       int64_t to;
-      if constexpr (LEAD) to = group + row < count ? lead.row[group + row] : g.rows;
-      else to = (int64_t)blockIdx.x * kRows + row;
-      if (to >= g.rows) continue;
+      bool in;
+      if constexpr (LEAD) {
+        in = group + row < rows.count;
+        to = rows.at(min(group + row, rows.count - 1));
+      } else {
+        to = (int64_t)blockIdx.x * kRows + row;
+        in = to < g.rows;
+      }
       f32x4 s = *reinterpret_cast<f32x4*>(&place[0][row][c]);
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(&place[w][row][c]);
-      *reinterpret_cast<f32x4*>(g.low + ((int64_t)blockIdx.y * g.rows + to) * (RT * 16) + c) = s;
+      if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)blockIdx.y * g.rows + to) * (RT * 16) + c) = s;
     }
   }
 }
@@ -222,66 +246,88 @@ template <int RT, int PARTS, typename T, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
-  constexpr int kQuads = kRows * RT * 4;                            // groups of four low-rank values of a tile
-  constexpr int kShare = kThreads / kQuads > 1 ? kThreads / kQuads : 1;   // threads that share one's slices
-  constexpr int kBatch = 8;                                         // slices loaded at once
-  __shared__ float place[kShare][kRows][RT * 16 + 4];
-  __shared__ LeadRows lead;
+  constexpr int kBatch = 8, kShares = 8;   // slices loaded at once; threads at most that share one value's slices
+  constexpr int kStride = kCols * kWaves;
+  struct Operands {
+    Raw8<T> base[2];
+    bf16x8 b[4][kRuns];
+  };
+  __shared__ f32x4 sums[kRows * RT * 4 > kThreads ? kRows * RT * 4 : kThreads];
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.y * g.per_block + kCols * wave, end = min(g.outs, (int)(blockIdx.y + 1) * g.per_block);
-  int count = kRows;
-  if constexpr (LEAD) count = lead_rows(g, lead);
-  for (int group = 0; group < count; group += kRows) {
+  LeadRows rows{kRows, 0, 0};
+  int leader = -1;
+  if constexpr (LEAD) {
+    leader = adapter_of(g, blockIdx.x);
+    rows = lead_rows(g, leader);
+  }
+  for (int group = 0; group < rows.count; group += kRows) {
+    const int here = LEAD ? min(kRows, rows.count - group) : kRows;   // rows of the tile
     auto row_of = [&](int i) -> int64_t {
-      if constexpr (LEAD) return group + i < count ? lead.row[group + i] : g.rows;
+      if constexpr (LEAD) return rows.at(min(group + i, rows.count - 1));
       else return (int64_t)blockIdx.x * kRows + i;
     };
     const int64_t t = row_of(col);
-    const int mine = adapter_of(g, t);
-    const bool any = __ballot(mine >= 0) != 0;
+    const bool real = LEAD ? col < here : t < g.rows;
+    const int64_t row = t < g.rows ? t : g.rows - 1;   // (lanes without a row load another's values, and drop them)
+    const int mine = LEAD ? (real ? leader : -1) : adapter_of(g, t);
+    const uint64_t with = __ballot(mine >= 0);
+    const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
+    // one adapter in the tile (and the registers for a second set of operands)
+    const bool alone = RT <= 4 && __ballot(mine >= 0 && mine != e0) == 0 && with != 0;
     auto load_base = [&](Raw8<T> (&v)[2], int c0) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + 16 * quad + 8 * h;
-        const bool in = g.base && c0 < end && t < g.rows && c < g.outs;
-        v[h] = in ? raw_at(static_cast<const T*>(g.base) + t * g.base_ld + c) : Raw8<T>{};
+      for (int h = 0; h < 2; ++h)
+        v[h] = raw_at(static_cast<const T*>(g.base) + row * g.base_ld + min(c0 + 16 * quad + 8 * h, g.outs - 8));
+    };
+    auto load_b = [&](bf16x8 (&v)[4][kRuns], int e, int c0) {
+      const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t bc = (uint32_t)min(c0 + 16 * (col >> 2) + 4 * j + (col & 3), g.outs - 1) * (uint32_t)g.r;
+#pragma unroll
+        for (int run = 0; run < kRuns; ++run)
+          v[j][run] = vector_at(b + (bc + (uint32_t)min(RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad, g.r - 8)));
       }
     };
-    Raw8<T> base[2];
-    load_base(base, first);
+    Operands now{};
+    if (alone && first < end) load_b(now.b, e0, first);
+    if (g.base && first < end) load_base(now.base, first);
     bf16x8 low[kSteps];
-    if (any) {   // (the wavefronts of a workgroup have the same rows)
+    if (with) {   // (the wavefronts of a workgroup have the same rows)
       if (LEAD && group > 0) __syncthreads();
       // the slices' sums, slices shared out among threads and loaded in batches
-      for (int i = threadIdx.x; i < kQuads * kShare; i += kThreads) {
-        const int row = i % kQuads / (RT * 4), c = i % (RT * 4) * 4, share = i / kQuads;
-        const int64_t from = row_of(row);
+      const int items = here * RT * 4, shares = max(1, min(kShares, kThreads / items));
+      for (int i0 = 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
+        const int i = min(i0 + (int)threadIdx.x, items * shares - 1), share = i / items, item = i - share * items;
+        const int64_t from = row_of(item / (RT * 4));
         f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (from < g.rows) {
-          const float* p = g.low + from * (RT * 16) + c;
-          for (int s0 = share; s0 < g.splits; s0 += kShare * kBatch) {
-            f32x4 v[kBatch];
+        const float* p = g.low + (from < g.rows ? from : g.rows - 1) * (RT * 16) + item % (RT * 4) * 4;
+        for (int s0 = share; s0 < g.splits; s0 += shares * kBatch) {
+          f32x4 v[kBatch];
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-              v[b] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + b * kShare, g.splits - 1) * g.rows * (RT * 16));
+          for (int b = 0; b < kBatch; ++b)
+            v[b] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + b * shares, g.splits - 1) * g.rows * (RT * 16));
 #pragma unroll
-            for (int b = 0; b < kBatch; ++b) sum += s0 + b * kShare < g.splits ? v[b] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-          }
+          for (int b = 0; b < kBatch; ++b) sum += s0 + b * shares < g.splits ? v[b] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         }
-        *reinterpret_cast<f32x4*>(&place[share][row][c]) = sum;
+        sums[i] = sum;
       }
-      __syncthreads();
       const float factor = mine >= 0 ? g.scale[mine] : 0.0f;
+      __syncthreads();
 #pragma unroll
       for (int run = 0; run < kRuns; ++run) {
-        const int rank = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
+        const int at = min(col, here - 1) * RT * 4 + (RT == 1 ? 2 * (quad & 1) : 8 * run + 2 * quad);
+        f32x4 lo = sums[at], hi = sums[at + 1];
+        for (int w = 1; w < shares; ++w) {
+          lo += sums[w * items + at];
+          hi += sums[w * items + at + 1];
+        }
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[i] = place[0][col][rank + i];
-#pragma unroll
-          for (int w = 1; w < kShare; ++w) v[i] += place[w][col][rank + i];
-          v[i] = mine >= 0 ? v[i] * factor : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          v[i] = mine >= 0 ? lo[i] * factor : 0.0f;
+          v[4 + i] = mine >= 0 ? hi[i] * factor : 0.0f;
         }
         if constexpr (RT == 1) {
 #pragma unroll
@@ -295,56 +341,71 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
         }
       }
     }
-    for (int c0 = first; c0 < end; c0 += kCols * kWaves) {
-      f32x4 kept[4];
+    // kept = the products with adapter e's rows of B, for the tokens that have e
+    auto multiply = [&](bf16x8 (&bv)[4][kRuns], int e, int rank, f32x4 (&kept)[4]) {
+      if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      Raw8<T> next[2];
-      load_base(next, c0 + kCols * kWaves);
-      for_adapters(mine, [&](int e) {
-        const int rank = rank_of(g, e);
-        const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
-        bf16x8 bv[4][kRuns];
+        for (int run = 0; run < kRuns; ++run) {
+          const int left = rank - (RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t bc = (uint32_t)min(c0 + 16 * (col >> 2) + 4 * j + (col & 3), g.outs - 1) * (uint32_t)g.r;
-#pragma unroll
-          for (int run = 0; run < kRuns; ++run) {
-            const int k = RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad;
-            bv[j][run] = vector_at(b + (bc + (uint32_t)min(k, g.r - 8)));
+          for (int j = 0; j < 4; ++j) {
+            uint4 q = __builtin_bit_cast(uint4, bv[j][run]);
+            q.x &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
+            q.y &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
+            q.z &= left > 5 ? ~0u : left > 4 ? 0xFFFFu : 0u;
+            q.w &= left > 7 ? ~0u : left > 6 ? 0xFFFFu : 0u;
+            bv[j][run] = __builtin_bit_cast(bf16x8, q);
           }
         }
-        if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
+      }
 #pragma unroll
-          for (int run = 0; run < kRuns; ++run) {
-            const int left = rank - (RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad);
+      for (int j = 0; j < 4; ++j) {
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (i >= left) bv[j][run][i] = (__bf16)0.0f;
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) acc = mfma(bv[j][RT == 1 ? 0 : s % kRuns], low[s], acc);
-          if (mine == e) kept[j] = acc;
-        }
-      });
-      const int c = c0 + 16 * quad;   // the lane's 16 columns
+        for (int s = 0; s < kSteps; ++s) acc = mfma(bv[j][RT == 1 ? 0 : s % kRuns], low[s], acc);
+        if (mine == e) kept[j] = acc;
+      }
+    };
+    auto store = [&](const Raw8<T> (&base)[2], const f32x4 (&kept)[4], int c0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (t >= g.rows || c + 8 * h >= g.outs) continue;
+        const int c = c0 + 16 * quad + 8 * h;   // the lane's 16 columns
+        if (!real || c >= g.outs) continue;
         float v[8];
-        T* to = static_cast<T*>(g.out) + t * g.out_ld + c + 8 * h;
         unpack8(base[h], v);
 #pragma unroll
         for (int i = 0; i < 8; ++i)   // (a row without an adapter keeps its base to the sign of a zero)
           v[i] = mine >= 0 ? v[i] + kept[2 * h + i / 4][i % 4] : v[i];
-        store8(to, v);
-        base[h] = next[h];
+        store8(static_cast<T*>(g.out) + t * g.out_ld + c, v);
+      }
+    };
+    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (alone) {   // the next columns' operands on their way while these are worked on
+      const int rank = rank_of(g, e0);
+      int c0 = first;
+      for (; c0 + kStride < end; c0 += kStride) {
+        Operands next{};
+        load_b(next.b, e0, c0 + kStride);
+        if (g.base) load_base(next.base, c0 + kStride);
+        f32x4 kept[4] = {none, none, none, none};
+        multiply(now.b, e0, rank, kept);
+        store(now.base, kept, c0);
+        now = next;
+      }
+      if (c0 < end) {
+        f32x4 kept[4] = {none, none, none, none};
+        multiply(now.b, e0, rank, kept);
+        store(now.base, kept, c0);
+      }
+    } else {
+      for (int c0 = first; c0 < end; c0 += kStride) {
+        f32x4 kept[4] = {none, none, none, none};
+        if (g.base && c0 > first) load_base(now.base, c0);
+        for_adapters(mine, [&](int e) {
+          load_b(now.b, e, c0);
+          multiply(now.b, e, rank_of(g, e), kept);
+        });
+        store(now.base, kept, c0);
       }
     }
   }
