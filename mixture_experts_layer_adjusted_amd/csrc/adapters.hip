@@ -37,7 +37,7 @@ struct AdapterArgs {
   int64_t rows, x_ld, base_ld, out_ld;
   int in, outs, n, r;
   int splits, per_split;         // slices of the first product, values of each
-  int per_block;                 // columns of a workgroup of the second product
+  int blocks, per_block;         // workgroups of a tile in the second product, columns of each
 };
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -66,7 +66,7 @@ __device__ __forceinline__ void for_adapters(int mine, F f) {
   }
 }
 
-// The rows of a workgroup that goes by adapters: blockIdx.x is a row, and if it is the first one with its adapter e
+// The rows of a workgroup that goes by adapters: `first` is its row, and if that is the first one with its adapter e
 // (or the first without one) the workgroup takes all rows that have the same; otherwise there are none.  Every wavefront
 // finds them by itself: a ballot for each 64 rows, and a permutation that brings the rows of e to the lanes in front.
 struct LeadRows {
@@ -76,8 +76,8 @@ struct LeadRows {
 __device__ __forceinline__ int bits_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
-__device__ __forceinline__ LeadRows lead_rows(const AdapterArgs& g, int e) {
-  const int lane = threadIdx.x & 63, first = blockIdx.x;
+__device__ __forceinline__ LeadRows lead_rows(const AdapterArgs& g, int first, int e) {
+  const int lane = threadIdx.x & 63;
   const bool is0 = lane < g.rows && adapter_of(g, lane) == e, is1 = lane + 64 < g.rows && adapter_of(g, lane + 64) == e;
   const uint64_t m0 = __ballot(is0), m1 = __ballot(is1);
   const uint64_t before = (uint64_t(1) << (first & 63)) - 1;
@@ -106,16 +106,17 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
   constexpr int kStride = kStep * kWaves;
   __shared__ float place[kWaves][kRows][RT * 16 + 4];
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int begin = blockIdx.y * g.per_split, end = min(g.in, begin + g.per_split);
+  const int64_t tile = blockIdx.x / g.splits;
+  const int slice = blockIdx.x - (unsigned)tile * g.splits, begin = slice * g.per_split, end = min(g.in, begin + g.per_split);
   // whole steps of the wavefront, and where a last one may end early
   const int first = begin + kStep * wave, n = first + kStep <= end ? (end - kStep - first) / kStride + 1 : 0;
   const int tail = first + n * kStride;
   LeadRows rows{kRows, 0, 0};
   int leader = -1;
   if constexpr (LEAD) {
-    leader = adapter_of(g, blockIdx.x);
+    leader = adapter_of(g, tile);
     if (leader < 0) return;
-    rows = lead_rows(g, leader);
+    rows = lead_rows(g, (int)tile, leader);
   }
   for (int group = 0; group < rows.count; group += kRows) {
     int64_t t;
@@ -124,11 +125,11 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
       t = rows.at(min(group + col, rows.count - 1));
       mine = group + col < rows.count ? leader : -1;
     } else {
-      t = (int64_t)blockIdx.x * kRows + col;
+      t = tile * kRows + col;
       mine = adapter_of(g, t);
     }
     // (32-bit offsets from the first row of the tile, or of all)
-    const uint16_t* x = g.x + (LEAD ? 0 : (int64_t)blockIdx.x * kRows * g.x_ld);
+    const uint16_t* x = g.x + (LEAD ? 0 : tile * kRows * g.x_ld);
     const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
     f32x4 kept[RT];
 #pragma unroll
@@ -215,13 +216,13 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
         in = group + row < rows.count;
         to = rows.at(min(group + row, rows.count - 1));
       } else {
-        to = (int64_t)blockIdx.x * kRows + row;
+        to = tile * kRows + row;
         in = to < g.rows;
       }
       f32x4 s = *reinterpret_cast<f32x4*>(&place[0][row][c]);
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(&place[w][row][c]);
-      if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)blockIdx.y * g.rows + to) * (RT * 16) + c) = s;
+      if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
     }
   }
 }
@@ -254,18 +255,20 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
   };
   __shared__ f32x4 sums[kRows * RT * 4 > kThreads ? kRows * RT * 4 : kThreads];
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int first = blockIdx.y * g.per_block + kCols * wave, end = min(g.outs, (int)(blockIdx.y + 1) * g.per_block);
+  const int64_t tile = blockIdx.x / g.blocks;
+  const int block = blockIdx.x - (unsigned)tile * g.blocks;
+  const int first = block * g.per_block + kCols * wave, end = min(g.outs, (block + 1) * g.per_block);
   LeadRows rows{kRows, 0, 0};
   int leader = -1;
   if constexpr (LEAD) {
-    leader = adapter_of(g, blockIdx.x);
-    rows = lead_rows(g, leader);
+    leader = adapter_of(g, tile);
+    rows = lead_rows(g, (int)tile, leader);
   }
   for (int group = 0; group < rows.count; group += kRows) {
     const int here = LEAD ? min(kRows, rows.count - group) : kRows;   // rows of the tile
     auto row_of = [&](int i) -> int64_t {
       if constexpr (LEAD) return rows.at(min(group + i, rows.count - 1));
-      else return (int64_t)blockIdx.x * kRows + i;
+      else return tile * kRows + i;
     };
     const int64_t t = row_of(col);
     const bool real = LEAD ? col < here : t < g.rows;
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
 struct AdapterPlan {
   int tiles16;                   // RT
   bool lead;                     // workgroups go by adapters
-  int splits, per_split, per_block;
+  int splits, per_split, blocks, per_block;
 };
 
 AdapterPlan plan_of(const moe_adapter_shape& s) {
@@ -425,17 +428,18 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));
   p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
-  const int64_t blocks = ceil_div(2048, tiles);
-  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, blocks), kCols * kWaves) * kCols * kWaves);
+  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(2048, tiles)), kCols * kWaves) * kCols * kWaves);
+  p.blocks = (int)ceil_div(s.out_cols, p.per_block);
   return p;
 }
 
 template <int RT, bool LEAD>
 hipError_t run_t(const AdapterArgs& g, int out_dtype, hipStream_t st) {
+  // (the slices or columns of a tile are neighbours in the grid: workgroups at work together cover whole rows)
   const unsigned tiles = (unsigned)(LEAD ? g.rows : ceil_div(g.rows, kRows));
-  const hipError_t err = launch_kernel(adapters_low_kernel<RT, LEAD>, dim3(tiles, (unsigned)g.splits), dim3(kThreads), 0, st, g);
+  const hipError_t err = launch_kernel(adapters_low_kernel<RT, LEAD>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g);
   if (err != hipSuccess) return err;
-  const dim3 grid(tiles, (unsigned)ceil_div(g.outs, g.per_block));
+  const dim3 grid(tiles * g.blocks);
   return out_dtype == MOE_DTYPE_F32
              ? launch_kernel(adapters_out_kernel<RT, 3, float, LEAD>, grid, dim3(kThreads), 0, st, g)
              : launch_kernel(adapters_out_kernel<RT, 2, uint16_t, LEAD>, grid, dim3(kThreads), 0, st, g);
@@ -471,6 +475,7 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       s.rank,
                       p.splits,
                       p.per_split,
+                      p.blocks,
                       p.per_block};
   switch (p.tiles16) {
     case 1: return p.lead ? run_t<1, true>(g, s.out_dtype, st) : run_t<1, false>(g, s.out_dtype, st);
