@@ -18,6 +18,8 @@ namespace moe {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 16;        // rows of a tile
@@ -92,25 +94,45 @@ __device__ __forceinline__ LeadRows lead_rows(const AdapterArgs& g, int first, i
   return l;
 }
 
-// The operands of one step of the first product: 64 values along the contraction, two of the instruction's
-template <int RT>
-struct LowStep {
-  bf16x8 x[2], a[2][RT];
+// One step of the first product for a tile of 16 rows (of x, or of A): 64 values of each, as they are loaded.  Eight
+// neighbouring lanes load a row's 128 bytes: the matrix instruction wants neighbouring lanes on different rows, which
+// the address unit takes one lane at a time (64 cycles a load in place of 16: the bound of both products before), so the
+// values go through LDS.  There chunk c of row m lies at c ^ (m mod 8): no two lanes of a read on the same banks.
+struct StepTile {
+  u32x4 q[2];   // rows lane / 8 and 8 + lane / 8
 };
+constexpr int kTileBytes = kRows * kStep * 2;
+__device__ __forceinline__ void tile_to_lds(char* to, const StepTile& s, int lane) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int m = 8 * h + (lane >> 3);
+    *reinterpret_cast<u32x4*>(to + m * 128 + ((lane & 7) ^ (m & 7)) * 16) = s.q[h];
+  }
+}
+// the instruction's operand for half h of the step
+__device__ __forceinline__ bf16x8 tile_operand(const char* from, int h, int lane) {
+  const int m = lane & 15;
+  return *reinterpret_cast<const bf16x8*>(from + m * 128 + ((4 * h + (lane >> 4)) ^ (m & 7)) * 16);
+}
 
 // The first product, transposed: ranks are the matrix instruction's rows, tokens its columns, so that a lane holds four
 // neighbouring ranks of one token.  RT tiles of 16 ranks.  A workgroup's wavefronts take every fourth run of 64.
 template <int RT, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
-  constexpr int kAhead = RT == 1 ? 3 : RT <= 4 ? 2 : 1;   // steps whose operands are in flight
+  constexpr int kAhead = RT == 1 ? 3 : RT == 2 ? 2 : 1;   // steps whose operands are in flight
   constexpr int kStride = kStep * kWaves;
-  __shared__ float place[kWaves][kRows][RT * 16 + 4];
+  constexpr int kAtOnce = RT < 4 ? RT : 4;                // tiles of A in LDS at once
+  constexpr int kPitch = RT * 16 + 4;                     // of the sums, which take the tiles' place
+  constexpr int kBytes = (1 + kAtOnce) * kTileBytes > kRows * kPitch * 4 ? (1 + kAtOnce) * kTileBytes : kRows * kPitch * 4;
+  __shared__ __align__(16) char lds[kWaves][kBytes];
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* mine_lds = lds[wave];
   const int64_t tile = blockIdx.x / g.splits;
   const int slice = blockIdx.x - (unsigned)tile * g.splits, begin = slice * g.per_split, end = min(g.in, begin + g.per_split);
   // whole steps of the wavefront, and where a last one may end early
   const int first = begin + kStep * wave, n = first + kStep <= end ? (end - kStep - first) / kStride + 1 : 0;
   const int tail = first + n * kStride;
+  const uint32_t chunk = 8 * (lane & 7);
   LeadRows rows{kRows, 0, 0};
   int leader = -1;
   if constexpr (LEAD) {
@@ -131,6 +153,9 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
     // (32-bit offsets from the first row of the tile, or of all)
     const uint16_t* x = g.x + (LEAD ? 0 : tile * kRows * g.x_ld);
     const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
+    uint32_t x_row[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) x_row[h] = (uint32_t)__shfl((int)at, 8 * h + (lane >> 3), 64) + chunk;
     f32x4 kept[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
@@ -138,27 +163,45 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
       const int rank = rank_of(g, e);
       if (rank == 0) return;
       const uint16_t* a = g.a + (int64_t)e * g.r * g.in;
-      uint32_t row[RT];   // of A; rows past the rank repeat the last one, their sums are dropped
+      uint32_t a_row[RT][2];   // rows past the rank repeat the last one, their sums are dropped
 #pragma unroll
-      for (int j = 0; j < RT; ++j) row[j] = (uint32_t)min(16 * j + col, rank - 1) * (uint32_t)g.in;
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) a_row[j][h] = (uint32_t)min(16 * j + 8 * h + (lane >> 3), rank - 1) * (uint32_t)g.in + chunk;
       f32x4 acc[RT];
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      LowStep<RT> step[kAhead];
-      auto load = [&](LowStep<RT>& s, int i) {
+      struct Step {
+        StepTile x, a[RT];
+      };
+      Step step[kAhead];
+      auto load = [&](Step& s, int i) {
+        const uint32_t k = first + i * kStride;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t k = first + i * kStride + 32 * h + 8 * quad;
-          s.x[h] = vector_at(x + (at + k));
+          s.x.q[h] = *reinterpret_cast<const u32x4*>(x + (x_row[h] + k));
 #pragma unroll
-          for (int j = 0; j < RT; ++j) s.a[h][j] = vector_at(a + (row[j] + k));
+          for (int j = 0; j < RT; ++j) s.a[j].q[h] = *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + k));
         }
       };
-      auto multiply = [&](const LowStep<RT>& s) {
+      auto multiply = [&](const Step& s) {
+        // (the LDS operations of one wavefront take effect in program order)
+        bf16x8 xv[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int j0 = 0; j0 < RT; j0 += kAtOnce) {
+          __builtin_amdgcn_wave_barrier();
+          if (j0 == 0) tile_to_lds(mine_lds, s.x, lane);
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[j] = mfma(s.a[h][j], s.x[h], acc[j]);
+          for (int j = 0; j < kAtOnce; ++j) tile_to_lds(mine_lds + (1 + j) * kTileBytes, s.a[j0 + j], lane);
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (j0 == 0) xv[h] = tile_operand(mine_lds, h, lane);
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j)
+              acc[j0 + j] = mfma(tile_operand(mine_lds + (1 + j) * kTileBytes, h, lane), xv[h], acc[j0 + j]);
+          }
+        }
       };
       if (n >= kAhead) {   // (no load under a condition before the last steps: each is waited for alone)
         int i = 0;
@@ -188,14 +231,17 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
           if (d < n) multiply(step[d]);
       }
       if (tail < end) {   // the contraction ends inside this step
+        Step s;
+        const bool in = tail + (int)chunk < end;
+        const u32x4 zero = {0u, 0u, 0u, 0u};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t k = tail + 32 * h + 8 * quad;
-          const bool in = (int)k < end;
-          const bf16x8 xv = in ? vector_at(x + (at + k)) : no_values();
+          s.x.q[h] = in ? *reinterpret_cast<const u32x4*>(x + (x_row[h] + (uint32_t)tail)) : zero;
 #pragma unroll
-          for (int j = 0; j < RT; ++j) acc[j] = mfma(in ? vector_at(a + (row[j] + k)) : no_values(), xv, acc[j]);
+          for (int j = 0; j < RT; ++j)
+            s.a[j].q[h] = in ? *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + (uint32_t)tail)) : zero;
         }
+        multiply(s);
       }
       if (mine == e) {
 #pragma unroll
@@ -204,9 +250,10 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
           for (int i = 0; i < 4; ++i) kept[j][i] = 16 * j + 4 * quad + i < rank ? acc[j][i] : 0.0f;
       }
     });
-    if (LEAD && group > 0) __syncthreads();
+    __builtin_amdgcn_wave_barrier();
 #pragma unroll
-    for (int j = 0; j < RT; ++j) *reinterpret_cast<f32x4*>(&place[wave][col][16 * j + 4 * quad]) = kept[j];
+    for (int j = 0; j < RT; ++j)
+      *reinterpret_cast<f32x4*>(mine_lds + (col * kPitch + 16 * j + 4 * quad) * 4) = kept[j];
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
       const int row = i / (RT * 4), c = i % (RT * 4) * 4;
@@ -219,11 +266,12 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
         to = tile * kRows + row;
         in = to < g.rows;
       }
-      f32x4 s = *reinterpret_cast<f32x4*>(&place[0][row][c]);
+      f32x4 s = *reinterpret_cast<f32x4*>(lds[0] + (row * kPitch + c) * 4);
 #pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(&place[w][row][c]);
+      for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(lds[w] + (row * kPitch + c) * 4);
       if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
     }
+    if (LEAD && group + kRows < rows.count) __syncthreads();
   }
 }
 
@@ -240,8 +288,30 @@ __device__ __forceinline__ bf16x8 part_of(float (&v)[8]) {
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
-// The second product, transposed as well: output columns are the instruction's rows, in an order that leaves a lane 16
-// neighbouring columns of its token (row m of tile j is column 16 (m / 4) + 4 j + m % 4 of the wavefront's 64).
+// four neighbouring values of base or out, as they lie in memory
+template <typename T>
+struct RawFour;
+template <>
+struct RawFour<uint16_t> {
+  u32x2 w;
+  __device__ __forceinline__ float at(int k) const {
+    return __uint_as_float(k & 1 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+  }
+  __device__ __forceinline__ void set(const float (&v)[4]) { w = u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}; }
+};
+template <>
+struct RawFour<float> {
+  u32x4 w;
+  __device__ __forceinline__ float at(int k) const { return __uint_as_float(w[k]); }
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    w = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+  }
+};
+
+// The second product: tokens are the matrix instruction's rows, output columns its columns, in an order that leaves a lane
+// four neighbouring columns of four tokens (lane n of tile j: column 4 n + j of the wavefront's 64), so that base and out
+// go in whole lines.  B, whose rows for neighbouring columns lie side by side, is loaded as it lies
+// and read from LDS, its 16-byte chunks turned so that the lanes of a read meet on no bank.
 // PARTS bf16 parts of the low-rank values.  RT == 1: one run of 32 holds two parts.
 template <int RT, int PARTS, typename T, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
@@ -249,12 +319,21 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
   constexpr int kBatch = 8, kShares = 8;   // slices loaded at once; threads at most that share one value's slices
   constexpr int kStride = kCols * kWaves;
+  constexpr int kChunks = kCols * RT * 2;                           // 16-byte chunks of B in LDS, RT * 2 a column
+  constexpr int kTurn = RT * 8 > 16 ? RT * 8 : 16;                  // chunks after which the next turn begins
+  constexpr int kLoads = kChunks / 64;
   struct Operands {
-    Raw8<T> base[2];
-    bf16x8 b[4][kRuns];
+    RawFour<T> base[4];
+    u32x4 b[kLoads];
   };
-  __shared__ f32x4 sums[kRows * RT * 4 > kThreads ? kRows * RT * 4 : kThreads];
+  constexpr int kSums = kRows * RT * 4 > kThreads ? kRows * RT * 4 : kThreads;
+  constexpr bool kShared = RT == 8;        // the sums lie where B will (64 KB in all)
+  __shared__ __align__(16) char lds[kWaves][kChunks * 16];
+  __shared__ f32x4 own_sums[kShared ? 1 : kSums];
+  f32x4* sums = kShared ? reinterpret_cast<f32x4*>(lds[0]) : own_sums;
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  char* mine_lds = lds[wave];
+  auto chunk_at = [&](int i) { return mine_lds + ((i & ~15) | ((i + i / kTurn) & 15)) * 16; };
   const int64_t tile = blockIdx.x / g.blocks;
   const int block = blockIdx.x - (unsigned)tile * g.blocks;
   const int first = block * g.per_block + kCols * wave, end = min(g.outs, (block + 1) * g.per_block);
@@ -265,37 +344,43 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
     rows = lead_rows(g, (int)tile, leader);
   }
   for (int group = 0; group < rows.count; group += kRows) {
-    const int here = LEAD ? min(kRows, rows.count - group) : kRows;   // rows of the tile
-    auto row_of = [&](int i) -> int64_t {
-      if constexpr (LEAD) return rows.at(min(group + i, rows.count - 1));
-      else return tile * kRows + i;
+    const int here = LEAD ? min(kRows, rows.count - group) : (int)min((int64_t)kRows, g.rows - tile * kRows);   // rows of the tile
+    auto row_of = [&](int i) -> int64_t {   // (rows the tile does not have: its last one)
+      if constexpr (LEAD) return rows.at(group + min(i, here - 1));
+      else return tile * kRows + min(i, here - 1);
     };
     const int64_t t = row_of(col);
-    const bool real = LEAD ? col < here : t < g.rows;
-    const int64_t row = t < g.rows ? t : g.rows - 1;   // (lanes without a row load another's values, and drop them)
-    const int mine = LEAD ? (real ? leader : -1) : adapter_of(g, t);
+    const int mine = col < here ? (LEAD ? leader : adapter_of(g, t)) : -1;
     const uint64_t with = __ballot(mine >= 0);
     const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
     // one adapter in the tile (and the registers for a second set of operands)
-    const bool alone = RT <= 4 && __ballot(mine >= 0 && mine != e0) == 0 && with != 0;
-    auto load_base = [&](Raw8<T> (&v)[2], int c0) {
+    const bool alone = RT <= 2 && __ballot(mine >= 0 && mine != e0) == 0 && with != 0;
+    // the lane's four tokens of the result, and their adapters
+    int64_t out_row[4];
+    int theirs[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        v[h] = raw_at(static_cast<const T*>(g.base) + row * g.base_ld + min(c0 + 16 * quad + 8 * h, g.outs - 8));
+    for (int i = 0; i < 4; ++i) {
+      out_row[i] = row_of(4 * quad + i);
+      theirs[i] = __shfl(mine, 4 * quad + i, 64);
+    }
+    auto load_base = [&](Operands& o, int c0) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        o.base[i] = *reinterpret_cast<const RawFour<T>*>(static_cast<const T*>(g.base) + out_row[i] * g.base_ld +
+                                                         min(c0 + 4 * col, g.outs - 4));
     };
-    auto load_b = [&](bf16x8 (&v)[4][kRuns], int e, int c0) {
+    auto load_b = [&](Operands& o, int e, int c0) {
       const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t bc = (uint32_t)min(c0 + 16 * (col >> 2) + 4 * j + (col & 3), g.outs - 1) * (uint32_t)g.r;
-#pragma unroll
-        for (int run = 0; run < kRuns; ++run)
-          v[j][run] = vector_at(b + (bc + (uint32_t)min(RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad, g.r - 8)));
+      for (int l = 0; l < kLoads; ++l) {
+        const int i = 64 * l + lane;
+        o.b[l] = *reinterpret_cast<const u32x4*>(b + ((uint32_t)min(c0 + i / (RT * 2), g.outs - 1) * (uint32_t)g.r +
+                                                      (uint32_t)min(i % (RT * 2) * 8, g.r - 8)));
       }
     };
     Operands now{};
-    if (alone && first < end) load_b(now.b, e0, first);
-    if (g.base && first < end) load_base(now.base, first);
+    if (alone && first < end) load_b(now, e0, first);
+    if (g.base && first < end) load_base(now, first);
     bf16x8 low[kSteps];
     if (with) {   // (the wavefronts of a workgroup have the same rows)
       if (LEAD && group > 0) __syncthreads();
@@ -303,9 +388,8 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
       const int items = here * RT * 4, shares = max(1, min(kShares, kThreads / items));
       for (int i0 = 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
         const int i = min(i0 + (int)threadIdx.x, items * shares - 1), share = i / items, item = i - share * items;
-        const int64_t from = row_of(item / (RT * 4));
         f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        const float* p = g.low + (from < g.rows ? from : g.rows - 1) * (RT * 16) + item % (RT * 4) * 4;
+        const float* p = g.low + row_of(item / (RT * 4)) * (RT * 16) + item % (RT * 4) * 4;
         for (int s0 = share; s0 < g.splits; s0 += shares * kBatch) {
           f32x4 v[kBatch];
 #pragma unroll
@@ -343,72 +427,85 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
           for (int p = 0; p < PARTS; ++p) low[p * kRuns + run] = part_of(v);
         }
       }
+      if (kShared) __syncthreads();
     }
     // kept = the products with adapter e's rows of B, for the tokens that have e
-    auto multiply = [&](bf16x8 (&bv)[4][kRuns], int e, int rank, f32x4 (&kept)[4]) {
-      if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
+    auto multiply = [&](const Operands& o, int e, int rank, f32x4 (&kept)[4]) {
+      __builtin_amdgcn_wave_barrier();   // (the LDS operations of one wavefront take effect in program order)
 #pragma unroll
-        for (int run = 0; run < kRuns; ++run) {
-          const int left = rank - (RT == 1 ? 8 * (quad & 1) : 32 * run + 8 * quad);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint4 q = __builtin_bit_cast(uint4, bv[j][run]);
-            q.x &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
-            q.y &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
-            q.z &= left > 5 ? ~0u : left > 4 ? 0xFFFFu : 0u;
-            q.w &= left > 7 ? ~0u : left > 6 ? 0xFFFFu : 0u;
-            bv[j][run] = __builtin_bit_cast(bf16x8, q);
-          }
+      for (int l = 0; l < kLoads; ++l) {
+        const int i = 64 * l + lane;
+        u32x4 q = o.b[l];
+        if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
+          const int left = rank - i % (RT * 2) * 8;
+          q[0] &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
+          q[1] &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
+          q[2] &= left > 5 ? ~0u : left > 4 ? 0xFFFFu : 0u;
+          q[3] &= left > 7 ? ~0u : left > 6 ? 0xFFFFu : 0u;
         }
+        *reinterpret_cast<u32x4*>(chunk_at(i)) = q;
       }
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const int c = 4 * col + j;   // the lane's column of this tile
+        bf16x8 bv[kRuns];
+#pragma unroll
+        for (int run = 0; run < kRuns; ++run)
+          bv[run] = *reinterpret_cast<const bf16x8*>(chunk_at(c * RT * 2 + (RT == 1 ? quad & 1 : 4 * run + quad)));
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) acc = mfma(bv[j][RT == 1 ? 0 : s % kRuns], low[s], acc);
-        if (mine == e) kept[j] = acc;
+        for (int s = 0; s < kSteps; ++s) acc = mfma(low[s], bv[RT == 1 ? 0 : s % kRuns], acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
       }
     };
-    auto store = [&](const Raw8<T> (&base)[2], const f32x4 (&kept)[4], int c0) {
+    auto store = [&](const Operands& o, const f32x4 (&kept)[4], int c0) {
+      const int c = c0 + 4 * col;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int c = c0 + 16 * quad + 8 * h;   // the lane's 16 columns
-        if (!real || c >= g.outs) continue;
-        float v[8];
-        unpack8(base[h], v);
+      for (int i = 0; i < 4; ++i) {
+        if (4 * quad + i >= here || c >= g.outs) continue;
+        float v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i)   // (a row without an adapter keeps its base to the sign of a zero)
-          v[i] = mine >= 0 ? v[i] + kept[2 * h + i / 4][i % 4] : v[i];
-        store8(static_cast<T*>(g.out) + t * g.out_ld + c, v);
+        for (int k = 0; k < 4; ++k)   // (a row without an adapter keeps its base to the sign of a zero)
+          v[k] = theirs[i] >= 0 ? o.base[i].at(k) + kept[k][i] : o.base[i].at(k);
+        RawFour<T> p;
+        p.set(v);
+        *reinterpret_cast<RawFour<T>*>(static_cast<T*>(g.out) + out_row[i] * g.out_ld + c) = p;
       }
     };
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto clear = [&](f32x4 (&kept)[4]) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kept[j] = none;
+    };
+    f32x4 kept[4];
     if (alone) {   // the next columns' operands on their way while these are worked on
       const int rank = rank_of(g, e0);
       int c0 = first;
       for (; c0 + kStride < end; c0 += kStride) {
         Operands next{};
-        load_b(next.b, e0, c0 + kStride);
-        if (g.base) load_base(next.base, c0 + kStride);
-        f32x4 kept[4] = {none, none, none, none};
-        multiply(now.b, e0, rank, kept);
-        store(now.base, kept, c0);
+        load_b(next, e0, c0 + kStride);
+        if (g.base) load_base(next, c0 + kStride);
+        clear(kept);
+        multiply(now, e0, rank, kept);
+        store(now, kept, c0);
         now = next;
       }
       if (c0 < end) {
-        f32x4 kept[4] = {none, none, none, none};
-        multiply(now.b, e0, rank, kept);
-        store(now.base, kept, c0);
+        clear(kept);
+        multiply(now, e0, rank, kept);
+        store(now, kept, c0);
       }
     } else {
       for (int c0 = first; c0 < end; c0 += kStride) {
-        f32x4 kept[4] = {none, none, none, none};
-        if (g.base && c0 > first) load_base(now.base, c0);
+        clear(kept);
+        if (g.base && c0 > first) load_base(now, c0);
         for_adapters(mine, [&](int e) {
-          load_b(now.b, e, c0);
-          multiply(now.b, e, rank_of(g, e), kept);
+          load_b(now, e, c0);
+          multiply(now, e, rank_of(g, e), kept);
         });
-        store(now.base, kept, c0);
+        store(now, kept, c0);
       }
     }
   }
@@ -428,7 +525,8 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));
   p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
-  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(2048, tiles)), kCols * kWaves) * kCols * kWaves);
+  const int64_t stride = kCols * kWaves;
+  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(2048, tiles)), stride) * stride);
   p.blocks = (int)ceil_div(s.out_cols, p.per_block);
   return p;
 }
