@@ -314,7 +314,7 @@ struct RawFour<float> {
 // and read from LDS, its 16-byte chunks turned so that the lanes of a read meet on no bank.
 // PARTS bf16 parts of the low-rank values.  RT == 1: one run of 32 holds two parts.
 template <int RT, int PARTS, typename T, bool LEAD>
-__global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
+__global__ void __launch_bounds__(kThreads, RT == 1 || (RT == 2 && !LEAD) ? 3 : 1) adapters_out_kernel(AdapterArgs g) {
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
   constexpr int kBatch = 8, kShares = 8;   // slices loaded at once; threads at most that share one value's slices
@@ -353,8 +353,7 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
     const int mine = col < here ? (LEAD ? leader : adapter_of(g, t)) : -1;
     const uint64_t with = __ballot(mine >= 0);
     const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
-    // one adapter in the tile (and the registers for a second set of operands)
-    const bool alone = RT <= 2 && __ballot(mine >= 0 && mine != e0) == 0 && with != 0;
+    const bool alone = RT <= 4 && with != 0 && __ballot(mine >= 0 && mine != e0) == 0;   // one adapter in the tile
     // the lane's four tokens of the result, and their adapters
     int64_t out_row[4];
     int theirs[4];
@@ -480,17 +479,25 @@ __global__ void __launch_bounds__(kThreads) adapters_out_kernel(AdapterArgs g) {
       for (int j = 0; j < 4; ++j) kept[j] = none;
     };
     f32x4 kept[4];
-    if (alone) {   // the next columns' operands on their way while these are worked on
+    if (alone) {
       const int rank = rank_of(g, e0);
       int c0 = first;
       for (; c0 + kStride < end; c0 += kStride) {
-        Operands next{};
-        load_b(next, e0, c0 + kStride);
-        if (g.base) load_base(next, c0 + kStride);
-        clear(kept);
-        multiply(now, e0, rank, kept);
-        store(now, kept, c0);
-        now = next;
+        if constexpr (RT <= 2) {   // the next columns' operands on their way while these are worked on
+          Operands next{};
+          load_b(next, e0, c0 + kStride);
+          if (g.base) load_base(next, c0 + kStride);
+          clear(kept);
+          multiply(now, e0, rank, kept);
+          store(now, kept, c0);
+          now = next;
+        } else {   // (no registers for a second set)
+          clear(kept);
+          multiply(now, e0, rank, kept);
+          store(now, kept, c0);
+          load_b(now, e0, c0 + kStride);
+          if (g.base) load_base(now, c0 + kStride);
+        }
       }
       if (c0 < end) {
         clear(kept);
