@@ -21,11 +21,15 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kWaves = 4, kThreads = 64 * kWaves, kWavesOfTile = kWaves;
 constexpr int kRows = 16;        // rows of a tile
 constexpr int kStep = 64;        // values of a wavefront's step along the first product's contraction
 constexpr int kCols = 64;        // output columns of a wavefront at a time
 constexpr int kLeadRows = 128;   // rows at most where workgroups go by adapters
+// One launch in place of two up to so many rows and values of an adapter's A, which every workgroup then reads whole.
+// In a graph, us, one kernel against two: 1 row, 16 x 2048 -> 7168: 5.4, 7.1; 16 rows, 32 x 2048 -> 4096: 7.5, 7.7;
+// 1 row, 16 x 7168 -> 4096: 8.2, 7.1; 32 rows, 32 x 2048 -> 4096: 8.5, 8.4.
+constexpr int kFewRows = 16, kFewValues = 1 << 16;
 
 struct AdapterArgs {
   const uint16_t* x;
@@ -115,24 +119,151 @@ __device__ __forceinline__ bf16x8 tile_operand(const char* from, int h, int lane
   return *reinterpret_cast<const bf16x8*>(from + m * 128 + ((4 * h + (lane >> 4)) ^ (m & 7)) * 16);
 }
 
+// LDS of a wavefront in the first product: a tile of x and up to four of A; the sums then take their place
+template <int RT>
+struct LowLds {
+  static constexpr int kAtOnce = RT < 4 ? RT : 4;
+  static constexpr int kPitch = RT * 16 + 4;   // values between the sums of neighbouring tokens
+  static constexpr int kTiles = (1 + kAtOnce) * kTileBytes, kSums = kRows * kPitch * 4;
+  static constexpr int kBytes = kTiles > kSums ? kTiles : kSums;
+};
+
 // The first product, transposed: ranks are the matrix instruction's rows, tokens its columns, so that a lane holds four
-// neighbouring ranks of one token.  RT tiles of 16 ranks.  A workgroup's wavefronts take every fourth run of 64.
+// neighbouring ranks of one token.  RT tiles of 16 ranks, kept[j]: ranks 16 j + 4 (lane / 16) of token lane mod 16, whose
+// adapter is `mine` and whose row of x begins at x + at.  The values from begin on, of which the wavefront takes
+// every waves-th run of 64, the operands of kAhead of them in flight.
+template <int RT, int kAhead>
+__device__ __forceinline__ void low_sums(const AdapterArgs& g, const uint16_t* x, uint32_t at, int mine, int begin, int end,
+                                         int wave, int waves, char* lds, f32x4 (&kept)[RT]) {
+  constexpr int kAtOnce = LowLds<RT>::kAtOnce;
+  const int lane = threadIdx.x & 63, quad = lane >> 4, stride = kStep * waves;
+  // whole steps of the wavefront, and where a last one may end early
+  const int first = begin + kStep * wave, n = first + kStep <= end ? (end - kStep - first) / stride + 1 : 0;
+  const int tail = first + n * stride;
+  const uint32_t chunk = 8 * (lane & 7);
+  uint32_t x_row[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) x_row[h] = (uint32_t)__shfl((int)at, 8 * h + (lane >> 3), 64) + chunk;
+#pragma unroll
+  for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  for_adapters(mine, [&](int e) {
+    const int rank = rank_of(g, e);
+    if (rank == 0) return;
+    const uint16_t* a = g.a + (int64_t)e * g.r * g.in;
+    uint32_t a_row[RT][2];   // rows past the rank repeat the last one, their sums are dropped
+#pragma unroll
+    for (int j = 0; j < RT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) a_row[j][h] = (uint32_t)min(16 * j + 8 * h + (lane >> 3), rank - 1) * (uint32_t)g.in + chunk;
+    f32x4 acc[RT];
+#pragma unroll
+    for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    struct Step {
+      StepTile x, a[RT];
+    };
+    Step step[kAhead];
+    auto load = [&](Step& s, int i) {
+      const uint32_t k = first + i * stride;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s.x.q[h] = *reinterpret_cast<const u32x4*>(x + (x_row[h] + k));
+#pragma unroll
+        for (int j = 0; j < RT; ++j) s.a[j].q[h] = *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + k));
+      }
+    };
+    auto multiply = [&](const Step& s) {
+      // (the LDS operations of one wavefront take effect in program order)
+      bf16x8 xv[2];
+#pragma unroll
+      for (int j0 = 0; j0 < RT; j0 += kAtOnce) {
+        __builtin_amdgcn_wave_barrier();
+        if (j0 == 0) tile_to_lds(lds, s.x, lane);
+#pragma unroll
+        for (int j = 0; j < kAtOnce; ++j) tile_to_lds(lds + (1 + j) * kTileBytes, s.a[j0 + j], lane);
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (j0 == 0) xv[h] = tile_operand(lds, h, lane);
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            acc[j0 + j] = mfma(tile_operand(lds + (1 + j) * kTileBytes, h, lane), xv[h], acc[j0 + j]);
+        }
+      }
+    };
+    if (n >= kAhead) {   // (no load under a condition before the last steps: each is waited for alone)
+      int i = 0;
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) load(step[d], d);
+      for (; i + 2 * kAhead <= n; i += kAhead) {
+#pragma unroll
+        for (int d = 0; d < kAhead; ++d) {
+          multiply(step[d]);
+          load(step[d], i + d + kAhead);
+        }
+      }
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d) {
+        multiply(step[d]);
+        if (i + d + kAhead < n) load(step[d], i + d + kAhead);
+      }
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d)
+        if (i + d + kAhead < n) multiply(step[d]);
+    } else {
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d)
+        if (d < n) load(step[d], d);
+#pragma unroll
+      for (int d = 0; d < kAhead; ++d)
+        if (d < n) multiply(step[d]);
+    }
+    if (tail < end) {   // the contraction ends inside this step
+      Step s;
+      const bool in = tail + (int)chunk < end;
+      const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        s.x.q[h] = in ? *reinterpret_cast<const u32x4*>(x + (x_row[h] + (uint32_t)tail)) : zero;
+#pragma unroll
+        for (int j = 0; j < RT; ++j)
+          s.a[j].q[h] = in ? *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + (uint32_t)tail)) : zero;
+      }
+      multiply(s);
+    }
+    if (mine == e) {
+#pragma unroll
+      for (int j = 0; j < RT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kept[j][i] = 16 * j + 4 * quad + i < rank ? acc[j][i] : 0.0f;
+    }
+  });
+}
+
+// leaves the wavefront's sums in its LDS, a token's side by side
+template <int RT>
+__device__ __forceinline__ void leave_sums(const f32x4 (&kept)[RT], char* lds) {
+  const int lane = threadIdx.x & 63;
+  __builtin_amdgcn_wave_barrier();
+#pragma unroll
+  for (int j = 0; j < RT; ++j)
+    *reinterpret_cast<f32x4*>(lds + ((lane & 15) * LowLds<RT>::kPitch + 16 * j + 4 * (lane >> 4)) * 4) = kept[j];
+}
+// the sum over the wavefronts' sums, four ranks from c on of the tile's row
+template <int RT, int WAVES, int BYTES>
+__device__ __forceinline__ f32x4 sum_of_waves(const char (&lds)[WAVES][BYTES], int row, int c) {
+  f32x4 s = *reinterpret_cast<const f32x4*>(lds[0] + (row * LowLds<RT>::kPitch + c) * 4);
+#pragma unroll
+  for (int w = 1; w < WAVES; ++w) s += *reinterpret_cast<const f32x4*>(lds[w] + (row * LowLds<RT>::kPitch + c) * 4);
+  return s;
+}
+
+// A slice of the first product for a tile of rows, or for the rows of an adapter.
 template <int RT, bool LEAD>
 __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
-  constexpr int kAhead = RT == 1 ? 3 : RT == 2 ? 2 : 1;   // steps whose operands are in flight
-  constexpr int kStride = kStep * kWaves;
-  constexpr int kAtOnce = RT < 4 ? RT : 4;                // tiles of A in LDS at once
-  constexpr int kPitch = RT * 16 + 4;                     // of the sums, which take the tiles' place
-  constexpr int kBytes = (1 + kAtOnce) * kTileBytes > kRows * kPitch * 4 ? (1 + kAtOnce) * kTileBytes : kRows * kPitch * 4;
-  __shared__ __align__(16) char lds[kWaves][kBytes];
-  const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  char* mine_lds = lds[wave];
+  __shared__ __align__(16) char lds[kWaves][LowLds<RT>::kBytes];
+  const int lane = threadIdx.x & 63, col = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t tile = blockIdx.x / g.splits;
   const int slice = blockIdx.x - (unsigned)tile * g.splits, begin = slice * g.per_split, end = min(g.in, begin + g.per_split);
-  // whole steps of the wavefront, and where a last one may end early
-  const int first = begin + kStep * wave, n = first + kStep <= end ? (end - kStep - first) / kStride + 1 : 0;
-  const int tail = first + n * kStride;
-  const uint32_t chunk = 8 * (lane & 7);
   LeadRows rows{kRows, 0, 0};
   int leader = -1;
   if constexpr (LEAD) {
@@ -151,109 +282,10 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
       mine = adapter_of(g, t);
     }
     // (32-bit offsets from the first row of the tile, or of all)
-    const uint16_t* x = g.x + (LEAD ? 0 : tile * kRows * g.x_ld);
     const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
-    uint32_t x_row[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) x_row[h] = (uint32_t)__shfl((int)at, 8 * h + (lane >> 3), 64) + chunk;
     f32x4 kept[RT];
-#pragma unroll
-    for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for_adapters(mine, [&](int e) {
-      const int rank = rank_of(g, e);
-      if (rank == 0) return;
-      const uint16_t* a = g.a + (int64_t)e * g.r * g.in;
-      uint32_t a_row[RT][2];   // rows past the rank repeat the last one, their sums are dropped
-#pragma unroll
-      for (int j = 0; j < RT; ++j)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) a_row[j][h] = (uint32_t)min(16 * j + 8 * h + (lane >> 3), rank - 1) * (uint32_t)g.in + chunk;
-      f32x4 acc[RT];
-#pragma unroll
-      for (int j = 0; j < RT; ++j) acc[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      struct Step {
-        StepTile x, a[RT];
-      };
-      Step step[kAhead];
-      auto load = [&](Step& s, int i) {
-        const uint32_t k = first + i * kStride;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s.x.q[h] = *reinterpret_cast<const u32x4*>(x + (x_row[h] + k));
-#pragma unroll
-          for (int j = 0; j < RT; ++j) s.a[j].q[h] = *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + k));
-        }
-      };
-      auto multiply = [&](const Step& s) {
-        // (the LDS operations of one wavefront take effect in program order)
-        bf16x8 xv[2];
-#pragma unroll
-        for (int j0 = 0; j0 < RT; j0 += kAtOnce) {
-          __builtin_amdgcn_wave_barrier();
-          if (j0 == 0) tile_to_lds(mine_lds, s.x, lane);
-#pragma unroll
-          for (int j = 0; j < kAtOnce; ++j) tile_to_lds(mine_lds + (1 + j) * kTileBytes, s.a[j0 + j], lane);
-          __builtin_amdgcn_wave_barrier();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            if (j0 == 0) xv[h] = tile_operand(mine_lds, h, lane);
-#pragma unroll
-            for (int j = 0; j < kAtOnce; ++j)
-              acc[j0 + j] = mfma(tile_operand(mine_lds + (1 + j) * kTileBytes, h, lane), xv[h], acc[j0 + j]);
-          }
-        }
-      };
-      if (n >= kAhead) {   // (no load under a condition before the last steps: each is waited for alone)
-        int i = 0;
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) load(step[d], d);
-        for (; i + 2 * kAhead <= n; i += kAhead) {
-#pragma unroll
-          for (int d = 0; d < kAhead; ++d) {
-            multiply(step[d]);
-            load(step[d], i + d + kAhead);
-          }
-        }
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d) {
-          multiply(step[d]);
-          if (i + d + kAhead < n) load(step[d], i + d + kAhead);
-        }
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d)
-          if (i + d + kAhead < n) multiply(step[d]);
-      } else {
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d)
-          if (d < n) load(step[d], d);
-#pragma unroll
-        for (int d = 0; d < kAhead; ++d)
-          if (d < n) multiply(step[d]);
-      }
-      if (tail < end) {   // the contraction ends inside this step
-        Step s;
-        const bool in = tail + (int)chunk < end;
-        const u32x4 zero = {0u, 0u, 0u, 0u};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          s.x.q[h] = in ? *reinterpret_cast<const u32x4*>(x + (x_row[h] + (uint32_t)tail)) : zero;
-#pragma unroll
-          for (int j = 0; j < RT; ++j)
-            s.a[j].q[h] = in ? *reinterpret_cast<const u32x4*>(a + (a_row[j][h] + (uint32_t)tail)) : zero;
-        }
-        multiply(s);
-      }
-      if (mine == e) {
-#pragma unroll
-        for (int j = 0; j < RT; ++j)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) kept[j][i] = 16 * j + 4 * quad + i < rank ? acc[j][i] : 0.0f;
-      }
-    });
-    __builtin_amdgcn_wave_barrier();
-#pragma unroll
-    for (int j = 0; j < RT; ++j)
-      *reinterpret_cast<f32x4*>(mine_lds + (col * kPitch + 16 * j + 4 * quad) * 4) = kept[j];
+    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1>(g, g.x + (LEAD ? 0 : tile * kRows * g.x_ld), at, mine, begin, end, wave, kWaves, lds[wave], kept);
+    leave_sums<RT>(kept, lds[wave]);
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
       const int row = i / (RT * 4), c = i % (RT * 4) * 4;
@@ -266,9 +298,7 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
         to = tile * kRows + row;
         in = to < g.rows;
       }
-      f32x4 s = *reinterpret_cast<f32x4*>(lds[0] + (row * kPitch + c) * 4);
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) s += *reinterpret_cast<f32x4*>(lds[w] + (row * kPitch + c) * 4);
+      const f32x4 s = sum_of_waves<RT>(lds, row, c);
       if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
     }
     if (LEAD && group + kRows < rows.count) __syncthreads();
@@ -313,8 +343,15 @@ struct RawFour<float> {
 // go in whole lines.  B, whose rows for neighbouring columns lie side by side, is loaded as it lies
 // and read from LDS, its 16-byte chunks turned so that the lanes of a read meet on no bank.
 // PARTS bf16 parts of the low-rank values.  RT == 1: one run of 32 holds two parts.
-template <int RT, int PARTS, typename T, bool LEAD>
-__global__ void __launch_bounds__(kThreads, RT == 1 || (RT == 2 && !LEAD) ? 3 : 1) adapters_out_kernel(AdapterArgs g) {
+// FORM: tiles of neighbouring rows, the rows of an adapter, or those with the first product in the same kernel (each
+// workgroup computes it whole, for its columns: for few rows and little of A that is less than a launch more).
+enum AdapterForm { kTileForm, kLeadForm, kFewForm };
+constexpr int kFewWaves = 8;
+template <int RT, int PARTS, typename T, int FORM>
+__global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, FORM != kFewForm && (RT == 1 || (RT == 2 && FORM == kTileForm)) ? 3 : 1)
+    adapters_out_kernel(AdapterArgs g) {
+  constexpr bool LEAD = FORM != kTileForm, FEW = FORM == kFewForm;
+  constexpr int kWaves = FEW ? kFewWaves : kWavesOfTile, kThreads = 64 * kWaves;
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
   constexpr int kBatch = 8, kShares = 8;   // slices loaded at once; threads at most that share one value's slices
@@ -328,7 +365,8 @@ __global__ void __launch_bounds__(kThreads, RT == 1 || (RT == 2 && !LEAD) ? 3 : 
   };
   constexpr int kSums = kRows * RT * 4 > kThreads ? kRows * RT * 4 : kThreads;
   constexpr bool kShared = RT == 8;        // the sums lie where B will (64 KB in all)
-  __shared__ __align__(16) char lds[kWaves][kChunks * 16];
+  constexpr int kBytes = FEW && LowLds<RT>::kBytes > kChunks * 16 ? LowLds<RT>::kBytes : kChunks * 16;
+  __shared__ __align__(16) char lds[kWaves][kBytes];
   __shared__ f32x4 own_sums[kShared ? 1 : kSums];
   f32x4* sums = kShared ? reinterpret_cast<f32x4*>(lds[0]) : own_sums;
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -383,9 +421,16 @@ __global__ void __launch_bounds__(kThreads, RT == 1 || (RT == 2 && !LEAD) ? 3 : 
     bf16x8 low[kSteps];
     if (with) {   // (the wavefronts of a workgroup have the same rows)
       if (LEAD && group > 0) __syncthreads();
+      const int items = here * RT * 4, shares = FEW ? 1 : max(1, min(kShares, kThreads / items));
+      if constexpr (FEW) {
+        f32x4 part[RT];
+        low_sums<RT, RT == 1 ? 3 : 2>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave, kWaves, mine_lds, part);
+        leave_sums<RT>(part, mine_lds);
+        __syncthreads();
+        for (int i = threadIdx.x; i < items; i += kThreads) sums[i] = sum_of_waves<RT>(lds, i / (RT * 4), i % (RT * 4) * 4);
+      }
       // the slices' sums, slices shared out among threads and loaded in batches
-      const int items = here * RT * 4, shares = max(1, min(kShares, kThreads / items));
-      for (int i0 = 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
+      for (int i0 = FEW ? items : 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
         const int i = min(i0 + (int)threadIdx.x, items * shares - 1), share = i / items, item = i - share * items;
         f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
         const float* p = g.low + row_of(item / (RT * 4)) * (RT * 16) + item % (RT * 4) * 4;
@@ -520,41 +565,52 @@ __global__ void __launch_bounds__(kThreads, RT == 1 || (RT == 2 && !LEAD) ? 3 : 
 
 struct AdapterPlan {
   int tiles16;                   // RT
-  bool lead;                     // workgroups go by adapters
+  AdapterForm form;
   int splits, per_split, blocks, per_block;
 };
 
 AdapterPlan plan_of(const moe_adapter_shape& s) {
   AdapterPlan p;
   p.tiles16 = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : s.rank <= 64 ? 4 : 8;
-  p.lead = s.rows <= kLeadRows;
+  p.form = s.rows <= kFewRows && p.tiles16 <= 2 && (int64_t)s.rank * s.in_cols <= kFewValues ? kFewForm
+           : s.rows <= kLeadRows                                                               ? kLeadForm
+                                                                                               : kTileForm;
   const int64_t tiles = std::max<int64_t>(1, ceil_div(s.rows, kRows)), run = kStep * kWaves;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));
   p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
-  const int64_t stride = kCols * kWaves;
+  const int64_t stride = kCols * (p.form == kFewForm ? kFewWaves : kWaves);
   p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(2048, tiles)), stride) * stride);
   p.blocks = (int)ceil_div(s.out_cols, p.per_block);
   return p;
 }
 
-template <int RT, bool LEAD>
-hipError_t run_t(const AdapterArgs& g, int out_dtype, hipStream_t st) {
+template <int RT, int FORM>
+hipError_t out_t(const AdapterArgs& g, int out_dtype, dim3 grid, hipStream_t st) {
+  const dim3 threads(FORM == kFewForm ? 64 * kFewWaves : kThreads);
+  return out_dtype == MOE_DTYPE_F32 ? launch_kernel(adapters_out_kernel<RT, 3, float, FORM>, grid, threads, 0, st, g)
+                                    : launch_kernel(adapters_out_kernel<RT, 2, uint16_t, FORM>, grid, threads, 0, st, g);
+}
+
+template <int RT>
+hipError_t run_t(const AdapterArgs& g, AdapterForm form, int out_dtype, hipStream_t st) {
   // (the slices or columns of a tile are neighbours in the grid: workgroups at work together cover whole rows)
-  const unsigned tiles = (unsigned)(LEAD ? g.rows : ceil_div(g.rows, kRows));
-  const hipError_t err = launch_kernel(adapters_low_kernel<RT, LEAD>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g);
-  if (err != hipSuccess) return err;
+  const unsigned tiles = (unsigned)(form == kTileForm ? ceil_div(g.rows, kRows) : g.rows);
   const dim3 grid(tiles * g.blocks);
-  return out_dtype == MOE_DTYPE_F32
-             ? launch_kernel(adapters_out_kernel<RT, 3, float, LEAD>, grid, dim3(kThreads), 0, st, g)
-             : launch_kernel(adapters_out_kernel<RT, 2, uint16_t, LEAD>, grid, dim3(kThreads), 0, st, g);
+  if constexpr (RT <= 2)
+    if (form == kFewForm) return out_t<RT, kFewForm>(g, out_dtype, grid, st);
+  const hipError_t err =
+      form == kTileForm ? launch_kernel(adapters_low_kernel<RT, false>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g)
+                        : launch_kernel(adapters_low_kernel<RT, true>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g);
+  if (err != hipSuccess) return err;
+  return form == kTileForm ? out_t<RT, kTileForm>(g, out_dtype, grid, st) : out_t<RT, kLeadForm>(g, out_dtype, grid, st);
 }
 
 }  // namespace
 
 size_t adapters_workspace(const moe_adapter_shape& s) {
   const AdapterPlan p = plan_of(s);
-  return (size_t)p.splits * s.rows * p.tiles16 * 16 * 4;
+  return p.form == kFewForm ? 0 : (size_t)p.splits * s.rows * p.tiles16 * 16 * 4;
 }
 
 hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int32_t* row_adapter, const void* a, const void* b,
@@ -583,10 +639,10 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       p.blocks,
                       p.per_block};
   switch (p.tiles16) {
-    case 1: return p.lead ? run_t<1, true>(g, s.out_dtype, st) : run_t<1, false>(g, s.out_dtype, st);
-    case 2: return p.lead ? run_t<2, true>(g, s.out_dtype, st) : run_t<2, false>(g, s.out_dtype, st);
-    case 4: return p.lead ? run_t<4, true>(g, s.out_dtype, st) : run_t<4, false>(g, s.out_dtype, st);
-    default: return p.lead ? run_t<8, true>(g, s.out_dtype, st) : run_t<8, false>(g, s.out_dtype, st);
+    case 1: return run_t<1>(g, p.form, s.out_dtype, st);
+    case 2: return run_t<2>(g, p.form, s.out_dtype, st);
+    case 4: return run_t<4>(g, p.form, s.out_dtype, st);
+    default: return run_t<8>(g, p.form, s.out_dtype, st);
   }
 }
 

@@ -1188,15 +1188,17 @@ moe_status moe_adapters(const moe_adapter_shape* shape, const void* x, const int
   moe_status rc = check_adapters(shape);
   if (rc != MOE_OK) return rc;
   if (shape->rows == 0) return MOE_OK;
-  if (!x || !row_adapter || !a || !b || !scale || !out || !workspace) return MOE_ERR_INVALID_ARG;
+  if (!x || !row_adapter || !a || !b || !scale || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x, a, b, base, out, workspace)) return MOE_ERR_INVALID_ARG;
   if (out == x || out == a || out == b || out == workspace) return MOE_ERR_INVALID_ARG;
   for (const void* p : {static_cast<const void*>(row_adapter), static_cast<const void*>(scale), static_cast<const void*>(ranks)})
-    if (out == p || workspace == p) return MOE_ERR_INVALID_ARG;
+    if (out == p || (workspace && workspace == p)) return MOE_ERR_INVALID_ARG;
   const int64_t base_ld = shape->base_ld ? shape->base_ld : shape->out_cols;
   const int64_t out_ld = shape->out_ld ? shape->out_ld : shape->out_cols;
   if (out == base && base_ld != out_ld) return MOE_ERR_INVALID_ARG;
-  if (workspace_bytes < adapters_workspace(*shape)) return MOE_ERR_WORKSPACE;
+  const size_t need = adapters_workspace(*shape);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  if (need > 0 && !workspace) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_adapters(*shape, x, row_adapter, a, b, scale, ranks, base, out, static_cast<float*>(workspace),
                                     stream));
 }
