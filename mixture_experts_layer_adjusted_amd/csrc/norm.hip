@@ -10,8 +10,8 @@
 // Squares, sums, y and the gradients are fp32.
 //
 // A row lies in the registers of one wavefront (up to 2048 values) or of one workgroup, eight neighbouring values a lane
-// and load, so that it is read once; which of the two goes by the row's length alone, so a row's results are the same bits
-// in every batch.  16 lanes hold a run of 128.  The weight's gradient: every thread sums its own columns over the
+// and load, so that it is read once.  The order of its sums goes by its length alone: a row's results are the same bits in
+// every batch.  16 lanes hold a run of 128.  The weight's gradient: every thread sums its own columns over the
 // workgroup's rows, the workgroups' sums are joined in a fixed order by a second kernel.
 // Bound by memory.
 #include "fp8_codec.h"
@@ -35,17 +35,19 @@ struct NormArgs {
   float eps;
 };
 
-// The sum of v over the row's lanes.  WAVE: the row's own wavefront.  Otherwise the workgroup: the wavefronts' sums
-// meet in LDS (`at` alternates between two places, so that one barrier a row is enough).
-template <bool WAVE>
-__device__ __forceinline__ float row_sum(float v, float (&place)[2][16], int at) {
-  v = sum_of<64>(v);
+// The sum of the lanes' V parts over the row.  WAVE: the row's own wavefront.  Otherwise the workgroup: the wavefronts'
+// sums meet in LDS (`at` alternates between two places, so that one barrier a row is enough).  A wavefront with four parts a
+// lane adds them up as two wavefronts with two parts each would: the same bits.
+template <bool WAVE, int V>
+__device__ __forceinline__ float row_sum(const float (&part)[V], float (&place)[2][16], int at) {
+  if constexpr (WAVE && V == 4) return sum_of<64>(part[0] + part[2]) + sum_of<64>(part[1] + part[3]);
+  const float v = sum_of<64>(sum_run<V>(part));
   if constexpr (WAVE) return v;
   const int waves = blockDim.x >> 6;
   if ((threadIdx.x & 63) == 0) place[at][threadIdx.x >> 6] = v;
   __syncthreads();
-  float s = 0.0f;
-  for (int w = 0; w < waves; ++w) s += place[at][w];
+  float s = place[at][0];
+  for (int w = 1; w < waves; ++w) s += place[at][w];
   return s;
 }
 
@@ -118,7 +120,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormA
     for (int i = 0; i < 8; ++i) sq[i] = h[j][i] * h[j][i];
     part[j] = (j * lanes + lane) * 8 < a.cols ? sum_run<8>(sq) : 0.0f;
   }
-  const float rstd = 1.0f / sqrtf(row_sum<WAVE>(sum_run<V>(part), place, 0) / (float)a.cols + a.eps);
+  const float rstd = 1.0f / sqrtf(row_sum<WAVE>(part, place, 0) / (float)a.cols + a.eps);
   if (a.rstd && lane == 0) a.rstd[r] = rstd;
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
       part[j] = (j * lanes + lane) * 8 < a.cols ? sum_run<8>(p) : 0.0f;
     }
     if (kAhead && r + step < a.rows) load(r + step);
-    const float mean = row_sum<WAVE>(sum_run<V>(part), place, at) / n;
+    const float mean = row_sum<WAVE>(part, place, at) / n;
     T* d_x = static_cast<T*>(a.d_x) + r * a.x_ld;
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -323,6 +325,13 @@ int64_t norm_blocks(const NormLanes& l, int64_t rows) {
   return std::min<int64_t>(ceil_div(rows, l.per), kParts);
 }
 
+// Rows of 1025 to 2048 values, up to 4096 of them: two wavefronts a row, more loads at once (in a graph, us, two
+// wavefronts against one: 1 x 2048 2.8, 3.5; 77 x 2048 3.1, 4.0; 4096 x 2048 11.0, 11.7; 65536 x 2048 166, 163)
+NormLanes forward_lanes_of(int cols, int64_t rows) {
+  const NormLanes l = lanes_of(cols);
+  return l.most == 64 && l.vectors == 4 && rows <= 4096 ? NormLanes{2, 512, 128, 1} : l;
+}
+
 template <typename T>
 hipError_t norm_forward_t(const NormLanes& l, const NormArgs& a, hipStream_t st) {
   const unsigned grid = (unsigned)ceil_div(a.rows, l.per);
@@ -349,7 +358,7 @@ hipError_t launch_norm_forward(const moe_norm_shape& s, const void* x, const voi
                                void* y, uint8_t* codes, float* scales, float* rstd, hipStream_t st) {
   const NormArgs a{x,    residual, weight, sum, y, codes, scales, rstd, s.rows, s.x_ld ? s.x_ld : s.cols,
                    s.y_ld ? s.y_ld : s.cols, s.cols, s.eps};
-  const NormLanes l = lanes_of(s.cols);
+  const NormLanes l = forward_lanes_of(s.cols, s.rows);
   return s.dtype == MOE_DTYPE_F32 ? norm_forward_t<float>(l, a, st) : norm_forward_t<uint16_t>(l, a, st);
 }
 

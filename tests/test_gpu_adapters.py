@@ -75,6 +75,18 @@ def test_against_float64(rows, d_in, d_out, n, r, ranks, out, order):
     check(p, run(p, base=None), base=False)
 
 
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d_in,d_out,n,r,ranks", [
+    (16, 2048, 640, 6, 32, True), (16, 2056, 136, 2, 32, False), (17, 264, 520, 2, 16, True), (100, 1032, 328, 2, 16, False),
+    (128, 520, 256, 40, 32, True), (128, 264, 72, 1, 64, False), (129, 264, 72, 1, 64, False), (140, 328, 136, 5, 32, True),
+    (200, 456, 72, 3, 64, True), (257, 72, 8, 60, 8, False), (300, 8, 328, 3, 128, True)])
+def test_rows_by_adapter_and_by_tile(rows, d_in, d_out, n, r, ranks, out):
+    """Few rows and little of A (one kernel), up to 128 rows (workgroups by adapter, more than 16 rows of one), tiles."""
+    for order in ("mixed", "prompts"):
+        p = problem(rows, d_in, d_out, n, r, rows + d_out, out, order, ranks)
+        check(p, run(p))
+
+
 def test_large_and_long():
     p = problem(5000, 512, 640, 6, 16, 1, order="prompts")
     out = run(p)

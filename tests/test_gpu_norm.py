@@ -154,6 +154,17 @@ def test_a_rows_results_are_its_own(cols):
         assert torch.equal(e, d[at:at + 1])
 
 
+@pytest.mark.parametrize("cols,stream", [(2048, "bf16"), (1032, "f32"), (1408, "bf16")])
+def test_many_rows_and_few_have_the_same_bits(cols, stream):
+    """Rows of 1025 to 2048 values lie on one wavefront or on two."""
+    x, r, w, _, _ = inputs(4097, cols, stream, 12)
+    codes = cols % 128 == 0
+    full = forward(x, r, w, stream, codes=codes)
+    part = forward(x[1000:1300].contiguous(), r[1000:1300].contiguous(), w, stream, codes=codes)
+    for k, v in part.items():
+        assert v is None or torch.equal(v.view(torch.uint8), full[k][1000:1300].contiguous().view(torch.uint8)), k
+
+
 def test_rows_that_are_zero_or_not_finite():
     x, _, w, d_y, _ = inputs(8, 1024, "bf16", 8)
     x[1] = 0
