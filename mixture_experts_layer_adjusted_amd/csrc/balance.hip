@@ -41,6 +41,7 @@ struct BalanceArgs {
 __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int64_t t) {
   if (!a.start) return 0;
   const int lane = threadIdx.x & 63;
+  if (a.S < 64) return __popcll(__ballot(a.start[min(lane, a.S)] <= t && lane <= a.S)) - 1;
   int lo = 0, hi = a.S + 1;   // the number is in [lo, hi]
   while (hi > lo) {
     const int step = (hi - lo + 63) / 64, at = lo + lane * step;
@@ -58,11 +59,9 @@ __device__ __forceinline__ int sequence_of(const BalanceArgs& a, int64_t t) {
   return lo - 1;
 }
 
-// the end of the piece of sequence s that begins at t, inside [t + 1, end]
-__device__ __forceinline__ int64_t piece_end(const BalanceArgs& a, int s, int64_t t, int64_t end) {
-  if (!a.start || s >= a.S) return end;
-  const int64_t e = a.start[s + 1];
-  return e <= t ? t + 1 : e < end ? e : end;
+// where sequence s (as sequence_of has it) ends
+__device__ __forceinline__ int64_t sequence_end(const BalanceArgs& a, int s) {
+  return !a.start || s >= a.S ? a.T : a.start[s + 1];
 }
 
 // The token's p, and for the sigmoid 1 - s; C runs of four a lane.  Where no logit of the token is positive the sigmoid's
@@ -236,6 +235,7 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
   load(begin);
   for (int i = threadIdx.x; i < a.N + 1; i += kPartThreads) counts[i] = 0;
   int s = sequence_of(a, begin);
+  int64_t s_end = sequence_end(a, s);
   __syncthreads();
   for (int64_t block = begin; block < end; block += kBlock) {
     const int64_t t = block + wave * kTokens + slot, stop = block + kBlock < end ? block + kBlock : end;
@@ -252,8 +252,11 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
     const bool real = max_of<L>((uint32_t)some) != 0;
     shares<L, C, SOFTMAX>(l, rest);
     for (int64_t t0 = block; t0 < stop;) {
-      if (t0 > begin) s = sequence_of(a, t0);
-      const int64_t t1 = s < 0 ? (a.start[0] < stop ? a.start[0] : stop) : piece_end(a, s, t0, stop);
+      if (t0 >= s_end && t0 > begin) {
+        s = sequence_of(a, t0);
+        s_end = sequence_end(a, s);
+      }
+      const int64_t t1 = s_end <= t0 ? t0 + 1 : s_end < stop ? s_end : stop;
       const bool inside = s >= 0 && s < a.S;
       if (seq >= 0 && s != seq) {
         __syncthreads();   // (the counts of the piece before)
