@@ -517,7 +517,7 @@ typedef struct moe_balance_config {
   int32_t top_k;         /* K: 1 to min(N, 32); tokens * top_k < 2^31 */
   int32_t logits_dtype;  /* MOE_DTYPE_F32 or MOE_DTYPE_BF16 (logits and their gradient) */
   int32_t score;         /* moe_score */
-  int32_t n_seqs;        /* S >= 1 */
+  int32_t n_seqs;        /* S: 1 to 2^24 */
   float alpha;           /* finite */
   int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
 } moe_balance_config;
@@ -536,7 +536,7 @@ moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* 
  *   prob_sum    [S, N]  fp32 out, or NULL: sum_t p_{t,i}.  With counts, seq_tokens and prob_sum added up
  *               over the ranks of a job, the loss of the whole batch is the formula above, and
  *               moe_balance_backward takes the sums
- * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512, top_k > 32 or tokens * top_k >= 2^31:
+ * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512, top_k > 32, n_seqs > 2^24 or tokens * top_k >= 2^31:
  * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE. */
 moe_status moe_balance_loss(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
                             const int32_t* seq_start, float* loss, int32_t* counts, int32_t* seq_tokens, float* prob_sum,
@@ -561,7 +561,7 @@ moe_status moe_balance_backward(const moe_balance_config* config, const void* lo
  * the contraction over A_e's first ranks[e] rows.  Rows may come in any order; those of one adapter side by side
  * (prompts) cost least.  For serving: there is no gradient. */
 typedef struct moe_adapter_shape {
-  int32_t rows;               /* T >= 0 */
+  int32_t rows;               /* T: 0 to 2^27 - 1 */
   int32_t in_cols, out_cols;  /* 8 to 2^20, multiples of 8 */
   int32_t n_adapters;         /* n >= 1 */
   int32_t rank;               /* r: rows of each A, columns of each B; 8 to 128, a multiple of 8 */

@@ -395,14 +395,14 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
 }
 
 __global__ void balance_zero_kernel(BalanceOut o, int S, int N) {
-  const int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (at < S) {
-    o.loss[at] = 0.0f;
-    o.tokens[at] = 0;
+  for (int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; at < (int64_t)S * N; at += (int64_t)gridDim.x * blockDim.x) {
+    if (at < S) {
+      o.loss[at] = 0.0f;
+      o.tokens[at] = 0;
+    }
+    o.counts[at] = 0;
+    if (o.prob_sum) o.prob_sum[at] = 0.0f;
   }
-  if (at >= (int64_t)S * N) return;
-  o.counts[at] = 0;
-  if (o.prob_sum) o.prob_sum[at] = 0.0f;
 }
 
 struct BalanceBwdArgs {
@@ -551,7 +551,7 @@ hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, 
   const BalanceArgs a = args_of(c, logits, idx, start);
   const BalanceOut o{loss, counts, tokens, prob_sum};
   if (c.tokens == 0)
-    return launch_kernel(balance_zero_kernel, dim3((unsigned)ceil_div((int64_t)c.n_seqs * c.n_routed, 256)), dim3(256), 0, st,
+    return launch_kernel(balance_zero_kernel, dim3((unsigned)std::min<int64_t>(ceil_div((int64_t)c.n_seqs * c.n_routed, 256), 1 << 16)), dim3(256), 0, st,
                          o, c.n_seqs, c.n_routed);
   const int chunk = chunk_of(c);
   const bool f32 = c.logits_dtype == MOE_DTYPE_F32;

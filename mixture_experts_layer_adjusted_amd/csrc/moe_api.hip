@@ -1121,6 +1121,7 @@ static moe_status check_balance(const moe_balance_config* c) {
   if (c->logits_ld != 0 && c->logits_ld < c->n_routed) return MOE_ERR_INVALID_ARG;
   if (c->n_routed > kMaxRouted || c->top_k > kMaxTopK) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)c->tokens * c->top_k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (c->n_seqs > (1 << 24)) return MOE_ERR_UNSUPPORTED;   // a workgroup each
   return MOE_OK;
 }
 
@@ -1171,6 +1172,7 @@ static moe_status check_adapters(const moe_adapter_shape* s) {
   if (s->in_cols > (1 << 20) || s->out_cols > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   if (s->x_ld % 8 != 0 || s->base_ld % 8 != 0 || s->out_ld % 8 != 0) return MOE_ERR_UNSUPPORTED;
   if (s->x_ld >= (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;   // 32-bit offsets inside 128 rows
+  if (s->rows >= (1 << 27)) return MOE_ERR_UNSUPPORTED;            // a workgroup for every 16 rows
   return MOE_OK;
 }
 

@@ -23,6 +23,7 @@ namespace moe {
 namespace {
 
 constexpr int kParts = 256;   // workgroups of a backward pass at most, one a CU
+constexpr int kMostBlocks = 1 << 21;   // of a forward pass along x, the others along y: fewer than 2^32 threads in each
 
 struct NormArgs {
   const void *x, *residual;
@@ -80,14 +81,15 @@ __device__ __forceinline__ float run_amax(const float (&v)[8]) {
   return fmaxf(m, __uint_as_float(turned<0x121>(__float_as_uint(m))));
 }
 
-// V vectors of eight a lane; MOST: threads of a workgroup at most, 64: a row to a wavefront.  One row each: rows that a
-// workgroup goes through with the next one's values on their way measured 5.1 TB/s against 5.6 (16384 x 7168).
+// V vectors of eight a lane; MOST: threads of a workgroup at most, 64: a row to a wavefront.  One row each:
+// rows that a workgroup goes through with the next one's values on their way measured 5.1 TB/s against 5.6 (16384 x 7168).
 template <typename T, int V, int MOST>
 __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormArgs a) {
   constexpr bool WAVE = MOST == 64;
   __shared__ float place[2][16];
   const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
-  const int64_t r = WAVE ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x;
+  const int64_t block = (int64_t)blockIdx.y * gridDim.x + blockIdx.x;
+  const int64_t r = WAVE ? block * 4 + (threadIdx.x >> 6) : block;
   if (r >= a.rows) return;
   Raw8<T> x[V], res[V];
   Raw8<float> w[V];
@@ -334,9 +336,10 @@ NormLanes forward_lanes_of(int cols, int64_t rows) {
 
 template <typename T>
 hipError_t norm_forward_t(const NormLanes& l, const NormArgs& a, hipStream_t st) {
-  const unsigned grid = (unsigned)ceil_div(a.rows, l.per);
+  const int64_t blocks = ceil_div(a.rows, l.per);
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, kMostBlocks), (unsigned)ceil_div(blocks, kMostBlocks));
   return with_lanes(l, [&](auto v, auto most) {
-    return launch_kernel(norm_fwd_kernel<T, decltype(v)::value, decltype(most)::value>, dim3(grid), dim3(l.threads), 0, st, a);
+    return launch_kernel(norm_fwd_kernel<T, decltype(v)::value, decltype(most)::value>, grid, dim3(l.threads), 0, st, a);
   });
 }
 

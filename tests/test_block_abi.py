@@ -90,7 +90,7 @@ def balance(**kw):
     (dict(logits_dtype=2), INVALID), (dict(score=2), INVALID), (dict(n_seqs=0), INVALID), (dict(logits_ld=63), INVALID),
     (dict(alpha=float("inf")), INVALID), (dict(alpha=float("nan")), INVALID), (dict(n_routed=513), UNSUPPORTED),
     (dict(top_k=33), UNSUPPORTED), (dict(tokens=1 << 30), UNSUPPORTED), (dict(), OK), (dict(logits_ld=65, alpha=-1.0), OK),
-    (dict(tokens=0), OK),
+    (dict(tokens=0), OK), (dict(n_seqs=(1 << 24) + 1), UNSUPPORTED), (dict(n_seqs=1 << 24), OK),
 ])
 def test_balance_limits(kw, status):
     c, n = balance(**kw), ctypes.c_size_t(0)
@@ -131,7 +131,7 @@ def adapters(**kw):
     (dict(out_ld=504), INVALID), (dict(in_cols=252), UNSUPPORTED), (dict(out_cols=500), UNSUPPORTED),
     (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(in_cols=(1 << 20) + 8), UNSUPPORTED),
     (dict(out_cols=(1 << 20) + 8), UNSUPPORTED), (dict(x_ld=260), UNSUPPORTED), (dict(base_ld=516), UNSUPPORTED),
-    (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
+    (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(rows=1 << 27), UNSUPPORTED), (dict(rows=(1 << 27) - 1), OK), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
 ])
 def test_adapter_limits(kw, status):
     s, n = adapters(**kw), ctypes.c_size_t(0)

@@ -223,6 +223,22 @@ def test_no_tokens_and_no_sum():
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_more_sequences_than_tokens():
+    """Most of them empty; and so many that the counts take several rounds to clear."""
+    logits, idx = problem(90, 12, 2, 14)
+    S = 5000
+    starts = torch.sort(torch.randint(0, 91, (S + 1,), device="cuda")).values.to(torch.int32)
+    starts[0], starts[-1] = 0, 90
+    out, _ = check(logits, idx, starts, True)
+    assert int(out[2].sum()) == 90
+    S, N = 70000, 512
+    cfg = moe.make_balance_config(0, N, 4, 0, 1, S, 1.0)
+    res = [torch.full((S,), 5.0, device="cuda"), torch.full((S, N), 5, dtype=torch.int32, device="cuda"),
+           torch.full((S,), 5, dtype=torch.int32, device="cuda"), torch.full((S, N), 5.0, device="cuda")]
+    moe.moe_balance_loss(cfg, None, None, torch.zeros(S + 1, dtype=torch.int32, device="cuda"), *res, None)
+    assert all((o == 0).all() for o in res)
+
+
 def test_large_batch_another_stream_and_a_graph():
     """More tokens than places of 64: longer chunks; the same bits again."""
     T, N, K = 150000, 64, 6

@@ -270,3 +270,16 @@ def test_offsets_past_32_bits(rows, cols):
     # the rows repeat: d_weight is near so many times that of the block
     size = (d_y.float() * block.float()).abs().sum(0) * (rows / 64)
     assert ((d_w - one * (rows / 64)).abs() <= 2.0 ** -8 * size).all()
+
+
+@pytest.mark.parametrize("cols", [8, 2056])
+def test_more_rows_than_a_launch_has_workgroups_for(cols):
+    """2^32 threads and more at a row a wavefront; 2^21 workgroups and more at a row each."""
+    rows = (1 << 26) + 7 if cols == 8 else (1 << 21) + 5
+    block, _, w, _, _ = inputs(512, cols, "bf16", 13)
+    x = block.repeat(rows // 512 + 1, 1)[:rows]
+    out = forward(x, None, w, "bf16", rstd=False)["y"]
+    want = forward(block, None, w, "bf16", rstd=False)["y"]
+    whole = rows // 512 * 512
+    assert torch.equal(out[:whole].view(-1, 512, cols), want.expand(rows // 512, 512, cols))
+    assert torch.equal(out[whole:], want[:rows - whole])
