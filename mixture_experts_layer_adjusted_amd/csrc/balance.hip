@@ -11,7 +11,12 @@
 // Sequences lie one behind the other and may begin anywhere.  16 lanes hold a token (32 above 128 experts, 64 above 256),
 // each one or two runs of four neighbouring experts.  A workgroup takes a chunk of tokens and writes its sums of p and its counts once for every sequence that it
 // meets: chunk c and sequence s have the place c + s, which no other pair has (from one pair to the next, at least one of
-// the two grows).  A second kernel adds up the places of each sequence, in order: no floating-point atomics.
+// the two grows).  A second kernel adds up the places of each sequence, in order: no floating-point atomics.  (A sum over
+// several workgroups a sequence, the last by a ticket, cost 2 us of device-wide atomics and gained less.)
+//
+// Bound by latency and instructions: 32768 tokens of 64 experts, softmax: 6.0 us (8.4 MB), the second kernel 5.8, the gradient
+// 6.3 (16.8 MB); 16384 tokens of 256 experts, sigmoid: 10.0 (16.8 MB; 330 vector instructions for two tokens), 6.5, 9.5 (33.6
+// MB).  Loads of one value each where four lie side by side cost the gradient 14.0 in place of 9.4.
 #include "lanes.h"
 #include "moe_internal.h"
 
@@ -21,7 +26,9 @@ namespace {
 constexpr int kPartWaves = 16, kPartThreads = 64 * kPartWaves;  // of a workgroup of the forward pass
 constexpr int kWaves = 4, kThreads = 64 * kWaves;             // of a workgroup of the backward pass
 constexpr int kJoinThreads = 1024;                            // of the second kernel
-constexpr int kPlaces = 256;                                  // places for the whole batch, or so
+// Places for the whole batch, or so: T=32768, 64 experts, 512 of them 8.8 + 5.7 us, 256 6.2 + 5.8; T=16384, 256 experts 12.7 +
+// 5.8, 10.0 + 5.9.
+constexpr int kPlaces = 256;
 
 // the places' layout: sums of p (fp32), counts, the number of tokens, columns rounded up to fours
 __host__ __device__ inline int place_cols(int n) { return (n + 3) & ~3; }

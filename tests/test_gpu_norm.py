@@ -70,8 +70,8 @@ def check_codes(out, y_ref):
 
 
 def depth(rows):
-    """Additions one after another: the rows of one of 256 workgroups, its wavefronts, the workgroups."""
-    return -(-rows // 256) + 3 + 4 + 16
+    """Additions one after another: the rows of one of 128 or more workgroups, its wavefronts, the workgroups."""
+    return -(-rows // 128) + 3 + 4 + 16
 
 
 CASES = [(1, 8, "bf16"), (1, 7168, "bf16"), (3, 128, "f32"), (5, 520, "bf16"), (77, 2048, "bf16"), (9, 2056, "f32"),
