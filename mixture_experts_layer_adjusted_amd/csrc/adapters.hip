@@ -11,8 +11,7 @@
 // 16 neighbouring rows form a tile.  The rows of a tile may have different adapters: for each that occurs the whole tile is
 // multiplied and the rows that have it keep the result, so every adapter in use is read once for a tile and rows need
 // no sorting.  Rows of other adapters are computed and dropped, never added as zeros: an infinity or NaN stays in its row.
-// Up to 128 rows, workgroups go by adapters instead and read each once (64 rows of 32 adapters, rank 64: 18.5 us against 90
-// by tiles, whose wavefronts take one adapter after the other).
+// Up to 128 rows of many adapters, workgroups go by adapters instead.
 //
 // Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6 for the
 // second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
@@ -31,7 +30,12 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves, kWavesOfTile = kWaves;
 constexpr int kRows = 16;        // rows of a tile
 constexpr int kStep = 64;        // values of a wavefront's step along the first product's contraction
 constexpr int kCols = 64;        // output columns of a wavefront at a time
-constexpr int kLeadRows = 128;   // rows at most where workgroups go by adapters
+// Workgroups go by adapters up to so many rows, and rows for each adapter there is: they read an adapter once, a tile of
+// rows reads each of its adapters one after the other; but an adapter of many rows is one workgroup's alone.  In a graph,
+// us, by adapters against by tiles, rows of all adapters mixed: 64 rows, 32 adapters, 16 x 7168 -> 4096: 10.8, 19.8; rank
+// 64: 17.8, 31.0; 128 rows 14.3, 19.1; rank 64 23.4, 31.7; 64 rows, 4 adapters, 16 x 2048 -> 7168: 10.4, 9.0.
+// Adapters side by side: 64 rows, 32 adapters 10.8, 15.7; 128 rows 14.1, 13.4; 64 rows, 4 adapters 14.5, 8.0.
+constexpr int kLeadRows = 128, kLeadShare = 4;
 // One launch in place of two up to so many rows and values of an adapter's A, which every workgroup then reads whole.
 // In a graph, us, one kernel against two: 1 row, 16 x 2048 -> 7168: 5.4, 7.1; 16 rows, 32 x 2048 -> 4096: 7.5, 7.7;
 // 1 row, 16 x 7168 -> 4096: 8.2, 7.1; 32 rows, 32 x 2048 -> 4096: 8.5, 8.4.
@@ -579,7 +583,7 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
   AdapterPlan p;
   p.tiles16 = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : s.rank <= 64 ? 4 : 8;
   p.form = s.rows <= kFewRows && p.tiles16 <= 2 && (int64_t)s.rank * s.in_cols <= kFewValues ? kFewForm
-           : s.rows <= kLeadRows                                                               ? kLeadForm
+           : s.rows <= kLeadRows && s.rows <= kLeadShare * (int64_t)s.n_adapters               ? kLeadForm
                                                                                                : kTileForm;
   const int64_t tiles = std::max<int64_t>(1, ceil_div(s.rows, kRows)), run = kStep * kWaves;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));

@@ -87,6 +87,15 @@ def test_rows_by_adapter_and_by_tile(rows, d_in, d_out, n, r, ranks, out):
         check(p, run(p))
 
 
+@pytest.mark.parametrize("rows,r,out", [(128, 16, torch.bfloat16), (100, 64, torch.float32), (97, 128, torch.bfloat16), (66, 32, torch.float32)])
+def test_many_rows_of_one_adapter_among_many(rows, r, out):
+    """Workgroups by adapter: one of them with more rows than a tile, and rows without an adapter likewise."""
+    p = problem(rows, 1096, 264, 40, r, rows + r, out)
+    pick = torch.rand(rows, device="cuda")
+    p["which"] = torch.where(pick < 0.4, 7, torch.where(pick < 0.7, -1, p["which"])).to(torch.int32)
+    check(p, run(p))
+
+
 def test_large_and_long():
     p = problem(5000, 512, 640, 6, 16, 1, order="prompts")
     out = run(p)
