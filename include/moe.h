@@ -537,7 +537,8 @@ moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* 
  *               over the ranks of a job, the loss of the whole batch is the formula above, and
  *               moe_balance_backward takes the sums
  * Errors: MOE_ERR_INVALID_ARG outside the limits (n_routed > 512, top_k > 32, n_seqs > 2^24 or tokens * top_k >= 2^31:
- * MOE_ERR_UNSUPPORTED) or for a null pointer; MOE_ERR_WORKSPACE. */
+ * MOE_ERR_UNSUPPORTED), for a null pointer or an output or the workspace in place of another buffer;
+ * MOE_ERR_WORKSPACE. */
 moe_status moe_balance_loss(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
                             const int32_t* seq_start, float* loss, int32_t* counts, int32_t* seq_tokens, float* prob_sum,
                             void* workspace, size_t workspace_bytes, hipStream_t stream);
@@ -547,7 +548,7 @@ moe_status moe_balance_loss(const moe_balance_config* config, const void* logits
  *   d_loss    [S]    fp32 dL/dloss
  *   d_logits  [T, N] out, rows d_logits_ld apart (0: n_routed): fp32 or bf16 (rounded once).  accumulate
  *             zero: every element written; non-zero: added to what is there (moe_gate_backward's), and rows without a
- *             gradient are left as they are.  May not alias logits
+ *             gradient are left as they are.  In place of no input
  * Errors as moe_balance_loss. */
 moe_status moe_balance_backward(const moe_balance_config* config, const void* logits, const int32_t* topk_idx,
                                 const int32_t* seq_start, const int32_t* counts, const int32_t* seq_tokens,

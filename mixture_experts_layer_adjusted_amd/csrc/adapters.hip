@@ -13,8 +13,8 @@
 // no sorting.  Rows of other adapters are computed and dropped, never added as zeros: an infinity or NaN stays in its row.
 // Up to 128 rows of many adapters, workgroups go by adapters instead.
 //
-// Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6 for the
-// second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
+// Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6
+// for the second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
 // wants them took 37 + 37 us: the address unit takes a lane at a time there (57 accesses a load in place of 16).
 #include "moe_internal.h"
 #include "rows.h"
@@ -59,7 +59,6 @@ struct AdapterArgs {
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ bf16x8 vector_at(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 __device__ __forceinline__ bf16x8 no_values() { return __builtin_bit_cast(bf16x8, make_uint4(0u, 0u, 0u, 0u)); }
 
 // the adapter of row t, -1 for none
@@ -301,7 +300,8 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
     // (32-bit offsets from the first row of the tile, or of all)
     const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
     f32x4 kept[RT];
-    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1, !LEAD && RT <= 2>(g, g.x + (LEAD ? 0 : tile * kRows * g.x_ld), at, mine, begin, end, wave, kWaves, lds[wave], kept);
+    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1, !LEAD && RT <= 2>(g, g.x + (LEAD ? 0 : tile * kRows * g.x_ld), at, mine,
+                                                                 begin, end, wave, kWaves, lds[wave], kept);
     leave_sums<RT>(kept, lds[wave]);
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
@@ -357,15 +357,17 @@ struct RawFour<float> {
 
 // The second product: tokens are the matrix instruction's rows, output columns its columns, in an order that leaves a lane
 // four neighbouring columns of four tokens (lane n of tile j: column 4 n + j of the wavefront's 64), so that base and out
-// go in whole lines.  B, whose rows for neighbouring columns lie side by side, is loaded as it lies
-// and read from LDS, its 16-byte chunks turned so that the lanes of a read meet on no bank.
-// PARTS bf16 parts of the low-rank values.  RT == 1: one run of 32 holds two parts.
+// go in whole lines.  B, whose rows for neighbouring columns lie side by side, is loaded as it lies and read from LDS, its
+// 16-byte chunks turned so that the lanes of a read meet on no bank.  PARTS bf16 parts of the low-rank values (RT == 1: one run
+// of 32 holds two).
 // FORM: tiles of neighbouring rows, the rows of an adapter, or those with the first product in the same kernel (each
 // workgroup computes it whole, for its columns: for few rows and little of A that is less than a launch more).
 enum AdapterForm { kTileForm, kLeadForm, kFewForm };
 constexpr int kFewWaves = 8;
+// wavefronts a SIMD that the registers have to leave room for: three where the kernel would take a little more than that allows
+constexpr int out_waves(int rt, int form) { return form != kFewForm && (rt == 1 || (rt == 2 && form == kTileForm)) ? 3 : 1; }
 template <int RT, int PARTS, typename T, int FORM>
-__global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, FORM != kFewForm && (RT == 1 || (RT == 2 && FORM == kTileForm)) ? 3 : 1)
+__global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, out_waves(RT, FORM))
     adapters_out_kernel(AdapterArgs g) {
   constexpr bool LEAD = FORM != kTileForm, FEW = FORM == kFewForm;
   constexpr int kWaves = FEW ? kFewWaves : kWavesOfTile, kThreads = 64 * kWaves;
@@ -399,7 +401,8 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
     rows = lead_rows(g, (int)tile, leader);
   }
   for (int group = 0; group < rows.count; group += kRows) {
-    const int here = LEAD ? min(kRows, rows.count - group) : (int)min((int64_t)kRows, g.rows - tile * kRows);   // rows of the tile
+    // rows of the tile
+    const int here = LEAD ? min(kRows, rows.count - group) : (int)min((int64_t)kRows, g.rows - tile * kRows);
     auto row_of = [&](int i) -> int64_t {   // (rows the tile does not have: its last one)
       if constexpr (LEAD) return rows.at(group + min(i, here - 1));
       else return tile * kRows + min(i, here - 1);
@@ -441,7 +444,8 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
       const int items = here * RT * 4, shares = FEW ? 1 : max(1, min(kShares, kThreads / items));
       if constexpr (FEW) {
         f32x4 part[RT];
-        low_sums<RT, RT == 1 ? 3 : 2, false>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave, kWaves, mine_lds, part);
+        low_sums<RT, RT == 1 ? 3 : 2, false>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave,
+                                             kWaves, mine_lds, part);
         leave_sums<RT>(part, mine_lds);
         __syncthreads();
         for (int i = threadIdx.x; i < items; i += kThreads) sums[i] = sum_of_waves<RT>(lds, i / (RT * 4), i % (RT * 4) * 4);

@@ -9,10 +9,11 @@
 //   softmax  dl_i = p_i (c_i - D);   sigmoid  dl_i = p_i (1 - s_i) (c_i - D).
 //
 // Sequences lie one behind the other and may begin anywhere.  16 lanes hold a token (32 above 128 experts, 64 above 256),
-// each one or two runs of four neighbouring experts.  A workgroup takes a chunk of tokens and writes its sums of p and its counts once for every sequence that it
-// meets: chunk c and sequence s have the place c + s, which no other pair has (from one pair to the next, at least one of
-// the two grows).  A second kernel adds up the places of each sequence, in order: no floating-point atomics.  (A sum over
-// several workgroups a sequence, the last by a ticket, cost 2 us of device-wide atomics and gained less.)
+// each one or two runs of four neighbouring experts.  A workgroup takes a chunk of tokens and writes its sums of p and its
+// counts once for every sequence that it meets: chunk c and sequence s have the place c + s, which no other pair has (from
+// one pair to the next, at least one of the two grows).  A second kernel adds up the places of each sequence, in order: no
+// floating-point atomics.  (A sum over several workgroups a sequence, the last by a ticket, cost 2 us of device-wide
+// atomics and gained less.)
 //
 // Bound by latency and instructions: 32768 tokens of 64 experts, softmax: 6.0 us (8.4 MB), the second kernel 5.8, the gradient
 // 6.3 (16.8 MB); 16384 tokens of 256 experts, sigmoid: 10.0 (16.8 MB; 330 vector instructions for two tokens), 6.5, 9.5 (33.6
@@ -402,7 +403,8 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
 }
 
 __global__ void balance_zero_kernel(BalanceOut o, int S, int N) {
-  for (int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; at < (int64_t)S * N; at += (int64_t)gridDim.x * blockDim.x) {
+  const int64_t step = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t at = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; at < (int64_t)S * N; at += step) {
     if (at < S) {
       o.loss[at] = 0.0f;
       o.tokens[at] = 0;
@@ -557,9 +559,10 @@ hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, 
                                hipStream_t st) {
   const BalanceArgs a = args_of(c, logits, idx, start);
   const BalanceOut o{loss, counts, tokens, prob_sum};
-  if (c.tokens == 0)
-    return launch_kernel(balance_zero_kernel, dim3((unsigned)std::min<int64_t>(ceil_div((int64_t)c.n_seqs * c.n_routed, 256), 1 << 16)), dim3(256), 0, st,
-                         o, c.n_seqs, c.n_routed);
+  if (c.tokens == 0) {
+    const int64_t blocks = std::min<int64_t>(ceil_div((int64_t)c.n_seqs * c.n_routed, 256), 1 << 16);
+    return launch_kernel(balance_zero_kernel, dim3((unsigned)blocks), dim3(256), 0, st, o, c.n_seqs, c.n_routed);
+  }
   const int chunk = chunk_of(c);
   const bool f32 = c.logits_dtype == MOE_DTYPE_F32;
   hipError_t err;

@@ -1143,6 +1143,14 @@ moe_status moe_balance_loss(const moe_balance_config* config, const void* logits
   const size_t need = balance_workspace(*config);
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   if (need > 0 && (!workspace || !aligned16(workspace))) return MOE_ERR_INVALID_ARG;
+  const void* in[] = {logits, topk_idx, seq_start};
+  const void* out[] = {loss, counts, seq_tokens, prob_sum, need > 0 ? workspace : nullptr};
+  for (int i = 0; i < 5; ++i) {
+    for (const void* p : in)
+      if (out[i] && out[i] == p) return MOE_ERR_INVALID_ARG;
+    for (int j = 0; j < i; ++j)
+      if (out[i] && out[i] == out[j]) return MOE_ERR_INVALID_ARG;
+  }
   return hip_status(launch_balance_loss(*config, logits, topk_idx, seq_start, loss, counts, seq_tokens, prob_sum,
                                         static_cast<float*>(workspace), stream));
 }
@@ -1156,8 +1164,10 @@ moe_status moe_balance_backward(const moe_balance_config* config, const void* lo
   if (d_logits_ld != 0 && d_logits_ld < config->n_routed) return MOE_ERR_INVALID_ARG;
   if (!seq_start && config->n_seqs != 1) return MOE_ERR_INVALID_ARG;
   if (config->tokens == 0) return MOE_OK;
-  if (!logits || !topk_idx || !counts || !seq_tokens || !d_loss || !d_logits || d_logits == logits)
-    return MOE_ERR_INVALID_ARG;
+  if (!logits || !topk_idx || !counts || !seq_tokens || !d_loss || !d_logits) return MOE_ERR_INVALID_ARG;
+  const void* in[] = {logits, topk_idx, seq_start, counts, seq_tokens, d_loss};
+  for (const void* p : in)
+    if (d_logits == p) return MOE_ERR_INVALID_ARG;
   return hip_status(launch_balance_backward(*config, logits, topk_idx, seq_start, counts, seq_tokens, d_loss, d_logits,
                                             d_logits_ld, accumulate != 0, stream));
 }
@@ -1193,7 +1203,8 @@ moe_status moe_adapters(const moe_adapter_shape* shape, const void* x, const int
   if (!x || !row_adapter || !a || !b || !scale || !out) return MOE_ERR_INVALID_ARG;
   if (!aligned16(x, a, b, base, out, workspace)) return MOE_ERR_INVALID_ARG;
   if (out == x || out == a || out == b || out == workspace) return MOE_ERR_INVALID_ARG;
-  for (const void* p : {static_cast<const void*>(row_adapter), static_cast<const void*>(scale), static_cast<const void*>(ranks)})
+  const void* small[] = {row_adapter, scale, ranks};
+  for (const void* p : small)
     if (out == p || (workspace && workspace == p)) return MOE_ERR_INVALID_ARG;
   const int64_t base_ld = shape->base_ld ? shape->base_ld : shape->out_cols;
   const int64_t out_ld = shape->out_ld ? shape->out_ld : shape->out_cols;

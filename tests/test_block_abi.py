@@ -110,10 +110,15 @@ def test_balance_pointers_and_workspace():
         assert f(*with_none(P[:8], i), BIG) == INVALID
     assert f(*P[:8], ctypes.c_size_t(n.value - 1)) == WORKSPACE
     assert f(*P[:7], off(P[7], 4), BIG) == INVALID
+    for i in (3, 4, 5, 6, 7):                                      # an output in place of an input, or of another output
+        for j in (0, 1, 2, 3 if i != 3 else 4):
+            a = list(P[:8])
+            a[i] = a[j]
+            assert f(*a, BIG) == INVALID
     g = lambda *a: lib.moe_balance_backward(ctypes.byref(c), *a, None)  # noqa: E731
     for i in range(7):
         assert g(*with_none(P[:7], i), 0, 0) == INVALID
-    assert g(*P[:6], P[0], 0, 0) == INVALID and g(*P[:7], 63, 0) == INVALID
+    assert all(g(*P[:6], P[j], 0, 0) == INVALID for j in range(6)) and g(*P[:7], 63, 0) == INVALID
     none = balance(tokens=0)
     assert lib.moe_balance_backward(ctypes.byref(none), P[0], P[1], P[2], *[None] * 4, 0, 0, None) == OK
     assert lib.moe_balance_loss(ctypes.byref(none), P[0], P[1], P[2], None, P[4], P[5], None, None, 0, None) == INVALID
@@ -131,7 +136,8 @@ def adapters(**kw):
     (dict(out_ld=504), INVALID), (dict(in_cols=252), UNSUPPORTED), (dict(out_cols=500), UNSUPPORTED),
     (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(in_cols=(1 << 20) + 8), UNSUPPORTED),
     (dict(out_cols=(1 << 20) + 8), UNSUPPORTED), (dict(x_ld=260), UNSUPPORTED), (dict(base_ld=516), UNSUPPORTED),
-    (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(rows=1 << 27), UNSUPPORTED), (dict(rows=(1 << 27) - 1), OK), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
+    (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(rows=1 << 27), UNSUPPORTED),
+    (dict(rows=(1 << 27) - 1), OK), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
 ])
 def test_adapter_limits(kw, status):
     s, n = adapters(**kw), ctypes.c_size_t(0)

@@ -1,7 +1,7 @@
 """moe_adapters on the GPU against float64.
 
-The products' fp32 sums have `in` and parts * r terms: at most (in + 3 r + 16) 2^-24 of the sum of magnitudes (additions one after
-another).  Under a bf16 output the low-rank values keep two bf16 parts, each half a step (2^-8) off: 2^-16; under fp32
+The products' fp32 sums have `in` and parts * r terms: at most (in + 3 r + 16) 2^-24 of the sum of magnitudes (additions
+one after another).  Under a bf16 output the low-rank values keep two bf16 parts, each half a step (2^-8) off: 2^-16; under fp32
 three: 2^-24.  The output's own rounding: 2^-8 or 2^-24 of it."""
 import numpy as np
 import pytest
@@ -87,7 +87,8 @@ def test_rows_by_adapter_and_by_tile(rows, d_in, d_out, n, r, ranks, out):
         check(p, run(p))
 
 
-@pytest.mark.parametrize("rows,r,out", [(128, 16, torch.bfloat16), (100, 64, torch.float32), (97, 128, torch.bfloat16), (66, 32, torch.float32)])
+@pytest.mark.parametrize("rows,r,out", [(128, 16, torch.bfloat16), (100, 64, torch.float32), (97, 128, torch.bfloat16),
+                                        (66, 32, torch.float32)])
 def test_many_rows_of_one_adapter_among_many(rows, r, out):
     """Workgroups by adapter: one of them with more rows than a tile, and rows without an adapter likewise."""
     p = problem(rows, 1096, 264, 40, r, rows + r, out)

@@ -1,7 +1,7 @@
 """moe_balance_loss and moe_balance_backward on the GPU against float64.
 
-Counts and tokens are whole numbers: equal.  A token's p is fp32: an exponential (2 units in the last place), a sum of positive terms
-(under 16 roundings), two quotients: under 2^-19 of the value.  A sequence's sum of p has at most 64 + 64 + 16 additions of
+Counts and tokens are whole numbers: equal.  A token's p is fp32: an exponential (2 units in the last place), a sum of
+positive terms (under 16 roundings), two quotients: under 2^-19 of the value.  A sequence's sum of p has at most 64 + 64 + 16 additions of
 positive terms one after another: 2^-24 each, so 2^-16 in all is asked; values below 2^-126 may be 0.  The gradient
 p (c - D) counts against p (|c| + sum p |c|), its terms, with 2^-18, and its type's rounding (bf16 2^-8)."""
 import numpy as np
@@ -29,7 +29,7 @@ def problem(T, N, K, seed, dtype=torch.float32, ld=0):
 
 
 def config(logits, idx, S, softmax, ld=0, alpha=ALPHA):
-    return moe.make_balance_config(logits.shape[0], logits.shape[1], idx.shape[1], DT[logits.dtype], SCORE[softmax], S, alpha, ld)
+    return moe.make_balance_config(*logits.shape, idx.shape[1], DT[logits.dtype], SCORE[softmax], S, alpha, ld)
 
 
 def forward(logits, idx, starts, softmax, ld=0, S=None, on=None):
@@ -79,9 +79,10 @@ def check(logits, idx, starts, softmax, d_loss=None, ld=0):
 
 
 @pytest.mark.parametrize("softmax", [True, False])
-@pytest.mark.parametrize("T,N,K,dtype", [(1, 1, 1, torch.float32), (3, 8, 2, torch.bfloat16), (64, 60, 4, torch.float32),
-                                         (65, 64, 6, torch.float32), (777, 129, 8, torch.bfloat16), (500, 256, 8, torch.float32),
-                                         (130, 511, 32, torch.float32), (200, 512, 17, torch.bfloat16), (70, 2, 1, torch.bfloat16)])
+@pytest.mark.parametrize("T,N,K,dtype", [
+    (1, 1, 1, torch.float32), (3, 8, 2, torch.bfloat16), (64, 60, 4, torch.float32), (65, 64, 6, torch.float32),
+    (777, 129, 8, torch.bfloat16), (500, 256, 8, torch.float32), (130, 511, 32, torch.float32),
+    (200, 512, 17, torch.bfloat16), (70, 2, 1, torch.bfloat16)])
 def test_one_sequence(T, N, K, dtype, softmax):
     logits, idx = problem(T, N, K, T + N, dtype)
     check(logits, idx, None, softmax, torch.tensor([1.5], device="cuda"))
@@ -91,7 +92,8 @@ def test_one_sequence(T, N, K, dtype, softmax):
 
 
 @pytest.mark.parametrize("softmax", [True, False])
-@pytest.mark.parametrize("lengths", [[1, 63, 64, 65, 0, 0, 200, 7, 1], [0, 5, 0], [1] * 100, [3] * 90 + [300, 0, 0, 0], [128, 128, 16, 16]])
+@pytest.mark.parametrize("lengths", [[1, 63, 64, 65, 0, 0, 200, 7, 1], [0, 5, 0], [1] * 100, [3] * 90 + [300, 0, 0, 0],
+                                     [128, 128, 16, 16]])
 def test_sequences(lengths, softmax):
     starts = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
     logits, idx = problem(int(starts[-1]), 48, 3, len(lengths))
@@ -118,7 +120,8 @@ def test_tokens_outside_the_sequences():
     d = backward(logits, idx, starts, True, out, d_loss)
     inner = logits[20:211].contiguous(), idx[20:211].contiguous(), starts - 20
     ref = forward(*inner, True)
-    assert torch.equal(ref[1], out[1]) and torch.equal(ref[2], out[2]) and torch.allclose(ref[0], out[0], rtol=2.0 ** -15, atol=0)
+    assert torch.equal(ref[1], out[1]) and torch.equal(ref[2], out[2])
+    assert torch.allclose(ref[0], out[0], rtol=2.0 ** -15, atol=0)
     assert torch.equal(d[20:211], backward(*inner, True, ref, d_loss)) and (d[:20] == 0).all() and (d[211:] == 0).all()
     into = torch.full_like(logits, 5.0)
     backward(logits, idx, starts, True, out, d_loss, into=into)
@@ -172,11 +175,13 @@ def test_masked_extreme_and_not_finite_logits(softmax):
 def check_padding(logits, idx, softmax, row):
     out = forward(logits, idx, None, softmax)
     keep = torch.arange(logits.shape[0], device="cuda") != row
-    ref = forward(logits[keep].contiguous(), idx[keep].contiguous(), None, softmax)
-    assert torch.equal(out[1], ref[1]) and torch.equal(out[2], ref[2]) and torch.allclose(out[3], ref[3], rtol=2.0 ** -15, atol=2.0 ** -120)
+    others = logits[keep].contiguous(), idx[keep].contiguous(), None, softmax
+    ref = forward(*others)
+    assert torch.equal(out[1], ref[1]) and torch.equal(out[2], ref[2])
+    assert torch.allclose(out[3], ref[3], rtol=2.0 ** -15, atol=2.0 ** -120)
     one = torch.ones(1, device="cuda")
     d = backward(logits, idx, None, softmax, out, one)
-    assert (d[row] == 0).all() and torch.equal(d[keep], backward(logits[keep].contiguous(), idx[keep].contiguous(), None, softmax, out, one))
+    assert (d[row] == 0).all() and torch.equal(d[keep], backward(*others, out, one))
     return out, d
 
 
@@ -219,7 +224,8 @@ def test_no_tokens_and_no_sum():
     a = forward(logits, idx, None, True)
     b = [torch.empty_like(o) for o in a[:3]]
     cfg = config(logits, idx, 1, True)
-    moe.moe_balance_loss(cfg, logits, idx, None, *b, None, torch.empty(moe.moe_balance_workspace_size(cfg), dtype=torch.uint8, device="cuda"))
+    ws = torch.empty(moe.moe_balance_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    moe.moe_balance_loss(cfg, logits, idx, None, *b, None, ws)
     assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 

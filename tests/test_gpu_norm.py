@@ -1,9 +1,9 @@
 """moe_norm_forward and moe_norm_backward on the GPU against float64.
 
 The sum is one fp32 addition and one rounding: compared bit for bit.  rstd is fp32: the squares' sum has at most 3 + 2 +
-6 + 16 roundings behind a square's (8 values, 4 vectors, 64 lanes, 16 wavefronts) and is halved by the root; division and root
-add three: under 20 of 2^-24, and 2^-19 is asked.  y has two products more and its type's rounding (bf16 2^-8).  A code is within half a step (2^-4 of
-the value, 2^-10 of the scale below 2^-6 of it) and y's fp32 error.  dh is a difference, so its error counts
+6 + 16 roundings behind a square's (8 values, 4 vectors, 64 lanes, 16 wavefronts) and is halved by the root; division and
+root add three: under 20 of 2^-24, and 2^-19 is asked.  y has two products more and its type's rounding (bf16 2^-8).  A
+code is within half a step (2^-4 of the value, 2^-10 of the scale below 2^-6 of it) and y's fp32 error.  dh is a difference, so its error counts
 against its terms; d_weight has D additions one after another, the rows of a workgroup and the workgroups:
 (2^-18 + D 2^-24) of its terms."""
 import numpy as np
@@ -33,12 +33,16 @@ def inputs(rows, cols, stream, seed, size=1.0):
     return x, r, w, d_y, d_s
 
 
+def empty_codes(rows, cols):
+    return torch.full((rows, cols), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+
+
 def forward(x, r, w, stream, codes=False, y=True, total=True, rstd=True, eps=EPS, on=None):
     rows, cols = x.shape
     shape = moe.make_norm_shape(rows, cols, TYPES[stream][1], eps)
     out = {"sum": torch.full_like(x, float("nan")) if total and r is not None else None,
            "y": torch.full_like(x, float("nan")) if y else None,
-           "codes": torch.full((rows, cols), 0x7F, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn) if codes else None,
+           "codes": empty_codes(rows, cols) if codes else None,
            "scales": torch.full((rows, cols // 128), float("nan"), device="cuda") if codes else None,
            "rstd": torch.full((rows,), float("nan"), device="cuda") if rstd else None}
     moe.moe_norm_forward(shape, x, r, w, out["sum"], out["y"], out["codes"], out["scales"], out["rstd"], on)
@@ -75,7 +79,8 @@ def depth(rows):
 
 
 CASES = [(1, 8, "bf16"), (1, 7168, "bf16"), (3, 128, "f32"), (5, 520, "bf16"), (77, 2048, "bf16"), (9, 2056, "f32"),
-         (255, 1408, "f32"), (33, 4096, "bf16"), (2, 16392, "bf16"), (3, 32768, "f32"), (1021, 1024, "bf16"), (700, 7168, "bf16")]
+         (255, 1408, "f32"), (33, 4096, "bf16"), (2, 16392, "bf16"), (3, 32768, "f32"), (1021, 1024, "bf16"),
+         (700, 7168, "bf16")]
 
 
 @pytest.mark.parametrize("residual", [True, False])
