@@ -501,8 +501,7 @@ __global__ void __launch_bounds__(kThreads) balance_bwd_kernel(BalanceArgs a, Ba
 // (any other number of experts than a multiple of four: 64 lanes whatever their number, one kernel in place of four)
 int lanes_of(int n) { return n % 4 != 0 ? 64 : n <= 128 ? 16 : n <= 256 ? 32 : 64; }
 
-// Tokens of a workgroup of the forward pass: whole blocks of what its wavefronts hold at once, one workgroup a CU or so (the
-// second kernel reads a place for each: T=32768, 64 experts, 512 places XX us, 256 YY)
+// Tokens of a workgroup of the forward pass: whole blocks of what its wavefronts hold at once
 int chunk_of(const moe_balance_config& c) {
   const int64_t block = kPartWaves * (64 / lanes_of(c.n_routed));
   return (int)(block * std::max<int64_t>(1, ceil_div(ceil_div(c.tokens, block), kPlaces)));

@@ -1205,7 +1205,9 @@ moe_status moe_adapters(const moe_adapter_shape* shape, const void* x, const int
   if (out == x || out == a || out == b || out == workspace) return MOE_ERR_INVALID_ARG;
   const void* small[] = {row_adapter, scale, ranks};
   for (const void* p : small)
-    if (out == p || (workspace && workspace == p)) return MOE_ERR_INVALID_ARG;
+    if (out == p || reinterpret_cast<uintptr_t>(p) % 4 != 0) return MOE_ERR_INVALID_ARG;
+  for (const void* p : {x, a, b, base, small[0], small[1], small[2]})
+    if (workspace && workspace == p) return MOE_ERR_INVALID_ARG;
   const int64_t base_ld = shape->base_ld ? shape->base_ld : shape->out_cols;
   const int64_t out_ld = shape->out_ld ? shape->out_ld : shape->out_cols;
   if (out == base && base_ld != out_ld) return MOE_ERR_INVALID_ARG;

@@ -137,7 +137,8 @@ def adapters(**kw):
     (dict(rank=12), UNSUPPORTED), (dict(rank=136), UNSUPPORTED), (dict(in_cols=(1 << 20) + 8), UNSUPPORTED),
     (dict(out_cols=(1 << 20) + 8), UNSUPPORTED), (dict(x_ld=260), UNSUPPORTED), (dict(base_ld=516), UNSUPPORTED),
     (dict(out_ld=513), UNSUPPORTED), (dict(x_ld=1 << 24), UNSUPPORTED), (dict(rows=1 << 27), UNSUPPORTED),
-    (dict(rows=(1 << 27) - 1), OK), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK), (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
+    (dict(rows=(1 << 27) - 1), OK), (dict(x_ld=(1 << 24) - 8), OK), (dict(), OK),
+    (dict(rank=128, out_dtype=0, x_ld=264), OK), (dict(rows=0), OK),
 ])
 def test_adapter_limits(kw, status):
     s, n = adapters(**kw), ctypes.c_size_t(0)
@@ -147,6 +148,7 @@ def test_adapter_limits(kw, status):
 
 
 def test_adapter_pointers_and_workspace():
+    byte = lambda p: ctypes.c_void_p(p.value + 2)  # noqa: E731
     s, n = adapters(), ctypes.c_size_t(0)
     assert lib.moe_adapters_workspace_size(None, ctypes.byref(n)) == INVALID
     assert lib.moe_adapters_workspace_size(ctypes.byref(s), None) == INVALID
@@ -161,7 +163,10 @@ def test_adapter_pointers_and_workspace():
               (x, wh, a, b, sc, rk, base, off(out), ws), (x, wh, a, b, sc, rk, base, out, off(ws)),
               (x, wh, a, b, sc, rk, base, x, ws), (x, wh, a, b, sc, rk, base, a, ws), (x, wh, a, b, sc, rk, base, b, ws),
               (x, wh, a, b, sc, rk, base, ws, ws), (x, wh, a, b, sc, rk, base, wh, ws), (x, wh, a, b, sc, rk, base, sc, ws),
-              (x, wh, a, b, sc, rk, base, rk, ws), (x, wh, a, b, sc, rk, base, out, wh)):
+              (x, wh, a, b, sc, rk, base, rk, ws), (x, wh, a, b, sc, rk, base, out, wh),
+              (x, wh, a, b, sc, rk, base, out, x), (x, wh, a, b, sc, rk, base, out, a), (x, wh, a, b, sc, rk, base, out, b),
+              (x, wh, a, b, sc, rk, base, out, base), (x, byte(wh), a, b, sc, rk, base, out, ws),
+              (x, wh, a, b, byte(sc), rk, base, out, ws), (x, wh, a, b, sc, byte(rk), base, out, ws)):
         assert f(*q, BIG) == INVALID
     wide = adapters(base_ld=520)
     assert lib.moe_adapters(ctypes.byref(wide), x, wh, a, b, sc, rk, out, out, ws, BIG, None) == INVALID
