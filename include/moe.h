@@ -559,8 +559,8 @@ moe_status moe_balance_backward(const moe_balance_config* config, const void* lo
  * Beside a projection that all requests share (moe_matmul_fp8, or a library's): row t belongs to a
  * request whose adapter is e = row_adapter[t], and
  *   out_t = base_t + scale_e B_e (A_e x_t),
- * the contraction over A_e's first ranks[e] rows.  Rows may come in any order; those of one adapter side by side
- * (prompts) cost least.  For serving: there is no gradient. */
+ * the contraction over A_e's first ranks[e] rows.  Rows may come in any order; in large batches those of one adapter
+ * side by side (prompts) cost least.  For serving: there is no gradient. */
 typedef struct moe_adapter_shape {
   int32_t rows;               /* T: 0 to 2^27 - 1 */
   int32_t in_cols, out_cols;  /* 8 to 2^20, multiples of 8 */

@@ -11,7 +11,7 @@
 // 16 neighbouring rows form a tile.  The rows of a tile may have different adapters: for each that occurs the whole tile is
 // multiplied and the rows that have it keep the result, so every adapter in use is read once for a tile and rows need
 // no sorting.  Rows of other adapters are computed and dropped, never added as zeros: an infinity or NaN stays in its row.
-// Up to 128 rows of many adapters, workgroups go by adapters instead.
+// Few rows of many adapters (a decode batch) go by adapters instead.
 //
 // Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6
 // for the second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
@@ -27,15 +27,21 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int kWaves = 4, kThreads = 64 * kWaves, kWavesOfTile = kWaves;
-constexpr int kRows = 16;        // rows of a tile
+constexpr int kRows = 16;        // rows of a tile, or of an adapter at a time
 constexpr int kStep = 64;        // values of a wavefront's step along the first product's contraction
 constexpr int kCols = 64;        // output columns of a wavefront at a time
-// Workgroups go by adapters up to so many rows, and rows for each adapter there is: they read an adapter once, a tile of
-// rows reads each of its adapters one after the other; but an adapter of many rows is one workgroup's alone.  In a graph,
-// us, by adapters against by tiles, rows of all adapters mixed: 64 rows, 32 adapters, 16 x 7168 -> 4096: 10.8, 19.8; rank
-// 64: 17.8, 31.0; 128 rows 14.3, 19.1; rank 64 23.4, 31.7; 64 rows, 4 adapters, 16 x 2048 -> 7168: 10.4, 9.0.
-// Adapters side by side: 64 rows, 32 adapters 10.8, 15.7; 128 rows 14.1, 13.4; 64 rows, 4 adapters 14.5, 8.0.
-constexpr int kLeadRows = 128, kLeadShare = 4;
+// Workgroups go by adapters up to so many rows (each looks through all of them), and rows for each adapter there is: they
+// read an adapter once for 16 of its rows, a tile of neighbouring rows reads all of its adapters one after the other; but
+// workgroups whose adapter has no further rows come for nothing.  In a graph, us, by adapters against by tiles, rows of all
+// adapters mixed, then rows of one side by side, 7168 -> 4096: 32 adapters of rank 64: 64 rows 15.0, 31.0; 14.5, 15.7.
+// 140 rows 16.3, 32.3; 16.1, 21.9.  500 rows 22.8, 59; 26.6, 25.4.  32 of rank 16: 500 rows 16.8, 24.1; 18.5, 13.6.  8 of
+// rank 16: 64 rows 7.9, 11.1; 9.7, 8.6.  256 rows (past the share) 11.3, 13.7; 11.3, 10.2.  An adapter's rows are shared by
+// more workgroups the more rows there are for each (one against two, 140 rows of 32 adapters of rank 64: 17.3, 16.3; 64
+// rows 15.0, 15.4; two against four, 500 rows: 22.4, 22.8; side by side 30.4, 26.6).
+constexpr int kUnitRows = 1024, kUnitShare = 16;
+// Workgroups of a product, or so.  By adapters about as many as the registers let run at once (in a graph, us, 512 against
+// 1024: 64 rows, 32 adapters of rank 64, 7168 -> 4096: 15.0, 16.6; 500 rows 22.8, 24.5)
+constexpr int kTileBlocks = 2048, kUnitBlocks = 512;
 // One launch in place of two up to so many rows and values of an adapter's A, which every workgroup then reads whole.
 // In a graph, us, one kernel against two: 1 row, 16 x 2048 -> 7168: 5.4, 7.1; 16 rows, 32 x 2048 -> 4096: 7.5, 7.7;
 // 1 row, 16 x 7168 -> 4096: 8.2, 7.1; 32 rows, 32 x 2048 -> 4096: 8.5, 8.4.
@@ -54,6 +60,7 @@ struct AdapterArgs {
   int in, outs, n, r;
   int splits, per_split;         // slices of the first product, values of each
   int blocks, per_block;         // workgroups of a tile in the second product, columns of each
+  int units, subs;               // by adapters: their number, workgroups that share an adapter's rows
 };
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -81,30 +88,46 @@ __device__ __forceinline__ void for_adapters(int mine, F f) {
   }
 }
 
-// The rows of a workgroup that goes by adapters: `first` is its row, and if that is the first one with its adapter e
-// (or the first without one) the workgroup takes all rows that have the same; otherwise there are none.  Every wavefront
-// finds them by itself: a ballot for each 64 rows, and a permutation that brings the rows of e to the lanes in front.
-struct LeadRows {
-  int count, low, high;   // rows number 0 to 63 and 64 to 127 of e, one a lane
-  __device__ __forceinline__ int at(int i) const { return i < 64 ? __shfl(low, i, 64) : __shfl(high, i - 64, 64); }
+// The rows of a workgroup that goes by adapters.  Its unit is an adapter or, with fewer rows than adapters, a row, which
+// stands for its adapter if it is the first to have it.  16 rows at a time: every wavefront finds
+// them by itself, a ballot for each 64 rows and a permutation that brings those of the adapter to the lanes in front.
+struct UnitRows {
+  int adapter;   // -1: none
+  int count;     // 0 to 16
+  int row;       // lane i < count: the i-th
 };
 __device__ __forceinline__ int bits_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
-__device__ __forceinline__ LeadRows lead_rows(const AdapterArgs& g, int first, int e) {
-  const int lane = threadIdx.x & 63;
-  const bool is0 = lane < g.rows && adapter_of(g, lane) == e, is1 = lane + 64 < g.rows && adapter_of(g, lane + 64) == e;
-  const uint64_t m0 = __ballot(is0), m1 = __ballot(is1);
-  const uint64_t before = (uint64_t(1) << (first & 63)) - 1;
-  LeadRows l{0, 0, 0};
-  if (first < 64 ? (m0 & before) != 0 : (m0 != 0 || (m1 & before) != 0)) return l;
-  const int n0 = __popcll(m0), n1 = __popcll(m1), b0 = bits_below(m0), b1 = bits_below(m1);
-  const int to0 = is0 ? b0 : n0 + lane - b0, to1 = (n0 + (is1 ? b1 : n1 + lane - b1)) & 63;
-  const int p0 = __builtin_amdgcn_ds_permute(4 * to0, lane), p1 = __builtin_amdgcn_ds_permute(4 * to1, lane + 64);
-  l.count = n0 + n1;
-  l.low = lane < n0 ? p0 : p1;
-  l.high = p1;
-  return l;
+__device__ __forceinline__ UnitRows unit_rows(const AdapterArgs& g, int unit, int group) {
+  constexpr int kBatch = 4;   // runs of 64 rows loaded at once
+  const int lane = threadIdx.x & 63, from = group * kRows, rows = (int)g.rows;
+  const bool leads = g.units < g.n;
+  const int own = leads ? g.row_adapter[unit] : unit;   // (on its way with the first rows)
+  UnitRows u{-1, 0, 0};
+  int seen = 0;
+  for (int r0 = 0; r0 < rows && seen < from + kRows; r0 += 64 * kBatch) {
+    int e[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) e[k] = g.row_adapter[min(r0 + 64 * k + lane, rows - 1)];
+    if (own < 0 || own >= g.n) return u;
+    u.adapter = own;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int r = r0 + 64 * k + lane;
+      if (r0 + 64 * k >= rows) break;
+      const bool has = r < rows && e[k] == u.adapter;
+      const uint64_t m = __ballot(has);
+      if (m == 0) continue;
+      if (leads && seen == 0 && r0 + 64 * k + __builtin_ctzll(m) != unit) return u;
+      const int begin = seen - from, at = begin + bits_below(m);
+      const int row = __builtin_amdgcn_ds_permute(4 * (has && at >= 0 && at < kRows ? at : kRows), r);
+      seen += __popcll(m);
+      if (lane >= begin && lane < seen - from) u.row = row;
+    }
+  }
+  u.count = max(0, min(kRows, seen - from));
+  return u;
 }
 
 // One step of the first product for a tile of 16 rows (of x, or of A): 64 values of each, as they are loaded.  Eight
@@ -141,18 +164,13 @@ struct LowLds {
 // neighbouring ranks of one token.  RT tiles of 16 ranks, kept[j]: ranks 16 j + 4 (lane / 16) of token lane mod 16, whose
 // adapter is `mine` and whose row of x begins at x + at.  The values from begin on, of which the wavefront takes
 // every waves-th run of 64, the operands of kAhead of them in flight.
-template <int RT, int kAhead, bool MIXED>
+template <int RT, int kAhead>
 __device__ __forceinline__ void low_sums(const AdapterArgs& g, const uint16_t* x, uint32_t at, int mine, int begin, int end,
                                          int wave, int waves, char* lds, f32x4 (&kept)[RT]) {
   constexpr int kAtOnce = LowLds<RT>::kAtOnce;
   const int lane = threadIdx.x & 63, quad = lane >> 4;
-  // MIXED: with as many adapters as wavefronts, these take an adapter each and all values, in place of all adapters one
-  // after the other and every waves-th run (140 rows of 128 adapters, 32 x 2048: 25.6 -> 22.2 us, both products)
-  int kinds = 0, number = 0;
-  if constexpr (MIXED) for_adapters(mine, [&](int) { ++kinds; });
-  const bool each = MIXED && kinds >= waves;
   // whole steps of the wavefront, and where a last one may end early
-  const int stride = each ? kStep : kStep * waves, first = begin + (each ? 0 : kStep * wave);
+  const int stride = kStep * waves, first = begin + kStep * wave;
   const int n = first + kStep <= end ? (end - kStep - first) / stride + 1 : 0;
   const int tail = first + n * stride;
   const uint32_t chunk = 8 * (lane & 7);
@@ -162,7 +180,6 @@ __device__ __forceinline__ void low_sums(const AdapterArgs& g, const uint16_t* x
 #pragma unroll
   for (int j = 0; j < RT; ++j) kept[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   for_adapters(mine, [&](int e) {
-    if (each && number++ % waves != wave) return;
     const int rank = rank_of(g, e);
     if (rank == 0) return;
     const uint16_t* a = g.a + (int64_t)e * g.r * g.in;
@@ -274,51 +291,50 @@ __device__ __forceinline__ f32x4 sum_of_waves(const char (&lds)[WAVES][BYTES], i
 }
 
 // A slice of the first product for a tile of rows, or for the rows of an adapter.
-template <int RT, bool LEAD>
+template <int RT, bool UNITS>
 __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
   __shared__ __align__(16) char lds[kWaves][LowLds<RT>::kBytes];
   const int lane = threadIdx.x & 63, col = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int64_t tile = blockIdx.x / g.splits;
+  const int tile = blockIdx.x / g.splits, sub = UNITS ? tile / (unsigned)g.units : 0, unit = tile - sub * g.units;
   const int slice = blockIdx.x - (unsigned)tile * g.splits, begin = slice * g.per_split, end = min(g.in, begin + g.per_split);
-  LeadRows rows{kRows, 0, 0};
-  int leader = -1;
-  if constexpr (LEAD) {
-    leader = adapter_of(g, tile);
-    if (leader < 0) return;
-    rows = lead_rows(g, (int)tile, leader);
-  }
-  for (int group = 0; group < rows.count; group += kRows) {
+  for (int group = sub;; group += g.subs) {
+    UnitRows rows{-1, kRows, 0};
+    if constexpr (UNITS) {
+      rows = unit_rows(g, unit, group);
+      if (rows.count == 0) return;
+    }
     int64_t t;
     int mine;
-    if constexpr (LEAD) {
-      t = rows.at(min(group + col, rows.count - 1));
-      mine = group + col < rows.count ? leader : -1;
+    if constexpr (UNITS) {
+      t = __shfl(rows.row, min(col, rows.count - 1), 64);
+      mine = col < rows.count ? rows.adapter : -1;
     } else {
-      t = tile * kRows + col;
+      t = (int64_t)tile * kRows + col;
       mine = adapter_of(g, t);
     }
     // (32-bit offsets from the first row of the tile, or of all)
-    const uint32_t at = mine < 0 ? 0u : (LEAD ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
+    const uint32_t at = mine < 0 ? 0u : (UNITS ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
     f32x4 kept[RT];
-    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1, !LEAD && RT <= 2>(g, g.x + (LEAD ? 0 : tile * kRows * g.x_ld), at, mine,
-                                                                 begin, end, wave, kWaves, lds[wave], kept);
+    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1>(g, g.x + (UNITS ? 0 : (int64_t)tile * kRows * g.x_ld), at, mine, begin, end,
+                                                wave, kWaves, lds[wave], kept);
     leave_sums<RT>(kept, lds[wave]);
     __syncthreads();
     for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
       const int row = i / (RT * 4), c = i % (RT * 4) * 4;
       int64_t to;
       bool in;
-      if constexpr (LEAD) {
-        in = group + row < rows.count;
-        to = rows.at(min(group + row, rows.count - 1));
+      if constexpr (UNITS) {
+        in = row < rows.count;
+        to = __shfl(rows.row, min(row, rows.count - 1), 64);
       } else {
-        to = tile * kRows + row;
+        to = (int64_t)tile * kRows + row;
         in = to < g.rows;
       }
       const f32x4 s = sum_of_waves<RT>(lds, row, c);
       if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
     }
-    if (LEAD && group + kRows < rows.count) __syncthreads();
+    if (!UNITS || rows.count < kRows) return;
+    __syncthreads();
   }
 }
 
@@ -362,14 +378,14 @@ struct RawFour<float> {
 // of 32 holds two).
 // FORM: tiles of neighbouring rows, the rows of an adapter, or those with the first product in the same kernel (each
 // workgroup computes it whole, for its columns: for few rows and little of A that is less than a launch more).
-enum AdapterForm { kTileForm, kLeadForm, kFewForm };
+enum AdapterForm { kTileForm, kUnitForm, kFewForm };
 constexpr int kFewWaves = 8;
 // wavefronts a SIMD that the registers have to leave room for: three where the kernel would take a little more than that allows
 constexpr int out_waves(int rt, int form) { return form != kFewForm && (rt == 1 || (rt == 2 && form == kTileForm)) ? 3 : 1; }
 template <int RT, int PARTS, typename T, int FORM>
 __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, out_waves(RT, FORM))
     adapters_out_kernel(AdapterArgs g) {
-  constexpr bool LEAD = FORM != kTileForm, FEW = FORM == kFewForm;
+  constexpr bool UNITS = FORM != kTileForm, FEW = FORM == kFewForm;
   constexpr int kWaves = FEW ? kFewWaves : kWavesOfTile, kThreads = 64 * kWaves;
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
@@ -391,24 +407,32 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char* mine_lds = lds[wave];
   auto chunk_at = [&](int i) { return mine_lds + ((i & ~15) | ((i + i / kTurn) & 15)) * 16; };
-  const int64_t tile = blockIdx.x / g.blocks;
+  const int tile = blockIdx.x / g.blocks, sub = UNITS ? tile / (unsigned)g.units : 0, unit = tile - sub * g.units;
+  const bool copy = UNITS && sub >= g.subs;   // the rows without an adapter of tile `copied`
+  const int copied = tile - g.units * g.subs;
   const int block = blockIdx.x - (unsigned)tile * g.blocks;
   const int first = block * g.per_block + kCols * wave, end = min(g.outs, (block + 1) * g.per_block);
-  LeadRows rows{kRows, 0, 0};
-  int leader = -1;
-  if constexpr (LEAD) {
-    leader = adapter_of(g, tile);
-    rows = lead_rows(g, (int)tile, leader);
-  }
-  for (int group = 0; group < rows.count; group += kRows) {
+  for (int group = sub;; group += g.subs) {
+    UnitRows rows{-1, kRows, 0};
+    if constexpr (UNITS) {
+      if (copy) {
+        const int r = copied * kRows + lane;
+        const bool without = lane < kRows && r < g.rows && adapter_of(g, r) < 0;
+        const uint64_t m = __ballot(without);
+        rows = {-1, (int)__popcll(m), __builtin_amdgcn_ds_permute(4 * (without ? bits_below(m) : kRows), r)};
+      } else {
+        rows = unit_rows(g, unit, group);
+      }
+      if (rows.count == 0) return;
+    }
     // rows of the tile
-    const int here = LEAD ? min(kRows, rows.count - group) : (int)min((int64_t)kRows, g.rows - tile * kRows);
+    const int here = UNITS ? rows.count : (int)min((int64_t)kRows, g.rows - (int64_t)tile * kRows);
     auto row_of = [&](int i) -> int64_t {   // (rows the tile does not have: its last one)
-      if constexpr (LEAD) return rows.at(group + min(i, here - 1));
-      else return tile * kRows + min(i, here - 1);
+      if constexpr (UNITS) return __shfl(rows.row, min(i, here - 1), 64);
+      else return (int64_t)tile * kRows + min(i, here - 1);
     };
     const int64_t t = row_of(col);
-    const int mine = col < here ? (LEAD ? leader : adapter_of(g, t)) : -1;
+    const int mine = col < here ? (UNITS ? rows.adapter : adapter_of(g, t)) : -1;
     const uint64_t with = __ballot(mine >= 0);
     const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
     const bool alone = RT <= 4 && with != 0 && __ballot(mine >= 0 && mine != e0) == 0;   // one adapter in the tile
@@ -440,11 +464,11 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
     if (g.base && first < end) load_base(now, first);
     bf16x8 low[kSteps];
     if (with) {   // (the wavefronts of a workgroup have the same rows)
-      if (LEAD && group > 0) __syncthreads();
+      if (UNITS && group > sub) __syncthreads();
       const int items = here * RT * 4, shares = FEW ? 1 : max(1, min(kShares, kThreads / items));
       if constexpr (FEW) {
         f32x4 part[RT];
-        low_sums<RT, RT == 1 ? 3 : 2, false>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave,
+        low_sums<RT, RT == 1 ? 3 : 2>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave,
                                              kWaves, mine_lds, part);
         leave_sums<RT>(part, mine_lds);
         __syncthreads();
@@ -581,6 +605,7 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
         store(now, kept, c0);
       }
     }
+    if (!UNITS || copy || here < kRows) return;
   }
 }
 
@@ -588,20 +613,26 @@ struct AdapterPlan {
   int tiles16;                   // RT
   AdapterForm form;
   int splits, per_split, blocks, per_block;
+  int units, subs;
 };
 
 AdapterPlan plan_of(const moe_adapter_shape& s) {
   AdapterPlan p;
   p.tiles16 = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : s.rank <= 64 ? 4 : 8;
+  const int64_t n = s.n_adapters, x_ld = s.x_ld ? s.x_ld : s.in_cols;
   p.form = s.rows <= kFewRows && p.tiles16 <= 2 && (int64_t)s.rank * s.in_cols <= kFewValues ? kFewForm
-           : s.rows <= kLeadRows && s.rows <= kLeadShare * (int64_t)s.n_adapters               ? kLeadForm
-                                                                                               : kTileForm;
-  const int64_t tiles = std::max<int64_t>(1, ceil_div(s.rows, kRows)), run = kStep * kWaves;
-  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(2048, tiles), ceil_div(s.in_cols, run)));
+           : s.rows <= kUnitRows && s.rows <= kUnitShare * n && s.rows * x_ld < (int64_t(1) << 32)   // (32-bit offsets)
+               ? kUnitForm
+               : kTileForm;
+  p.units = (int)std::min<int64_t>(s.rows, n);
+  p.subs = p.form != kUnitForm || s.rows <= 4 * n ? 1 : s.rows <= 8 * n ? 2 : 4;
+  const int64_t tiles = p.form == kUnitForm ? p.units * p.subs : std::max<int64_t>(1, ceil_div(s.rows, kRows));
+  const int64_t some = p.form == kUnitForm ? kUnitBlocks : kTileBlocks, run = kStep * kWaves;
+  const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(some, tiles), ceil_div(s.in_cols, run)));
   p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
   const int64_t stride = kCols * (p.form == kFewForm ? kFewWaves : kWaves);
-  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(2048, tiles)), stride) * stride);
+  p.per_block = (int)(ceil_div(ceil_div(s.out_cols, ceil_div(some, tiles)), stride) * stride);
   p.blocks = (int)ceil_div(s.out_cols, p.per_block);
   return p;
 }
@@ -616,15 +647,17 @@ hipError_t out_t(const AdapterArgs& g, int out_dtype, dim3 grid, hipStream_t st)
 template <int RT>
 hipError_t run_t(const AdapterArgs& g, AdapterForm form, int out_dtype, hipStream_t st) {
   // (the slices or columns of a tile are neighbours in the grid: workgroups at work together cover whole rows)
-  const unsigned tiles = (unsigned)(form == kTileForm ? ceil_div(g.rows, kRows) : g.rows);
-  const dim3 grid(tiles * g.blocks);
+  const int64_t row_tiles = ceil_div(g.rows, kRows);
+  const unsigned tiles = (unsigned)(form == kTileForm ? row_tiles : (int64_t)g.units * g.subs);
+  // by adapters, the rows without one are copied by further workgroups, unless they are where they belong
+  const dim3 grid((tiles + (unsigned)(form == kTileForm || g.base == g.out ? 0 : row_tiles)) * g.blocks);
   if constexpr (RT <= 2)
     if (form == kFewForm) return out_t<RT, kFewForm>(g, out_dtype, grid, st);
   const hipError_t err =
       form == kTileForm ? launch_kernel(adapters_low_kernel<RT, false>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g)
                         : launch_kernel(adapters_low_kernel<RT, true>, dim3(tiles * g.splits), dim3(kThreads), 0, st, g);
   if (err != hipSuccess) return err;
-  return form == kTileForm ? out_t<RT, kTileForm>(g, out_dtype, grid, st) : out_t<RT, kLeadForm>(g, out_dtype, grid, st);
+  return form == kTileForm ? out_t<RT, kTileForm>(g, out_dtype, grid, st) : out_t<RT, kUnitForm>(g, out_dtype, grid, st);
 }
 
 }  // namespace
@@ -658,7 +691,9 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       p.splits,
                       p.per_split,
                       p.blocks,
-                      p.per_block};
+                      p.per_block,
+                      p.units,
+                      p.subs};
   switch (p.tiles16) {
     case 1: return run_t<1>(g, p.form, s.out_dtype, st);
     case 2: return run_t<2>(g, p.form, s.out_dtype, st);

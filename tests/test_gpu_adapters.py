@@ -81,7 +81,7 @@ def test_against_float64(rows, d_in, d_out, n, r, ranks, out, order):
     (128, 520, 256, 40, 32, True), (128, 264, 72, 1, 64, False), (129, 264, 72, 1, 64, False), (140, 328, 136, 5, 32, True),
     (200, 456, 72, 3, 64, True), (257, 72, 8, 60, 8, False), (300, 8, 328, 3, 128, True)])
 def test_rows_by_adapter_and_by_tile(rows, d_in, d_out, n, r, ranks, out):
-    """Few rows and little of A (one kernel), up to 128 rows (workgroups by adapter, more than 16 rows of one), tiles."""
+    """Few rows and little of A (one kernel), workgroups by adapter (more than 16 rows of one), tiles."""
     for order in ("mixed", "prompts"):
         p = problem(rows, d_in, d_out, n, r, rows + d_out, out, order, ranks)
         check(p, run(p))
@@ -95,6 +95,46 @@ def test_many_rows_of_one_adapter_among_many(rows, r, out):
     pick = torch.rand(rows, device="cuda")
     p["which"] = torch.where(pick < 0.4, 7, torch.where(pick < 0.7, -1, p["which"])).to(torch.int32)
     check(p, run(p))
+
+
+@pytest.mark.parametrize("out", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d_in,d_out,n,r,ranks", [
+    (1024, 520, 136, 64, 16, False), (1023, 264, 328, 100, 32, True), (1025, 264, 72, 100, 32, False),
+    (500, 1032, 520, 32, 64, True), (513, 264, 72, 32, 24, False), (700, 136, 264, 1200, 8, False),
+    (1024, 72, 72, 1025, 24, True), (320, 264, 1096, 40, 128, True), (257, 2056, 264, 16, 16, False),
+    (128, 40, 2056, 8, 48, True)])
+def test_decode_batches(rows, d_in, d_out, n, r, ranks, out):
+    """Up to 1024 rows and 16 an adapter go by adapters: one, two and four workgroups that share an adapter's rows, fewer
+    rows than adapters, one adapter with most rows; rows without one copied, or left where they are."""
+    p = problem(rows, d_in, d_out, n, r, rows + d_in + n, out, ranks=ranks)
+    for k in range(3):
+        if k == 1:
+            p["which"] = torch.sort(p["which"]).values.flip(0).contiguous()
+        if k == 2:
+            pick = torch.rand(rows, device="cuda")
+            p["which"] = torch.where(pick < 0.6, n - 1, torch.where(pick < 0.8, n + 5, p["which"])).to(torch.int32)
+        first = run(p)
+        check(p, first)
+        in_place = p["base"].clone()
+        run({**p, "own": in_place}, base="own", into=in_place)
+        assert torch.equal(in_place, first)
+    p["which"][:] = -9
+    assert torch.equal(run(p), p["base"])
+    check(p, run(p, base=None), base=False)
+
+
+@pytest.mark.parametrize("rows", [511, 600])
+def test_rows_far_apart(rows):
+    """x beyond 2^32 elements: by adapters up to there, by tiles past it."""
+    p = problem(rows, 264, 136, 64, 16, rows)
+    first = run(p)
+    far = torch.empty((rows - 1 << 23) + 264, dtype=torch.bfloat16, device="cuda").as_strided((rows, 264), (1 << 23, 1))
+    far.copy_(p["x"])
+    p["x"] = far
+    out = run(p, x_ld=1 << 23)
+    check({**p, "x": far.contiguous()}, out)
+    if rows == 511:
+        assert torch.equal(out, first)
 
 
 def test_large_and_long():
