@@ -364,40 +364,49 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   counts[wave][lane] = n;
   if (lane == 0) lens[wave] = len;
   __syncthreads();
-  const int wide = quads > 64 ? quads / 64 : 1;   // wavefronts of a row of columns
-  float f = 0.0f;
-  if (tid < quads) {
-    p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    n = i32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int w = 0; w < kMost; ++w) {   // (all loads at once)
-      const f32x4 v = sums[w][lane];
-      const i32x4 m = counts[w][lane];
-      if (w < waves && (wide == 1 || (w & 1) == wave)) {
-        p += v;
-        n += m;
-      }
-    }
-    float term[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int i = 4 * tid + j;
-      term[j] = i < a.N ? (float)n[j] * p[j] : 0.0f;
-      if (i < a.N) {
-        o.counts[(int64_t)s * a.N + i] = n[j];
-        if (o.prob_sum) o.prob_sum[(int64_t)s * a.N + i] = p[j];
-      }
-    }
-    f = sum_run<4>(term);
-  }
-  f = sum_of<64>(f);
-  if (lane == 0 && wave < 2) dots[wave] = f;
-  __syncthreads();
-  if (tid != 0) return;
+  const int wide = quads > 64 ? 2 : 1;   // wavefronts of a row of columns
+  if (wide == 1 && wave > 0) return;
+  const int half = wave & (wide - 1);
+  p = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  n = i32x4{0, 0, 0, 0};
   len = 0;
+  for (int w0 = half; w0 < waves; w0 += 4 * wide) {   // (four loads at once; waves is a multiple of wide)
+    f32x4 v[4];
+    i32x4 m[4];
+    int q[4];
 #pragma unroll
-  for (int w = 0; w < kMost; ++w) len += w < waves && (wide == 1 || (w & 1) == 0) ? lens[w] : 0;
-  const float dot = wide == 2 ? dots[0] + dots[1] : dots[0];
+    for (int k = 0; k < 4; ++k) {
+      const int w = min(w0 + k * wide, waves - wide + half);
+      v[k] = sums[w][lane];
+      m[k] = counts[w][lane];
+      q[k] = lens[w];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (w0 + k * wide < waves) {
+        p += v[k];
+        n += m[k];
+        len += q[k];
+      }
+  }
+  float term[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int i = 4 * tid + j;
+    const bool in = i < a.N && tid < quads;
+    term[j] = in ? (float)n[j] * p[j] : 0.0f;
+    if (in) {
+      o.counts[(int64_t)s * a.N + i] = n[j];
+      if (o.prob_sum) o.prob_sum[(int64_t)s * a.N + i] = p[j];
+    }
+  }
+  float dot = sum_of<64>(sum_run<4>(term));
+  if (wide == 2) {
+    if (lane == 0 && wave < 2) dots[wave] = dot;
+    __syncthreads();
+    dot = dots[0] + dots[1];
+  }
+  if (tid != 0) return;
   o.tokens[s] = len;
   o.loss[s] = len == 0 ? 0.0f : a.alpha * (dot / (float)len) * ((float)a.N / ((float)a.K * (float)len));
 }
