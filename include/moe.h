@@ -522,7 +522,7 @@ typedef struct moe_balance_config {
   int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
 } moe_balance_config;
 
-/* Bytes of device workspace that moe_balance_loss needs for `config`. */
+/* Bytes of device workspace that moe_balance_loss needs for `config` (0 where one kernel does all). */
 moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* bytes);
 
 /*   logits      [T, N]  fp32 or bf16 (an expert at -inf has p = 0)

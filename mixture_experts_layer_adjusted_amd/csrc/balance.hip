@@ -13,11 +13,12 @@
 // counts once for every sequence that it meets: chunk c and sequence s have the place c + s, which no other pair has (from
 // one pair to the next, at least one of the two grows).  A second kernel adds up the places of each sequence, in order: no
 // floating-point atomics.  (A sum over several workgroups a sequence, the last by a ticket, cost 2 us of device-wide
-// atomics and gained less.)
+// atomics and gained less.)  Few tokens take one kernel, a workgroup a sequence.
 //
 // Bound by latency and instructions: 32768 tokens of 64 experts, softmax: 6.0 us (8.4 MB), the second kernel 5.8, the gradient
 // 6.3 (16.8 MB); 16384 tokens of 256 experts, sigmoid: 10.0 (16.8 MB; 330 vector instructions for two tokens), 6.5, 9.5 (33.6
-// MB).  Loads of one value each where four lie side by side cost the gradient 14.0 in place of 9.4.
+// MB).  Loads of one value each where four lie side by side cost the gradient 14.0 in place of 9.4.  7 sequences of 1021 tokens
+// of 60 experts, softmax: 7.1 in one kernel (5.6 + 3.9 in two), the gradient 3.1.
 #include "lanes.h"
 #include "moe_internal.h"
 
@@ -192,6 +193,98 @@ __device__ __forceinline__ void load_picks(const BalanceArgs& a, int64_t t, int 
   for (int h = 0; h < kPicks<L>; ++h) pick[h] = lane + h * L < a.K ? a.idx[t * a.K + lane + h * L] : -1;
 }
 
+struct BalanceOut {
+  float* loss;
+  int32_t *counts, *tokens;
+  float* prob_sum;   // or null
+};
+
+// the loss from sum_i n_i sum_t p_{t,i} and L
+__device__ __forceinline__ float balance_of(const BalanceArgs& a, float dot, int len) {
+  return len == 0 ? 0.0f : a.alpha * (dot / (float)len) * ((float)a.N / ((float)a.K * (float)len));
+}
+
+// Few tokens (few_tokens, below): a workgroup a sequence does all of it.
+template <int L, int C, bool WHOLE, typename TL, bool SOFTMAX>
+__global__ void __launch_bounds__(kPartThreads) balance_few_kernel(BalanceArgs a, BalanceOut o) {
+  extern __shared__ float lds[];   // [kPartWaves][N] sums, then int [N] counts, int [1] tokens
+  __shared__ float dots[kPartWaves];
+  constexpr int kTokens = 64 / L, kBlock = kPartWaves * kTokens;
+  const int lane = threadIdx.x & (L - 1), slot = (threadIdx.x & 63) / L, wave = threadIdx.x >> 6, s = blockIdx.x;
+  int* counts = reinterpret_cast<int*>(lds + kPartWaves * a.N);
+  const int T = (int)a.T, begin = a.start ? max(0, a.start[s]) : 0, end = a.start ? min(T, a.start[s + 1]) : T;
+  float total[C][4];
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) total[c][j] = 0.0f;
+  // a block's logits and picks, on their way while the block before is worked on
+  Four<WHOLE, TL> next[C];
+  int next_pick[kPicks<L>];
+  auto load = [&](int block) {
+    const int t = min(block + wave * kTokens + slot, end - 1);
+    load_token<L, C, WHOLE>(static_cast<const TL*>(a.logits) + t * a.ld, a.N, lane, next);
+    load_picks<L>(a, t, lane, next_pick);
+  };
+  if (begin < end) load(begin);
+  for (int i = threadIdx.x; i < a.N + 1; i += kPartThreads) counts[i] = 0;
+  __syncthreads();
+  for (int block = begin; block < end; block += kBlock) {
+    float l[C][4], rest[C][4];
+    int pick[kPicks<L>];
+    bool some = false;
+    unpack_token<L, C, WHOLE>(next, a.N, lane, l);
+#pragma unroll
+    for (int h = 0; h < kPicks<L>; ++h) {
+      pick[h] = next_pick[h] < a.N ? next_pick[h] : -1;
+      some |= pick[h] >= 0;
+    }
+    if (block + kBlock < end) load(block + kBlock);
+    const bool real = max_of<L>((uint32_t)some) != 0 && block + wave * kTokens + slot < end;
+    shares<L, C, SOFTMAX>(l, rest);
+    if (real) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) total[c][j] += l[c][j];
+#pragma unroll
+      for (int h = 0; h < kPicks<L>; ++h)
+        if (pick[h] >= 0) atomicAdd(&counts[pick[h]], 1);
+      if (lane == 0) atomicAdd(&counts[a.N], 1);
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = 4 * (c * L + lane) + j;
+      const float v = slots_sum<L>(total[c][j]);
+      if (slot == 0 && i < a.N) lds[wave * a.N + i] = v;
+    }
+  __syncthreads();
+  const int i = threadIdx.x;
+  float term = 0.0f;
+  if (i < a.N) {   // (N is at most 512)
+    float v[kPartWaves];
+#pragma unroll
+    for (int w = 0; w < kPartWaves; ++w) v[w] = lds[w * a.N + i];
+    const float p = sum_run<kPartWaves>(v);
+    const int n = counts[i];
+    term = (float)n * p;
+    o.counts[(int64_t)s * a.N + i] = n;
+    if (o.prob_sum) o.prob_sum[(int64_t)s * a.N + i] = p;
+  }
+  term = sum_of<64>(term);
+  if ((i & 63) == 0) dots[wave] = term;
+  __syncthreads();
+  if (i != 0) return;
+  float dot = 0.0f;
+  for (int w = 0; 64 * w < a.N; ++w) dot += dots[w];
+  const int len = counts[a.N];
+  o.tokens[s] = len;
+  o.loss[s] = balance_of(a, dot, len);
+}
+
 // L lanes a token.  chunk: tokens of a workgroup, in blocks that lie in registers together
 template <int L, int C, bool WHOLE, typename TL, bool SOFTMAX>
 __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs a, int chunk, float* __restrict__ places) {
@@ -289,12 +382,6 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
     leave();
   }
 }
-
-struct BalanceOut {
-  float* loss;
-  int32_t *counts, *tokens;
-  float* prob_sum;   // or null
-};
 
 // One workgroup a sequence: its places added up in order, then the loss, which is a sum over all columns.  `quads` threads (a
 // power of two, 16 at least) take four columns each, groups of them every further place, eight loads at once.
@@ -408,7 +495,7 @@ __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs 
   }
   if (tid != 0) return;
   o.tokens[s] = len;
-  o.loss[s] = len == 0 ? 0.0f : a.alpha * (dot / (float)len) * ((float)a.N / ((float)a.K * (float)len));
+  o.loss[s] = balance_of(a, dot, len);
 }
 
 __global__ void balance_zero_kernel(BalanceOut o, int S, int N) {
@@ -532,6 +619,25 @@ hipError_t with_lanes(int n, F f) {
   return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, bool_constant<true>{});
 }
 
+// One kernel, a workgroup a sequence, for few tokens: a block of them costs such a workgroup 0.8 us (1.5 us where a lane has
+// two runs), and the longest sequence may have them all.  In a graph, us with the gradient, one kernel against two: 64
+// experts: 64 tokens 5.6, 9.0; 256 7.8, 9.1; 512 10.9, 9.4; 7 sequences of 1021 9.1, 10.8; 64 of 2048 7.0, 17.9.  256
+// experts, sigmoid: 64 tokens 8.0, 10.4; 256 17.5, 11.8; 7 sequences of 256 10.5, 13.4; 64 of 512 8.5, 22.5.
+bool few_tokens(const moe_balance_config& c) {
+  const int runs = c.n_routed <= 64 && c.n_routed % 4 == 0 ? 1 : 2;
+  const int64_t blocks = ceil_div(c.tokens, kPartWaves * (64 / lanes_of(c.n_routed)));
+  return blocks * runs <= std::min<int64_t>(2 * (int64_t)c.n_seqs + 2, 32) && c.n_seqs <= 4096;
+}
+
+template <typename TL, bool SOFTMAX>
+hipError_t few_t(const BalanceArgs& a, const BalanceOut& o, hipStream_t st) {
+  const size_t lds = (size_t)(kPartWaves * a.N + a.N + 4) * 4;
+  return with_lanes(a.N, [&](auto l, auto c, auto whole) {
+    return launch_kernel(balance_few_kernel<decltype(l)::value, decltype(c)::value, decltype(whole)::value, TL, SOFTMAX>,
+                         dim3((unsigned)a.S), dim3(kPartThreads), lds, st, a, o);
+  });
+}
+
 template <typename TL, bool SOFTMAX>
 hipError_t part_t(const BalanceArgs& a, int chunk, float* places, hipStream_t st) {
   const size_t lds = (size_t)(kPartWaves * a.N + a.N + 4) * 4;
@@ -559,7 +665,8 @@ hipError_t bwd_l(const BalanceArgs& a, const BalanceBwdArgs& w, bool softmax, bo
 }  // namespace
 
 size_t balance_workspace(const moe_balance_config& c) {
-  return c.tokens == 0 ? 0 : (size_t)(ceil_div(c.tokens, chunk_of(c)) + c.n_seqs) * place_words(c.n_routed) * 4;
+  if (c.tokens == 0 || few_tokens(c)) return 0;
+  return (size_t)(ceil_div(c.tokens, chunk_of(c)) + c.n_seqs) * place_words(c.n_routed) * 4;
 }
 
 hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
@@ -571,9 +678,13 @@ hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, 
     const int64_t blocks = std::min<int64_t>(ceil_div((int64_t)c.n_seqs * c.n_routed, 256), 1 << 16);
     return launch_kernel(balance_zero_kernel, dim3((unsigned)blocks), dim3(256), 0, st, o, c.n_seqs, c.n_routed);
   }
-  const int chunk = chunk_of(c);
   const bool f32 = c.logits_dtype == MOE_DTYPE_F32;
   hipError_t err;
+  if (few_tokens(c)) {
+    if (c.score == MOE_SCORE_SOFTMAX) return f32 ? few_t<float, true>(a, o, st) : few_t<uint16_t, true>(a, o, st);
+    return f32 ? few_t<float, false>(a, o, st) : few_t<uint16_t, false>(a, o, st);
+  }
+  const int chunk = chunk_of(c);
   if (c.score == MOE_SCORE_SOFTMAX)
     err = f32 ? part_t<float, true>(a, chunk, places, st) : part_t<uint16_t, true>(a, chunk, places, st);
   else

@@ -101,7 +101,7 @@ def test_balance_limits(kw, status):
 
 
 def test_balance_pointers_and_workspace():
-    c, n = balance(), ctypes.c_size_t(0)
+    c, n = balance(tokens=20000), ctypes.c_size_t(0)
     assert lib.moe_balance_workspace_size(None, ctypes.byref(n)) == INVALID
     assert lib.moe_balance_workspace_size(ctypes.byref(c), None) == INVALID
     assert lib.moe_balance_workspace_size(ctypes.byref(c), ctypes.byref(n)) == OK and n.value > 0

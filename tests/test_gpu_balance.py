@@ -112,6 +112,22 @@ def test_sequences(lengths, softmax):
             assert torch.allclose(alone[0][0], out[0][s], rtol=2.0 ** -15, atol=0)
 
 
+@pytest.mark.parametrize("softmax", [True, False])
+@pytest.mark.parametrize("N,dtype,lengths", [
+    (64, torch.float32, [256]), (64, torch.bfloat16, [257]), (61, torch.float32, [31]), (61, torch.bfloat16, [33]),
+    (256, torch.float32, [64]), (256, torch.bfloat16, [65]), (500, torch.bfloat16, [20, 0, 44, 1, 15]),
+    (64, torch.float32, [1, 63, 64, 65, 0, 0, 200, 7, 1] * 9), (60, torch.bfloat16, [0, 0, 1000, 1, 0, 47] * 3),
+    (256, torch.float32, [1, 31, 32, 33, 0, 0, 200, 7, 1] * 4), (130, torch.bfloat16, [5, 300, 1, 1, 0, 9] * 3),
+    (512, torch.float32, [1, 15, 16, 17, 0, 0, 100, 7, 1] * 4)])
+def test_one_kernel_and_two(N, dtype, lengths, softmax):
+    """Few tokens in one kernel and more in two: where the one ends, with sequences that begin anywhere in a block."""
+    starts = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]), dtype=torch.int32, device="cuda")
+    logits, idx = problem(int(starts[-1]), N, 5, N + len(lengths), dtype)
+    idx[::5] = -1
+    idx[1::9, 2] = N + 7
+    check(logits, idx, starts, softmax)
+
+
 def test_tokens_outside_the_sequences():
     logits, idx = problem(300, 40, 4, 3)
     starts = torch.tensor([20, 90, 90, 211], dtype=torch.int32, device="cuda")
