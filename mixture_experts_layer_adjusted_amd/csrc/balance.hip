@@ -384,12 +384,12 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
 }
 
 // One workgroup a sequence: its places added up in order, then the loss, which is a sum over all columns.  `quads` threads (a
-// power of two, 16 at least) take four columns each, groups of them every further place, eight loads at once.
+// power of two, 16 at least) take four columns each, groups of them every further place, four loads at once.
 __global__ void __launch_bounds__(kJoinThreads) balance_join_kernel(BalanceArgs a, int chunk, const float* __restrict__ places,
                                                                     BalanceOut o, int quads) {
   typedef float f32x4 __attribute__((ext_vector_type(4)));
   typedef int i32x4 __attribute__((ext_vector_type(4)));
-  constexpr int kBatch = 8, kMost = kJoinThreads / 64;
+  constexpr int kBatch = 4, kMost = kJoinThreads / 64;
   __shared__ f32x4 sums[kMost][64];
   __shared__ i32x4 counts[kMost][64];
   __shared__ int lens[kMost];
