@@ -389,7 +389,9 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
   constexpr int kWaves = FEW ? kFewWaves : kWavesOfTile, kThreads = 64 * kWaves;
   constexpr int kRuns = RT == 1 ? 1 : RT / 2;                       // runs of 32 ranks (RT == 1: 16 ranks twice)
   constexpr int kSteps = RT == 1 ? (PARTS + 1) / 2 : kRuns * PARTS;
-  constexpr int kBatch = 8, kShares = 8;   // slices loaded at once; threads at most that share one value's slices
+  // slices loaded at once (in a graph, us, 4 against 8: 1 row, 16 x 7168 -> 4096: 7.1, 7.3; 64 rows, 128 x 4096 -> 4096, side by
+  // side: 16.5, 15.1); threads at most that share one value's slices
+  constexpr int kBatch = RT <= 2 ? 4 : 8, kShares = 8;
   constexpr int kStride = kCols * kWaves;
   constexpr int kChunks = kCols * RT * 2;                           // 16-byte chunks of B in LDS, RT * 2 a column
   constexpr int kTurn = RT * 8 > 16 ? RT * 8 : 16;                  // chunks after which the next turn begins
