@@ -324,12 +324,13 @@ hipError_t with_lanes(const NormLanes& l, F f) {
   return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
 }
 
-// Workgroups of a backward pass, each with its own sums of the weight's gradient: half as many for few rows, whose sums cost
-// as much as the rows (7168 values, us with the second kernel, 128 workgroups against 256: 300 rows 11.7, 14.6; 512 rows
-// 13.1, 14.9; 700 rows 14.7, 14.8; 1024 rows 17.5, 17.0)
+// Workgroups of a backward pass, each with its own sums of the weight's gradient: half as many for few rows of a workgroup
+// each, whose sums cost as much as the rows (7168 values, us with the second kernel, 128 workgroups against 256: 300 rows
+// 11.7, 14.6; 512 rows 13.1, 14.9; 700 rows 14.7, 14.8; 1024 rows 17.5, 17.0; but rows of a wavefront, 1408 values in
+// fp32: 300 rows 6.1, 6.2; 600 rows 8.7, 7.3; 1021 rows 9.7, 9.0)
 int64_t norm_blocks(const NormLanes& l, int64_t rows) {
   const int64_t each = ceil_div(rows, l.per);
-  return std::min<int64_t>(each, each <= 5 * (kParts / 2) ? kParts / 2 : kParts);
+  return std::min<int64_t>(each, l.per == 1 && each <= 5 * (kParts / 2) ? kParts / 2 : kParts);
 }
 
 // Rows of 1025 to 2048 values, up to 4096 of them: two wavefronts a row, more loads at once (in a graph, us, two
