@@ -188,6 +188,62 @@ def test_masked_extreme_and_not_finite_logits(softmax):
     assert torch.isnan(out[0]).all() and torch.isnan(out[3]).any()
 
 
+@pytest.mark.parametrize("softmax", [True, False])
+def test_extreme_logits_in_a_large_batch(softmax):
+    """The same where the sums take two kernels, in a sequence of its own and among others."""
+    logits, idx = problem(900, 64, 6, 21)
+    logits[:, 7] = -float("inf")
+    logits[300] = -float("inf")
+    logits[301] = -200.0
+    logits[302] = torch.where(torch.arange(64, device="cuda") == 9, -3.4e38, -100.0)
+    logits[303:305] = 200.0
+    logits[899] = -3.4e38
+    for starts in (None, torch.tensor([0, 299, 302, 303, 900], dtype=torch.int32, device="cuda")):
+        check(logits, idx, starts, softmax)
+    logits[511] = float("nan")
+    idx[511] = -1
+    check_padding(logits, idx, softmax, 511)
+    idx[511] = idx[512]
+    out = forward(logits, idx, torch.tensor([0, 500, 600, 900], dtype=torch.int32, device="cuda"), softmax)
+    assert torch.isnan(out[0]).tolist() == [False, True, False] and torch.isfinite(out[3][0]).all()
+
+
+def test_two_graphs_share_a_workspace():
+    g = torch.Generator("cuda").manual_seed(4)
+    calls, ws = [], None
+    for T, N, K in ((5000, 64, 4), (3000, 200, 8)):
+        logits, idx = problem(T, N, K, T)
+        cfg = config(logits, idx, 1, True)
+        need = moe.moe_balance_workspace_size(cfg)
+        ws = torch.empty(max(need, 1 << 21), dtype=torch.uint8, device="cuda") if ws is None else ws
+        assert 0 < need <= ws.numel()
+        out = [torch.empty(1, device="cuda"), torch.empty(1, N, dtype=torch.int32, device="cuda"),
+               torch.empty(1, dtype=torch.int32, device="cuda"), torch.empty(1, N, device="cuda")]
+        forward(logits, idx, None, True)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_balance_loss(cfg, logits, idx, None, *out, ws)
+        calls.append((graph, logits, idx, out))
+    for k in range(6):
+        graph, logits, idx, out = calls[k % 2]
+        logits.copy_(torch.randn(logits.shape, device="cuda", generator=g))
+        want = forward(logits, idx, None, True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+def test_few_tokens_need_no_workspace():
+    logits, idx = problem(60, 64, 6, 22)
+    cfg = config(logits, idx, 1, True)
+    assert moe.moe_balance_workspace_size(cfg) == 0
+    out = [torch.empty(1, device="cuda"), torch.empty(1, 64, dtype=torch.int32, device="cuda"),
+           torch.empty(1, dtype=torch.int32, device="cuda")]
+    moe.moe_balance_loss(cfg, logits, idx, None, *out, None, None)
+    assert all(torch.equal(x, y) for x, y in zip(out, forward(logits, idx, None, True)))
+
+
 def check_padding(logits, idx, softmax, row):
     out = forward(logits, idx, None, softmax)
     keep = torch.arange(logits.shape[0], device="cuda") != row
