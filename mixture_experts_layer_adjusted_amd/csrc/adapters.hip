@@ -40,7 +40,9 @@ constexpr int kCols = 64;        // output columns of a wavefront at a time
 // rows 15.0, 15.4; two against four, 500 rows: 22.4, 22.8; side by side 30.4, 26.6).
 constexpr int kUnitRows = 1024, kUnitShare = 16;
 // Workgroups of a product, or so.  By adapters about as many as the registers let run at once (in a graph, us, 512 against
-// 1024: 64 rows, 32 adapters of rank 64, 7168 -> 4096: 15.0, 16.6; 500 rows 22.8, 24.5)
+// 1024: 64 rows, 32 adapters of rank 64, 7168 -> 4096: 15.0, 16.6; 500 rows 22.8, 24.5).  By tiles 2048, 1024 above rank 32
+// (rows of one adapter side by side, 1024 against 2048: 2000 rows of 8 adapters of rank 64, 4096 -> 4096 29.3, 35.2; 600 rows,
+// 2048 -> 7168 21.1, 20.1; 2000 rows of 4 of rank 128 47, 58; of rank 16, 7168 -> 4096: 8192 rows 71.5, 61.4)
 constexpr int kTileBlocks = 2048, kUnitBlocks = 512;
 // One launch in place of two up to so many rows and values of an adapter's A, which every workgroup then reads whole.
 // In a graph, us, one kernel against two: 1 row, 16 x 2048 -> 7168: 5.4, 7.1; 16 rows, 32 x 2048 -> 4096: 7.5, 7.7;
@@ -629,7 +631,8 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
   p.units = (int)std::min<int64_t>(s.rows, n);
   p.subs = p.form != kUnitForm || s.rows <= 4 * n ? 1 : s.rows <= 8 * n ? 2 : 4;
   const int64_t tiles = p.form == kUnitForm ? p.units * p.subs : std::max<int64_t>(1, ceil_div(s.rows, kRows));
-  const int64_t some = p.form == kUnitForm ? kUnitBlocks : kTileBlocks, run = kStep * kWaves;
+  const int64_t some = p.form == kUnitForm ? kUnitBlocks : p.tiles16 <= 2 ? kTileBlocks : kTileBlocks / 2;
+  const int64_t run = kStep * kWaves;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(some, tiles), ceil_div(s.in_cols, run)));
   p.per_split = (int)(ceil_div(ceil_div(s.in_cols, want), run) * run);
   p.splits = (int)ceil_div(s.in_cols, p.per_split);
