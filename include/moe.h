@@ -473,7 +473,8 @@ typedef struct moe_norm_shape {
   int64_t y_ld;         /* elements between rows of y and d_y; 0: cols (both multiples of 8) */
 } moe_norm_shape;
 
-/* Bytes of device workspace that moe_norm_backward needs for `shape` (moe_norm_forward needs none). */
+/* Bytes of device workspace that moe_norm_backward needs for `shape` with d_weight (0 for few rows; moe_norm_forward needs
+ * none). */
 moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
 
 /*   x         [rows, cols]

@@ -12,7 +12,8 @@
 // A row lies in the registers of one wavefront (up to 2048 values) or of one workgroup, eight neighbouring values a lane
 // and load, so that it is read once.  The order of its sums goes by its length alone: a row's results are the same bits in
 // every batch.  16 lanes hold a run of 128.  The weight's gradient: every thread sums its own columns over the
-// workgroup's rows, the workgroups' sums are joined in a fixed order by a second kernel.
+// workgroup's rows, the workgroups' sums are joined in a fixed order by a second kernel; for few rows, further workgroups
+// sum up columns in the same kernel.
 // Bound by memory: 16384 x 7168 in bf16, forward with y and codes 177 us for 1.06 GB (6.0 TB/s), backward 176 us for 0.94 GB
 // (5.3 TB/s) and 5 us for the join; 8192 x 7168 forward with codes alone 76 us for 0.41 GB (5.4 TB/s).  Few rows by latency:
 // one row of 7168 3.2 us, 77 of 2048 3.5 us.
@@ -150,10 +151,63 @@ struct NormBwdArgs {
   const void *d_y, *d_sum, *h;
   const float *weight, *rstd;
   void* d_x;
-  float* parts;   // [gridDim.x, cols], or null
+  float* parts;   // [workgroups, cols], or null
   int64_t rows, x_ld, y_ld;
   int cols;
+  float* d_weight;   // where workgroups 0 to column_blocks - 1 sum up columns in place of parts
+  int column_blocks;
 };
+
+// The weight's gradient of 64 bytes of neighbouring columns, for a batch of few rows: what the workgroups of the rows do
+// not wait for.  Four lanes a row; every thread sums its rows, then the threads of a wavefront, then the wavefronts.
+template <typename T>
+__device__ __forceinline__ void sum_columns(const NormBwdArgs& a, float (&place)[16][32]) {
+  constexpr int kVals = 16 / sizeof(T), kBatch = 8;   // rows loaded at once
+  struct __attribute__((aligned(16))) Raw { uint4 q; };
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6, step = waves * 16;
+  const int column = blockIdx.x * (4 * kVals) + (lane & 3) * kVals, at = min(column, a.cols - kVals);
+  const int rows = (int)a.rows;
+  const T *d_y = static_cast<const T*>(a.d_y) + at, *h = static_cast<const T*>(a.h) + at;
+  float dw[kVals];
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) dw[i] = 0.0f;
+  for (int r0 = wave * 16 + (lane >> 2); r0 < rows; r0 += step * kBatch) {
+    Raw g[kBatch], u[kBatch];
+    float rstd[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int64_t r = min(r0 + k * step, rows - 1);
+      g[k] = *reinterpret_cast<const Raw*>(d_y + r * a.y_ld);
+      u[k] = *reinterpret_cast<const Raw*>(h + r * a.x_ld);
+      rstd[k] = a.rstd[r];
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (r0 + k * step >= rows) break;
+      const uint32_t gw[4] = {g[k].q.x, g[k].q.y, g[k].q.z, g[k].q.w}, uw[4] = {u[k].q.x, u[k].q.y, u[k].q.z, u[k].q.w};
+#pragma unroll
+      for (int i = 0; i < kVals; ++i) {
+        auto value = [&](const uint32_t (&w)[4]) {
+          if constexpr (sizeof(T) == 4) return __uint_as_float(w[i]);
+          else return __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        };
+        dw[i] = fmaf(value(gw), value(uw) * rstd[k], dw[i]);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kVals; ++i) {
+#pragma unroll
+    for (int off = 4; off < 64; off *= 2) dw[i] += __shfl_xor(dw[i], off, 64);
+    if (lane < 4) place[wave][lane * kVals + i] = dw[i];
+  }
+  __syncthreads();
+  const int c = blockIdx.x * (4 * kVals) + threadIdx.x;
+  if (threadIdx.x >= 4 * kVals || c >= a.cols) return;
+  float sum = place[0][threadIdx.x];
+  for (int w = 1; w < waves; ++w) sum += place[w][threadIdx.x];
+  a.d_weight[c] = sum;
+}
 
 // kAhead: a workgroup goes through its rows with the next one's values on their way, which lets one workgroup a CU reach what
 // the memory gives (16384 x 7168, bf16: 169 us with 256 workgroups, 5.6 TB/s; 183 with 512; 230 with one row each).  Where
@@ -165,8 +219,14 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
   const int lanes = WAVE ? 64 : blockDim.x, lane = WAVE ? threadIdx.x & 63 : threadIdx.x;
   const int per = WAVE ? blockDim.x >> 6 : 1;
   const int first = WAVE ? threadIdx.x >> 6 : 0;
-  const int64_t step = (int64_t)gridDim.x * per;
+  const int64_t step = (int64_t)(gridDim.x - a.column_blocks) * per;
   const float n = (float)a.cols;
+  if ((int)blockIdx.x < a.column_blocks) {
+    __shared__ float columns[16][32];
+    sum_columns<T>(a, columns);
+    return;
+  }
+  const int64_t block = blockIdx.x - a.column_blocks;
   float dw[V][8];
   Raw8<float> w[V];
   Raw8<T> h[V], d_y[V], d_sum[V];
@@ -188,7 +248,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
       for (int j = 0; j < V; ++j) d_sum[j] = raw_at(static_cast<const T*>(a.d_sum) + r * a.x_ld + column(j));
     }
   };
-  int64_t r = (int64_t)blockIdx.x * per + first;
+  int64_t r = block * per + first;
   if (kAhead && r < a.rows) load(r);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
@@ -244,7 +304,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormB
     }
   }
   if (!a.parts) return;
-  float* mine = a.parts + (int64_t)blockIdx.x * a.cols;
+  float* mine = a.parts + block * a.cols;
   if constexpr (WAVE) {   // the four wavefronts' sums, in their order
     __shared__ float sums[4][V * 512];
 #pragma unroll
@@ -333,6 +393,14 @@ int64_t norm_blocks(const NormLanes& l, int64_t rows) {
   return std::min<int64_t>(each, l.per == 1 && each <= 5 * (kParts / 2) ? kParts / 2 : kParts);
 }
 
+// Up to so many rows and bytes of them, the weight's gradient is summed by columns in the kernel of the rows: one launch in
+// place of two, against reading dy and h twice.  In a graph, us, one against two: 1408 in fp32: 1 row 2.5, 4.7; 300 rows 4.5,
+// 6.1; 512 rows 6.9, 6.8; 1021 rows 11.8, 8.9.  7168 in bf16: 64 rows 4.8, 7.4; 384 rows 11.0, 10.7; in fp32 300 rows 13.7,
+// 13.8; 384 rows 17.8, 14.5.
+bool by_columns(const moe_norm_shape& s) {
+  return s.rows <= 384 && (int64_t)s.rows * s.cols * (s.dtype == MOE_DTYPE_F32 ? 4 : 2) <= (8 << 20);
+}
+
 // Rows of 1025 to 2048 values, up to 4096 of them: two wavefronts a row, more loads at once (in a graph, us, two
 // wavefronts against one: 1 x 2048 2.8, 3.5; 77 x 2048 3.1, 4.0; 4096 x 2048 11.0, 11.7; 65536 x 2048 166, 163)
 NormLanes forward_lanes_of(int cols, int64_t rows) {
@@ -360,7 +428,7 @@ hipError_t norm_backward_t(const NormLanes& l, const NormBwdArgs& a, unsigned gr
 
 size_t norm_workspace(const moe_norm_shape& s) {
   const NormLanes l = lanes_of(s.cols);
-  return (size_t)norm_blocks(l, s.rows) * s.cols * 4;
+  return by_columns(s) ? 0 : (size_t)norm_blocks(l, s.rows) * s.cols * 4;
 }
 
 hipError_t launch_norm_forward(const moe_norm_shape& s, const void* x, const void* residual, const float* weight, void* sum,
@@ -377,14 +445,18 @@ hipError_t launch_norm_backward(const moe_norm_shape& s, const void* d_y, const 
   if (s.rows == 0)
     return launch_kernel(norm_zero_kernel, dim3((unsigned)ceil_div(s.cols, 256)), dim3(256), 0, st, d_weight, s.cols);
   const NormLanes l = lanes_of(s.cols);
-  const unsigned grid = (unsigned)norm_blocks(l, s.rows);
-  const NormBwdArgs a{d_y, d_sum, h, weight, rstd, d_x, d_weight ? parts : nullptr, s.rows, s.x_ld ? s.x_ld : s.cols,
-                      s.y_ld ? s.y_ld : s.cols, s.cols};
+  const bool columns = by_columns(s);
+  const int elem = s.dtype == MOE_DTYPE_F32 ? 4 : 2;
+  const int column_blocks = columns && d_weight ? (int)ceil_div(s.cols * elem, 64) : 0;
+  const unsigned blocks = (unsigned)(columns ? ceil_div(s.rows, l.per) : norm_blocks(l, s.rows));
+  const NormBwdArgs a{d_y, d_sum, h, weight, rstd, d_x, d_weight && !columns ? parts : nullptr, s.rows,
+                      s.x_ld ? s.x_ld : s.cols, s.y_ld ? s.y_ld : s.cols, s.cols, d_weight, column_blocks};
+  const unsigned grid = blocks + column_blocks;
   const hipError_t err =
       s.dtype == MOE_DTYPE_F32 ? norm_backward_t<float>(l, a, grid, st) : norm_backward_t<uint16_t>(l, a, grid, st);
-  if (err != hipSuccess || !d_weight) return err;
+  if (err != hipSuccess || !d_weight || columns) return err;
   return launch_kernel(norm_join_kernel, dim3((unsigned)ceil_div(s.cols, 16)), dim3(1024), 0, st, parts,
-                       (int)grid, s.cols, d_weight);
+                       (int)blocks, s.cols, d_weight);
 }
 
 }  // namespace moe

@@ -64,7 +64,7 @@ def test_norm_pointers():
 
 
 def test_norm_backward_pointers_and_workspace():
-    s, n = moe.make_norm_shape(10, 256, 1, 1e-6), ctypes.c_size_t(0)
+    s, n = moe.make_norm_shape(1000, 256, 1, 1e-6), ctypes.c_size_t(0)
     assert lib.moe_norm_workspace_size(ctypes.byref(s), ctypes.byref(n)) == OK and n.value > 0
     b = lambda *a: lib.moe_norm_backward(ctypes.byref(s), *a, None)  # noqa: E731
     dy, ds, h, w, rs, dx, dw, ws = P[:8]

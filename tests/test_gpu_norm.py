@@ -111,6 +111,29 @@ def test_against_float64(rows, cols, stream, residual):
     assert (np.abs(np_(d_w) - ref_w) <= (2.0 ** -18 + depth(rows) * 2.0 ** -24) * size).all()
 
 
+@pytest.mark.parametrize("rows,cols,stream", [
+    (1, 8, "bf16"), (2, 8, "f32"), (3, 40, "bf16"), (384, 520, "f32"), (385, 520, "f32"), (383, 1032, "bf16"),
+    (384, 2056, "bf16"), (292, 7168, "f32"), (293, 7168, "f32"), (64, 32768, "f32"), (65, 32768, "f32"), (129, 32760, "bf16"),
+    (333, 24, "f32"), (100, 16384, "bf16")])
+def test_weight_gradient_by_columns_and_by_rows(rows, cols, stream):
+    """Few rows sum it up by columns in one kernel: both sides of where that ends.  Also rows whose d_y is zero."""
+    x, r, w, d_y, d_s = inputs(rows, cols, stream, rows + cols)
+    d_y[rows // 2] = 0
+    out = forward(x, r, w, stream)
+    d_x, d_w = backward(d_y, d_s, out["sum"], w, out["rstd"], stream)
+    u = np_(out["sum"]).astype(np.float64) * np_(out["rstd"]).astype(np.float64)[:, None]
+    terms = np_(d_y) * u
+    assert (np.abs(np_(d_w) - terms.sum(axis=0)) <= (2.0 ** -18 + depth(rows) * 2.0 ** -24) * np.abs(terms).sum(axis=0)).all()
+    alone, _ = backward(d_y, d_s, out["sum"], w, out["rstd"], stream, weight=False)
+    again, w2 = backward(d_y, d_s, out["sum"], w, out["rstd"], stream)
+    assert torch.equal(alone, d_x) and torch.equal(again, d_x) and torch.equal(w2, d_w)
+    in_place = d_s.clone()
+    shape = moe.make_norm_shape(rows, cols, TYPES[stream][1], EPS)
+    w3, ws = torch.empty_like(w), torch.empty(moe.moe_norm_workspace_size(shape), dtype=torch.uint8, device="cuda")
+    moe.moe_norm_backward(shape, d_y, in_place, out["sum"], w, out["rstd"], in_place, w3, ws)
+    assert torch.equal(in_place, d_x) and torch.equal(w3, d_w)
+
+
 def test_codes_are_the_quantisers():
     """fp32 y and codes of one call: the codes are those of the fp32 quotients; and with moe_quantize_act on values that
     bf16 holds (a weight of ones, rows whose rstd is a power of two)."""
