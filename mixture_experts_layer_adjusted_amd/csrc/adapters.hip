@@ -35,7 +35,9 @@ constexpr int kCols = 64;        // output columns of a wavefront at a time
 // workgroups whose adapter has no further rows come for nothing.  In a graph, us, by adapters against by tiles, rows of all
 // adapters mixed, then rows of one side by side, 7168 -> 4096: 32 adapters of rank 64: 64 rows 15.0, 31.0; 14.5, 15.7.
 // 140 rows 16.3, 32.3; 16.1, 21.9.  500 rows 22.8, 59; 26.6, 25.4.  32 of rank 16: 500 rows 16.8, 24.1; 18.5, 13.6.  8 of
-// rank 16: 64 rows 7.9, 11.1; 9.7, 8.6.  256 rows (past the share) 11.3, 13.7; 11.3, 10.2.  An adapter's rows are shared by
+// rank 16: 64 rows 7.9, 11.1; 9.7, 8.6.  256 rows (past the share) 11.3, 13.7; 11.3, 10.2.  Above rank 32 twice as many: 1000
+// rows of 32 of rank 64 31.7, 137; 55.9, 34.5; 500 rows of 16 of rank 128, 4096 -> 4096: 30.7, 51.5; 36.4, 25.4; 140 rows of 8
+// of rank 64, 2048 -> 7168: 13.1, 19.6; 15.4, 13.0.  An adapter's rows are shared by
 // more workgroups the more rows there are for each (one against two, 140 rows of 32 adapters of rank 64: 17.3, 16.3; 64
 // rows 15.0, 15.4; two against four, 500 rows: 22.4, 22.8; side by side 30.4, 26.6).
 constexpr int kUnitRows = 1024, kUnitShare = 16;
@@ -625,7 +627,8 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
   p.tiles16 = s.rank <= 16 ? 1 : s.rank <= 32 ? 2 : s.rank <= 64 ? 4 : 8;
   const int64_t n = s.n_adapters, x_ld = s.x_ld ? s.x_ld : s.in_cols;
   p.form = s.rows <= kFewRows && p.tiles16 <= 2 && (int64_t)s.rank * s.in_cols <= kFewValues ? kFewForm
-           : s.rows <= kUnitRows && s.rows <= kUnitShare * n && s.rows * x_ld < (int64_t(1) << 32)   // (32-bit offsets)
+           : s.rows <= kUnitRows && s.rows <= (p.tiles16 <= 2 ? 1 : 2) * kUnitShare * n &&
+                     s.rows * x_ld < (int64_t(1) << 32)   // (32-bit offsets)
                ? kUnitForm
                : kTileForm;
   p.units = (int)std::min<int64_t>(s.rows, n);
