@@ -384,8 +384,11 @@ struct RawFour<float> {
 // workgroup computes it whole, for its columns: for few rows and little of A that is less than a launch more).
 enum AdapterForm { kTileForm, kUnitForm, kFewForm };
 constexpr int kFewWaves = 8;
-// wavefronts a SIMD that the registers have to leave room for: three where the kernel would take a little more than that allows
-constexpr int out_waves(int rt, int form) { return form != kFewForm && (rt == 1 || (rt == 2 && form == kTileForm)) ? 3 : 1; }
+// wavefronts a SIMD that the registers have to leave room for: three where the kernel would take a little more than that
+// allows
+constexpr int out_waves(int rt, int form) {
+  return form != kFewForm && (rt == 1 || (rt == 2 && form == kTileForm)) ? 3 : 1;
+}
 template <int RT, int PARTS, typename T, int FORM>
 __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, out_waves(RT, FORM))
     adapters_out_kernel(AdapterArgs g) {

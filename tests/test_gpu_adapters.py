@@ -102,7 +102,8 @@ def test_many_rows_of_one_adapter_among_many(rows, r, out):
     (1024, 520, 136, 64, 16, False), (1023, 264, 328, 100, 32, True), (1025, 264, 72, 100, 32, False),
     (500, 1032, 520, 32, 64, True), (513, 264, 72, 32, 24, False), (700, 136, 264, 1200, 8, False),
     (1024, 72, 72, 1025, 24, True), (320, 264, 1096, 40, 128, True), (257, 2056, 264, 16, 16, False),
-    (128, 40, 2056, 8, 48, True), (256, 264, 520, 8, 64, True), (257, 264, 520, 8, 64, False), (600, 328, 264, 20, 128, True)])
+    (128, 40, 2056, 8, 48, True), (256, 264, 520, 8, 64, True), (257, 264, 520, 8, 64, False),
+    (600, 328, 264, 20, 128, True)])
 def test_decode_batches(rows, d_in, d_out, n, r, ranks, out):
     """Up to 1024 rows and 16 an adapter (32 above rank 32) go by adapters: one, two and four workgroups that share an adapter's rows, fewer
     rows than adapters, one adapter with most rows; rows without one copied, or left where they are."""
