@@ -636,7 +636,8 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
                : kTileForm;
   p.units = (int)std::min<int64_t>(s.rows, n);
   p.subs = p.form != kUnitForm || s.rows <= 4 * n ? 1 : s.rows <= 8 * n ? 2 : 4;
-  const int64_t tiles = p.form == kUnitForm ? p.units * p.subs : std::max<int64_t>(1, ceil_div(s.rows, kRows));
+  // (at least one: the size query may be asked for no rows)
+  const int64_t tiles = std::max<int64_t>(1, p.form == kUnitForm ? p.units * p.subs : ceil_div(s.rows, kRows));
   const int64_t some = p.form == kUnitForm ? kUnitBlocks : p.tiles16 <= 2 ? kTileBlocks : kTileBlocks / 2;
   const int64_t run = kStep * kWaves;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(some, tiles), ceil_div(s.in_cols, run)));

@@ -1,0 +1,30 @@
+"""Host-side size queries of the norm, the balance loss and the adapters at their limits."""
+import ctypes
+
+import pytest
+
+import mixture_experts_layer_adjusted_amd as moe
+from mixture_experts_layer_adjusted_amd import binding
+
+lib = binding.raw_lib()
+
+
+@pytest.mark.parametrize("rank", [8, 16, 24, 32, 48, 64, 128])
+@pytest.mark.parametrize("in_cols", [8, 256, 7168, 1 << 20])
+@pytest.mark.parametrize("n", [1, 8, 5000])
+def test_adapters_of_no_rows(n, in_cols, rank):
+    """A batch that has run empty: no bytes, and the call returns, whatever the adapters' sizes are."""
+    shape = moe.make_adapter_shape(0, in_cols, 4096, n, rank, moe.MOE_DTYPE_BF16)
+    assert moe.moe_adapters_workspace_size(shape) == 0
+    assert lib.moe_adapters(ctypes.byref(shape), *[None] * 9, 0, None) == 0
+
+
+@pytest.mark.parametrize("cols", [8, 2048, 7168, 32768])
+def test_norm_of_no_rows(cols):
+    assert moe.moe_norm_workspace_size(moe.make_norm_shape(0, cols, moe.MOE_DTYPE_BF16, 1e-6)) == 0
+
+
+@pytest.mark.parametrize("n,seqs", [(1, 1), (64, 7), (512, 1 << 24)])
+def test_balance_of_no_tokens(n, seqs):
+    cfg = moe.make_balance_config(0, n, 1, moe.MOE_DTYPE_F32, moe.MOE_SCORE_SOFTMAX, seqs)
+    assert moe.moe_balance_workspace_size(cfg) == 0
