@@ -342,15 +342,20 @@ __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
   }
 }
 
-// the next bf16 part of v (and what it leaves); nothing is left of what is not finite
+// the next bf16 part of v (and what it leaves).  A finite value's parts are finite, also above 3.396e38, which rounds to
+// infinity: its first part is bf16's largest.  Nothing is left of what is not finite.
 __device__ __forceinline__ bf16x8 part_of(float (&v)[8]) {
+  constexpr float kMost = 0x1.fep127f;
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
-    const float lo = __uint_as_float(w[i] << 16), hi = __uint_as_float(w[i] & 0xFFFF0000u);
-    v[2 * i] = fabsf(lo) < __builtin_inff() ? v[2 * i] - lo : 0.0f;
-    v[2 * i + 1] = fabsf(hi) < __builtin_inff() ? v[2 * i + 1] - hi : 0.0f;
+    const bool some[2] = {fabsf(v[2 * i]) < __builtin_inff(), fabsf(v[2 * i + 1]) < __builtin_inff()};
+    float c[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) c[h] = some[h] ? __builtin_amdgcn_fmed3f(v[2 * i + h], -kMost, kMost) : v[2 * i + h];
+    w[i] = bf16_pair(c[0], c[1]);
+    v[2 * i] = some[0] ? v[2 * i] - __uint_as_float(w[i] << 16) : 0.0f;
+    v[2 * i + 1] = some[1] ? v[2 * i + 1] - __uint_as_float(w[i] & 0xFFFF0000u) : 0.0f;
   }
   return __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
 }
