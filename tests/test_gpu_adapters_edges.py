@@ -53,3 +53,23 @@ def test_low_rank_values_near_the_largest(rows, d_in, d_out, n, r, out):
     p["b"][:] = (torch.rand(p["b"].shape, device="cuda") + 0.5).bfloat16() * 2.0 ** -100
     p["scale"][:] = 1
     check_with_infinities(p, run(p))
+
+
+@pytest.mark.parametrize("out", OUT)
+@pytest.mark.parametrize("rows,d_in,d_out,n,r", FORMS)
+def test_an_infinite_weight_makes_an_infinity(rows, d_in, d_out, n, r, out):
+    """B's infinities meet low-rank values that bf16 holds (their remainder is zero) and others (their remainder has either
+    sign): the value's own sign decides, once."""
+    p = problem(rows, d_in, d_out, n, r, rows + r, out)
+    p["which"][:] = (torch.arange(rows, device="cuda") % (n + 1)) - 1
+    p["a"][:, 0] = 0
+    p["a"][:, 0, 0] = 1                                # the first low-rank value is x's first
+    p["x"][:, 0] = torch.where(torch.arange(rows, device="cuda") % 3 == 0, -1.5, 2.0).bfloat16()
+    p["b"][:, 3, 0] = float("inf")
+    p["b"][:, 9, 0] = -float("inf")
+    p["b"][:, 17, r // 2] = float("inf")               # (that value is a sum: nonzero)
+    p["b"][:, 40, 0] = float("inf")
+    p["b"][:, 40, r - 1] = float("nan")
+    if n > 1:
+        p["b"][1, 50] = torch.where(torch.arange(r, device="cuda") % 2 == 0, float("inf"), -float("inf")).bfloat16()
+    check_with_infinities(p, run(p))
