@@ -575,7 +575,7 @@ typedef struct moe_adapter_shape {
 moe_status moe_adapters_workspace_size(const moe_adapter_shape* shape, size_t* bytes);
 
 /*   x            [T, in]     bf16
- *   row_adapter  [T]         int32; outside [0, n): the row has no adapter and out is base
+ *   row_adapter  [T]         int32; outside [0, n): the row has no adapter and out is base, bit for bit
  *   a            [n, r, in]  bf16;   b [n, out, r] bf16
  *   scale        [n]         fp32
  *   ranks        [n]         int32, 0 to r (others: the nearer of the two), what a and b hold from

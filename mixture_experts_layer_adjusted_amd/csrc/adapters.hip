@@ -607,10 +607,10 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
         if (4 * quad + i >= here || c >= g.outs) continue;
         float v[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k)   // (a row without an adapter keeps its base to the sign of a zero)
-          v[k] = theirs[i] >= 0 ? o.base[i].at(k) + kept[k][i] : o.base[i].at(k);
+        for (int k = 0; k < 4; ++k) v[k] = o.base[i].at(k) + kept[k][i];
         RawFour<T> p;
         p.set(v);
+        if (theirs[i] < 0) p = o.base[i];   // (a row without an adapter keeps its base's bits)
         *reinterpret_cast<RawFour<T>*>(static_cast<T*>(g.out) + out_row[i] * g.out_ld + c) = p;
       }
     };

@@ -73,3 +73,24 @@ def test_an_infinite_weight_makes_an_infinity(rows, d_in, d_out, n, r, out):
     if n > 1:
         p["b"][1, 50] = torch.where(torch.arange(r, device="cuda") % 2 == 0, float("inf"), -float("inf")).bfloat16()
     check_with_infinities(p, run(p))
+
+
+@pytest.mark.parametrize("out", OUT)
+@pytest.mark.parametrize("rows,d_in,d_out,n,r", FORMS)
+def test_rows_without_an_adapter_keep_their_bits(rows, d_in, d_out, n, r, out):
+    """Whatever they hold: signalling NaN, payloads, the zeros' signs, subnormals."""
+    p = problem(rows, d_in, d_out, n, r, rows + r, out)
+    p["which"][::2] = -1
+    p["which"][1::8] = n
+    bits = torch.int16 if out == torch.bfloat16 else torch.int32
+    odd = [0x7F81, 0xFFA5, 0x7FC1, 0x8000, 0x0001, 0xFF80] if out == torch.bfloat16 else \
+        [0x7F800001, 0xFFA00005, 0x7FC12345, 0x80000000, 0x00000001, 0xFF800000]
+    wrap = 1 << (16 if out == torch.bfloat16 else 32)
+    values = torch.tensor([v - wrap if v >= wrap // 2 else v for v in odd], dtype=bits, device="cuda")
+    none = (p["which"] < 0) | (p["which"] >= n)
+    held = p["base"].view(bits)
+    held[none] = values[torch.randint(0, 6, (int(none.sum()), d_out), device="cuda")]
+    assert torch.equal(run(p).view(bits)[none], held[none])
+    in_place = p["base"].clone()
+    run({**p, "own": in_place}, base="own", into=in_place)
+    assert torch.equal(in_place.view(bits)[none], held[none])
