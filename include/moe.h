@@ -571,7 +571,8 @@ typedef struct moe_adapter_shape {
   int64_t x_ld, base_ld, out_ld;   /* elements between rows; 0: dense; multiples of 8, x_ld below 2^24 */
 } moe_adapter_shape;
 
-/* Bytes of device workspace that moe_adapters needs for `shape`. */
+/* Bytes of device workspace that moe_adapters needs for `shape`, or for one that differs from it in having fewer rows: a buffer
+ * of the largest batch's size serves every smaller one. */
 moe_status moe_adapters_workspace_size(const moe_adapter_shape* shape, size_t* bytes);
 
 /*   x            [T, in]     bf16

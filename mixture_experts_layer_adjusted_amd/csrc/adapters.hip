@@ -716,9 +716,14 @@ hipError_t run_t(const AdapterArgs& g, AdapterForm form, int out_dtype, hipStrea
 
 }  // namespace
 
+// What any batch of up to so many rows needs (the slices are fewer the more rows there are, and end unevenly): a plan's
+// slices are fewer than some / tiles + 1, and no more than the runs of 256 values.  With kRows rows a tile, or at most that many
+// for each workgroup by adapters and slice, slices * rows <= kRows * some + rows.
 size_t adapters_workspace(const moe_adapter_shape& s) {
   const AdapterPlan p = plan_of(s);
-  return p.form == kFewForm ? 0 : (size_t)p.splits * s.rows * p.tiles16 * 16 * 4;
+  if (p.form == kFewForm) return 0;
+  const int64_t most = kRows * (p.tiles16 <= 2 ? kTileBlocks : kTileBlocks / 2) + s.rows;
+  return (size_t)std::min(s.rows * ceil_div(s.in_cols, kStep * kWaves), most) * p.tiles16 * 16 * 4;
 }
 
 hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int32_t* row_adapter, const void* a, const void* b,

@@ -28,3 +28,15 @@ def test_norm_of_no_rows(cols):
 def test_balance_of_no_tokens(n, seqs):
     cfg = moe.make_balance_config(0, n, 1, moe.MOE_DTYPE_F32, moe.MOE_SCORE_SOFTMAX, seqs)
     assert moe.moe_balance_workspace_size(cfg) == 0
+
+
+BATCHES = [*range(0, 1200), *range(1200, 9000, 7), *range(9000, 200000, 997)]
+
+
+@pytest.mark.parametrize("n,rank,in_cols", [(8, 16, 7168), (32, 64, 7168), (64, 32, 2048), (4, 128, 4096), (1, 8, 2048),
+                                            (300, 24, 1000), (1, 128, 8)])
+def test_a_smaller_batch_of_adapters_needs_no_more(n, rank, in_cols):
+    """A server sizes its buffer for its largest batch."""
+    sizes = [moe.moe_adapters_workspace_size(moe.make_adapter_shape(t, in_cols, 4096, n, rank, moe.MOE_DTYPE_BF16))
+             for t in BATCHES]
+    assert sizes == sorted(sizes) and sizes[0] == 0 and sizes[-1] > 0
