@@ -474,7 +474,7 @@ typedef struct moe_norm_shape {
 } moe_norm_shape;
 
 /* Bytes of device workspace that moe_norm_backward needs for `shape` with d_weight (0 for few rows; moe_norm_forward needs
- * none). */
+ * none), or for one that differs from it in having fewer rows. */
 moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
 
 /*   x         [rows, cols]
@@ -523,7 +523,8 @@ typedef struct moe_balance_config {
   int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
 } moe_balance_config;
 
-/* Bytes of device workspace that moe_balance_loss needs for `config` (0 where one kernel does all). */
+/* Bytes of device workspace that moe_balance_loss needs for `config` (0 for few tokens), or for one that differs from it in
+ * having fewer tokens or sequences. */
 moe_status moe_balance_workspace_size(const moe_balance_config* config, size_t* bytes);
 
 /*   logits      [T, N]  fp32 or bf16 (an expert at -inf has p = 0)

@@ -664,10 +664,17 @@ hipError_t bwd_l(const BalanceArgs& a, const BalanceBwdArgs& w, bool softmax, bo
 
 }  // namespace
 
+// What any batch of up to so many tokens and sequences needs: chunks of whole blocks, kPlaces of them at most, and a place more
+// for each sequence.  (None where one kernel does all, for these sequences and for a single one.)
 size_t balance_workspace(const moe_balance_config& c) {
-  if (c.tokens == 0 || few_tokens(c)) return 0;
-  return (size_t)(ceil_div(c.tokens, chunk_of(c)) + c.n_seqs) * place_words(c.n_routed) * 4;
+  moe_balance_config one = c;
+  one.n_seqs = 1;
+  if (c.tokens == 0 || (few_tokens(c) && few_tokens(one))) return 0;
+  const int64_t blocks = ceil_div(c.tokens, kPartWaves * (64 / lanes_of(c.n_routed)));
+  return (size_t)(std::min<int64_t>(blocks, kPlaces) + c.n_seqs) * place_words(c.n_routed) * 4;
 }
+
+bool balance_in_one_kernel(const moe_balance_config& c) { return c.tokens == 0 || few_tokens(c); }
 
 hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
                                float* loss, int32_t* counts, int32_t* tokens, float* prob_sum, float* places,

@@ -1140,7 +1140,7 @@ moe_status moe_balance_loss(const moe_balance_config* config, const void* logits
   if (rc != MOE_OK) return rc;
   if (!loss || !counts || !seq_tokens || (!seq_start && config->n_seqs != 1)) return MOE_ERR_INVALID_ARG;
   if (config->tokens > 0 && (!logits || !topk_idx)) return MOE_ERR_INVALID_ARG;
-  const size_t need = balance_workspace(*config);
+  const size_t need = balance_in_one_kernel(*config) ? 0 : balance_workspace(*config);
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   if (need > 0 && (!workspace || !aligned16(workspace))) return MOE_ERR_INVALID_ARG;
   const void* in[] = {logits, topk_idx, seq_start};

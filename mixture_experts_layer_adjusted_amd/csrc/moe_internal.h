@@ -264,6 +264,7 @@ hipError_t launch_norm_backward(const moe_norm_shape& s, const void* d_y, const 
 
 // balance loss from logits (balance.hip); places: the workspace; prob_sum may be null
 size_t balance_workspace(const moe_balance_config& c);
+bool balance_in_one_kernel(const moe_balance_config& c);   // which takes no workspace
 hipError_t launch_balance_loss(const moe_balance_config& c, const void* logits, const int32_t* idx, const int32_t* start,
                                float* loss, int32_t* counts, int32_t* tokens, float* prob_sum, float* places,
                                hipStream_t st);
