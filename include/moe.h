@@ -489,7 +489,7 @@ moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
  *   rstd      [rows] fp32 out: 1 / sqrt(mean(h^2) + eps), for moe_norm_backward; may be NULL
  * Squares and sums are fp32: a row whose sum of squares passes 3.4e38 has rstd 0, and a row of zeros
  * under eps = 0 is NaN.  A row's results do not depend on the other rows.  No buffer is another's, but for sum as above;
- * x_ld and y_ld are multiples of 8, and all pointers but rstd and scales multiples of 16.
+ * x_ld and y_ld are multiples of 8, and all pointers multiples of 16 (scales, rstd and d_weight: of 4).
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, a negative size, ld < cols, buffers in
  * place of one another), MOE_ERR_UNSUPPORTED (other limits). */
 moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const void* residual, const float* weight,

@@ -280,6 +280,10 @@ template <typename... P>
 static bool aligned16(P... p) {
   return ((reinterpret_cast<uintptr_t>(p) | ...) & 15) == 0;
 }
+template <typename... P>
+static bool aligned4(P... p) {
+  return ((reinterpret_cast<uintptr_t>(p) | ...) & 3) == 0;
+}
 
 extern "C" {
 
@@ -1078,7 +1082,7 @@ moe_status moe_norm_forward(const moe_norm_shape* shape, const void* x, const vo
   if (codes && shape->cols % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if (shape->rows == 0) return MOE_OK;
   if (!x || !weight || (!y && !codes) || !codes != !scales || (sum && !residual)) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(x, residual, weight, sum, y, codes)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x, residual, weight, sum, y, codes) || !aligned4(scales, rstd)) return MOE_ERR_INVALID_ARG;
   const void* in[] = {x, residual, weight, sum};
   const void* out[] = {y, codes, scales, rstd};
   for (int i = 0; i < 4; ++i) {
@@ -1096,11 +1100,12 @@ moe_status moe_norm_backward(const moe_norm_shape* shape, const void* d_y, const
                              size_t workspace_bytes, hipStream_t stream) {
   moe_status rc = check_norm(shape);
   if (rc != MOE_OK) return rc;
+  if (shape->rows == 0 && !aligned4(d_weight)) return MOE_ERR_INVALID_ARG;
   if (shape->rows == 0) return d_weight ? hip_status(launch_norm_backward(*shape, d_y, d_sum, h, weight, rstd, d_x, d_weight,
                                                                           nullptr, stream))
                                         : MOE_OK;
   if (!d_y || !h || !weight || !rstd || !d_x) return MOE_ERR_INVALID_ARG;
-  if (!aligned16(d_y, d_sum, h, weight, d_x, workspace)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(d_y, d_sum, h, weight, d_x, workspace) || !aligned4(rstd, d_weight)) return MOE_ERR_INVALID_ARG;
   for (const void* p : {d_y, h, static_cast<const void*>(weight), static_cast<const void*>(rstd)})
     if (d_x == p || d_weight == p || (workspace && workspace == p)) return MOE_ERR_INVALID_ARG;
   if (d_weight && (d_weight == d_x || d_weight == d_sum)) return MOE_ERR_INVALID_ARG;
