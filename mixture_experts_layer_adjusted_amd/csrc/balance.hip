@@ -285,19 +285,22 @@ __global__ void __launch_bounds__(kPartThreads) balance_few_kernel(BalanceArgs a
   o.loss[s] = balance_of(a, dot, len);
 }
 
-// L lanes a token.  chunk: tokens of a workgroup, in blocks that lie in registers together
+// L lanes a token.  chunk: tokens of a workgroup, in blocks that lie in registers together.  After kHeld blocks a lane's sums go
+// into second ones: thousands of fp32 additions one after another may all round the same way (2^26 tokens of 64 experts, all
+// alike, 4096 additions: 2^-14 of the sum; 2^-19 with these).  Chunks of up to kHeld blocks (2^20 tokens at 64 experts) do not.
 template <int L, int C, bool WHOLE, typename TL, bool SOFTMAX>
 __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs a, int chunk, float* __restrict__ places) {
   extern __shared__ float lds[];   // [kPartWaves][N] sums, then int [N] counts, int [1] tokens
-  constexpr int kTokens = 64 / L, kBlock = kPartWaves * kTokens;
+  constexpr int kTokens = 64 / L, kBlock = kPartWaves * kTokens, kHeld = 64;
   const int lane = threadIdx.x & (L - 1), slot = (threadIdx.x & 63) / L, wave = threadIdx.x >> 6;
   const int64_t begin = (int64_t)blockIdx.x * chunk, end = begin + chunk < a.T ? begin + chunk : a.T;
   int* counts = reinterpret_cast<int*>(lds + kPartWaves * a.N);
-  float total[C][4];
+  float total[C][4], before[C][4];
+  int held = 0;   // blocks whose sums are in total
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) total[c][j] = 0.0f;
+    for (int j = 0; j < 4; ++j) total[c][j] = before[c][j] = 0.0f;
   int seq = -1;   // the sequence of what has been summed so far
   // writes the sums of sequence `seq` and begins anew
   auto leave = [&]() {
@@ -306,9 +309,9 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = 4 * (c * L + lane) + j;
-        const float v = slots_sum<L>(total[c][j]);
+        const float v = slots_sum<L>(before[c][j] + total[c][j]);
         if (slot == 0 && i < a.N) lds[wave * a.N + i] = v;
-        total[c][j] = 0.0f;
+        total[c][j] = before[c][j] = 0.0f;
       }
     __syncthreads();
     float* place = places + ((int64_t)blockIdx.x + seq) * place_words(a.N);
@@ -375,6 +378,16 @@ __global__ void __launch_bounds__(kPartThreads) balance_part_kernel(BalanceArgs 
         if (lane == 0) atomicAdd(&counts[a.N], 1);
       }
       t0 = t1;
+    }
+    if (++held == kHeld) {
+      held = 0;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          before[c][j] += total[c][j];
+          total[c][j] = 0.0f;
+        }
     }
   }
   if (seq >= 0) {
