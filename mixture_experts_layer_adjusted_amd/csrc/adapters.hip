@@ -11,7 +11,7 @@
 // 16 neighbouring rows form a tile.  The rows of a tile may have different adapters: for each that occurs the whole tile is
 // multiplied and the rows that have it keep the result, so every adapter in use is read once for a tile and rows need
 // no sorting.  Rows of other adapters are computed and dropped, never added as zeros: an infinity or NaN stays in its row.
-// Few rows of many adapters (a decode batch) go by adapters instead.
+// Few rows of many adapters (a decode batch) go by adapters instead: a workgroup finds 16 rows of one.
 //
 // Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6
 // for the second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
@@ -31,19 +31,18 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves, kWavesOfTile = kWaves;
 constexpr int kRows = 16;        // rows of a tile, or of an adapter at a time
 constexpr int kStep = 64;        // values of a wavefront's step along the first product's contraction
 constexpr int kCols = 64;        // output columns of a wavefront at a time
-// Workgroups go by adapters up to so many rows (each looks through all of them), and rows for each adapter there is: they
-// read an adapter once for 16 of its rows, a tile of neighbouring rows reads all of its adapters one after the other; but
-// workgroups whose adapter has no further rows come for nothing.  In a graph, us, by adapters against by tiles, rows of all
-// adapters mixed, then rows of one side by side, 7168 -> 4096: 32 adapters of rank 64: 64 rows 15.0, 31.0; 14.5, 15.7.
-// 140 rows 16.3, 32.3; 16.1, 21.9.  500 rows 22.8, 59; 26.6, 25.4.  32 of rank 16: 500 rows 16.8, 24.1; 18.5, 13.6.  8 of
-// rank 16: 64 rows 7.9, 11.1; 9.7, 8.6.  256 rows (past the share) 11.3, 13.7; 11.3, 10.2.  Above rank 32 twice as many: 1000
-// rows of 32 of rank 64 31.7, 137; 55.9, 34.5; 500 rows of 16 of rank 128, 4096 -> 4096: 30.7, 51.5; 36.4, 25.4; 140 rows of 8
-// of rank 64, 2048 -> 7168: 13.1, 19.6; 15.4, 13.0.  An adapter's rows are shared by
-// more workgroups the more rows there are for each (one against two, 140 rows of 32 adapters of rank 64: 17.3, 16.3; 64
-// rows 15.0, 15.4; two against four, 500 rows: 22.4, 22.8; side by side 30.4, 26.6).
+// Workgroups go by adapters (16 rows of one each) up to so many rows, which each of them looks through, and rows for each adapter
+// there is: they read an adapter once for 16 of its rows, a tile of neighbouring rows reads all of its adapters one after the
+// other.  In a graph, us, by adapters against by tiles, rows of all adapters mixed, then side by side, then all rows on one
+// adapter: 32 adapters of rank 64, 7168 -> 4096: 64 rows 15.0, 31.2; 14.5, 22.6; 12.4, 9.9.  500 rows 21.7, 60; 22.4, 25.6; 16.8,
+// 16.5.  1000 rows 30, 138; 31, 34; 24.1, 22.5.  256 of rank 16, 2048 -> 4096: 256 rows 16.0, 22.6; 16.5, 21.2; 15.3, 6.9 (the
+// largest loss found); 1000 rows 19.6, 28.3; 19.7, 19.7; 17.6, 10.9.  8 of rank 16, 7168 -> 4096: 128 rows 10.1, 13.4; 10.2, 9.3;
+// 9.8, 7.3; above 16 rows an adapter (32 above rank 32) tiles are at least as good side by side and hold few adapters each.  (A
+// workgroup for each adapter and all of its rows: 269 with all of 1000 rows on one of 64 adapters of rank 16, 742 on one of 256.)
 constexpr int kUnitRows = 1024, kUnitShare = 16;
-// Workgroups of a product, or so.  By adapters about as many as the registers let run at once (in a graph, us, 512 against
-// 1024: 64 rows, 32 adapters of rank 64, 7168 -> 4096: 15.0, 16.6; 500 rows 22.8, 24.5).  By tiles 2048, 1024 above rank 32
+// Workgroups of a product, or so.  By adapters about as many as the registers let run at once (in a graph, us, 256, 512, 1024,
+// mixed: 64 rows, 32 adapters of rank 64, 7168 -> 4096: 15.7, 15.0, 16.2; 500 rows 22.6, 21.7, 24.6; 256 rows, 256 of rank 16,
+// 2048 -> 4096: 20.1, 15.9, 15.1; 1000 rows 23.4, 19.6, 22.6).  By tiles 2048, 1024 above rank 32
 // (rows of one adapter side by side, 1024 against 2048: 2000 rows of 8 adapters of rank 64, 4096 -> 4096 29.3, 35.2; 600 rows,
 // 2048 -> 7168 21.1, 20.1; 2000 rows of 4 of rank 128 47, 58; of rank 16, 7168 -> 4096: 8192 rows 71.5, 61.4)
 constexpr int kTileBlocks = 2048, kUnitBlocks = 512;
@@ -61,11 +60,12 @@ struct AdapterArgs {
   const void* base;
   void* out;
   float* low;                    // [splits, rows, RT * 16]
+  int2* found;                   // by adapters: [units, 16] rows and adapters, row -1: none
   int64_t rows, x_ld, base_ld, out_ld;
   int in, outs, n, r;
   int splits, per_split;         // slices of the first product, values of each
   int blocks, per_block;         // workgroups of a tile in the second product, columns of each
-  int units, subs;               // by adapters: their number, workgroups that share an adapter's rows
+  int units;                     // by adapters: groups of rows at most, or adapters (or rows) for few rows
 };
 
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
@@ -93,46 +93,130 @@ __device__ __forceinline__ void for_adapters(int mine, F f) {
   }
 }
 
-// The rows of a workgroup that goes by adapters.  Its unit is an adapter or, with fewer rows than adapters, a row, which
-// stands for its adapter if it is the first to have it.  16 rows at a time: every wavefront finds
-// them by itself, a ballot for each 64 rows and a permutation that brings those of the adapter to the lanes in front.
+// The rows of a workgroup that goes by adapters: up to 16 of one adapter, as every wavefront has them.
 struct UnitRows {
-  int adapter;   // -1: none
-  int count;     // 0 to 16
-  int row;       // lane i < count: the i-th
+  int count;          // 0 to 16
+  int row, adapter;   // lane i < count: the i-th
 };
 __device__ __forceinline__ int bits_below(uint64_t m) {
   return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
 }
-__device__ __forceinline__ UnitRows unit_rows(const AdapterArgs& g, int unit, int group) {
-  constexpr int kBatch = 4;   // runs of 64 rows loaded at once
-  const int lane = threadIdx.x & 63, from = group * kRows, rows = (int)g.rows;
-  const bool leads = g.units < g.n;
-  const int own = leads ? g.row_adapter[unit] : unit;   // (on its way with the first rows)
-  UnitRows u{-1, 0, 0};
-  int seen = 0;
-  for (int r0 = 0; r0 < rows && seen < from + kRows; r0 += 64 * kBatch) {
-    int e[kBatch];
+// Rows by adapters are cut into groups of 16, in their order.  Up to kScanRows rows, a unit is first an adapter (with fewer
+// rows than adapters: a row, which stands for its adapter if it is the first to have it) and its first 16 rows, which every
+// wavefront finds by itself, a ballot for each 64 rows and a permutation that brings those of the adapter to the lanes in
+// front; then a number among the further groups.  Beyond, a unit is a number among all groups.  (In a graph, us, against numbers
+// among all groups from the first row on, mixed: 64 rows of 64 adapters of rank 16, 7168 -> 4096: 10.6, 12.0; 140 rows of 32 of
+// rank 64 16.5, 17.8; 256 rows of 64 of rank 16 14.1, 14.3.)
+constexpr int kScanRows = 256;
+__host__ __device__ inline int first_units(int64_t rows, int n) { return rows < n ? (int)rows : n; }
+__device__ __forceinline__ UnitRows first_rows(const AdapterArgs& g, int unit) {
+  const int lane = threadIdx.x & 63, rows = (int)g.rows;
+  const bool leads = rows < g.n;
+  const int own = leads ? g.row_adapter[unit] : unit;   // (on its way with the rows)
+  int e[kScanRows / 64];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) e[k] = g.row_adapter[min(r0 + 64 * k + lane, rows - 1)];
-    if (own < 0 || own >= g.n) return u;
-    u.adapter = own;
+  for (int k = 0; k < kScanRows / 64; ++k) e[k] = g.row_adapter[min(64 * k + lane, rows - 1)];
+  UnitRows u{0, 0, own};
+  if (own < 0 || own >= g.n) return u;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int r = r0 + 64 * k + lane;
-      if (r0 + 64 * k >= rows) break;
-      const bool has = r < rows && e[k] == u.adapter;
-      const uint64_t m = __ballot(has);
-      if (m == 0) continue;
-      if (leads && seen == 0 && r0 + 64 * k + __builtin_ctzll(m) != unit) return u;
-      const int begin = seen - from, at = begin + bits_below(m);
-      const int row = __builtin_amdgcn_ds_permute(4 * (has && at >= 0 && at < kRows ? at : kRows), r);
-      seen += __popcll(m);
-      if (lane >= begin && lane < seen - from) u.row = row;
-    }
+  for (int k = 0; k < kScanRows / 64; ++k) {
+    const int r = 64 * k + lane;
+    if (64 * k >= rows || u.count >= kRows) break;
+    const bool has = r < rows && e[k] == own;
+    const uint64_t m = __ballot(has);
+    if (m == 0) continue;
+    if (leads && u.count == 0 && 64 * k + __builtin_ctzll(m) != unit) return u;
+    const int at = u.count + bits_below(m), more = __builtin_amdgcn_ds_permute(4 * (has && at < kRows ? at : kRows), r);
+    if (lane >= u.count) u.row = more;
+    u.count += __popcll(m);
   }
-  u.count = max(0, min(kRows, seen - from));
+  u.count = min(kRows, u.count);
   return u;
+}
+
+// A unit that is a group's number, of up to kUnitRows rows; further: among those behind an adapter's first.  The workgroup
+// counts the rows of every adapter in LDS, adds up their groups, and gives the rows of its own their places, which go by the
+// rows' order alone.  (Above kBuckets adapters, those that are alike in their last bits together: a group may have rows of
+// several.)
+constexpr int kBuckets = 4 * kThreads;
+// whether first_rows finds the first groups
+__device__ __forceinline__ bool scanned(const AdapterArgs& g) { return g.rows <= kScanRows && g.n <= kBuckets; }
+struct GroupLds {
+  int rows_of[kBuckets];
+  int groups[kWaves];                    // of a wavefront's buckets
+  int bucket, group;                     // the unit's
+  int matches[kUnitRows / 64];           // of each 64 rows
+  int row[kRows], adapter[kRows];
+};
+__device__ __forceinline__ UnitRows group_rows(const AdapterArgs& g, int unit, bool further, GroupLds& lds) {
+  constexpr int kEach = kUnitRows / kThreads;
+  static_assert(kEach * kThreads == kUnitRows && kWaves == 4, "rows of a thread, totals of the wavefronts");
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, rows = (int)g.rows;
+  int e[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) e[k] = g.row_adapter[min(k * kThreads + tid, rows - 1)];
+  reinterpret_cast<int4*>(lds.rows_of)[tid] = make_int4(0, 0, 0, 0);
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    if (k * kThreads + tid >= rows || e[k] < 0 || e[k] >= g.n) e[k] = -1;
+    if (e[k] >= 0) atomicAdd(&lds.rows_of[e[k] & (kBuckets - 1)], 1);
+  }
+  __syncthreads();
+  const int4 c = reinterpret_cast<const int4*>(lds.rows_of)[tid];
+  auto groups = [&](int rows) { return (uint32_t)max(0, rows + (further ? -1 : kRows - 1)) / kRows; };
+  const int q[4] = {(int)groups(c.x), (int)groups(c.y), (int)groups(c.z), (int)groups(c.w)};
+  const int own = q[0] + q[1] + q[2] + q[3];
+  int upto = own;   // with the lanes before: row_shr 1, 2, 4, 8, then the last lane of the row, of the half before
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xF, 0xF, true);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xF, 0xF, true);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xF, 0xF, true);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xF, 0xF, true);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x142, 0xA, 0xF, false);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x143, 0xC, 0xF, false);
+  if (lane == 63) lds.groups[wave] = upto;
+  __syncthreads();
+  int before = upto - own, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? lds.groups[w] : 0;
+    total += lds.groups[w];
+  }
+  if (unit >= total) return {0, 0, -1};   // (all threads)
+  if (unit >= before && unit < before + own) {
+    int bucket = 0, group = unit - before;
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (bucket == i && group >= q[i]) {
+        group -= q[i];
+        bucket = i + 1;
+      }
+    lds.bucket = 4 * tid + bucket;
+    lds.group = group;
+  }
+  __syncthreads();
+  const int bucket = lds.bucket, from = (lds.group + further) * kRows;
+  uint64_t m[kEach];
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    m[k] = __ballot(e[k] >= 0 && (e[k] & (kBuckets - 1)) == bucket);
+    if (lane == 0) lds.matches[k * kWaves + wave] = __popcll(m[k]);
+  }
+  __syncthreads();
+  int seen = 0;
+#pragma unroll
+  for (int i = 0; i < kEach * kWaves; ++i) {
+    if (i % kWaves == wave) {
+      const int k = i / kWaves, at = seen + bits_below(m[k]) - from;
+      if ((m[k] >> lane & 1) && at >= 0 && at < kRows) {
+        lds.row[at] = k * kThreads + tid;
+        lds.adapter[at] = e[k];
+      }
+    }
+    seen += lds.matches[i];
+  }
+  __syncthreads();
+  return {min(kRows, seen - from), lds.row[lane & (kRows - 1)], lds.adapter[lane & (kRows - 1)]};
 }
 
 // One step of the first product for a tile of 16 rows (of x, or of A): 64 values of each, as they are loaded.  Eight
@@ -295,51 +379,57 @@ __device__ __forceinline__ f32x4 sum_of_waves(const char (&lds)[WAVES][BYTES], i
   return s;
 }
 
-// A slice of the first product for a tile of rows, or for the rows of an adapter.
+// A slice of the first product for a tile of rows, or for a group of an adapter's rows, which the second product finds
+// in `found`.
 template <int RT, bool UNITS>
 __global__ void __launch_bounds__(kThreads) adapters_low_kernel(AdapterArgs g) {
-  __shared__ __align__(16) char lds[kWaves][LowLds<RT>::kBytes];
+  union Lds {
+    char of[kWaves][LowLds<RT>::kBytes];
+    GroupLds group;
+  };
+  __shared__ __align__(16) Lds lds;
   const int lane = threadIdx.x & 63, col = lane & 15, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tile = blockIdx.x / g.splits, sub = UNITS ? tile / (unsigned)g.units : 0, unit = tile - sub * g.units;
+  const int tile = blockIdx.x / g.splits;
   const int slice = blockIdx.x - (unsigned)tile * g.splits, begin = slice * g.per_split, end = min(g.in, begin + g.per_split);
-  for (int group = sub;; group += g.subs) {
-    UnitRows rows{-1, kRows, 0};
+  UnitRows rows{kRows, 0, -1};
+  if constexpr (UNITS) {
+    const int firsts = scanned(g) ? first_units(g.rows, g.n) : 0;
+    rows = tile < firsts ? first_rows(g, tile) : group_rows(g, tile - firsts, firsts > 0, lds.group);
+    if (slice == 0 && wave == 0 && lane < kRows)
+      g.found[tile * kRows + lane] = lane < rows.count ? make_int2(rows.row, rows.adapter) : make_int2(-1, -1);
+    if (rows.count == 0) return;
+    __syncthreads();   // (the products' LDS is the groups')
+  }
+  int64_t t;
+  int mine;
+  if constexpr (UNITS) {
+    const int e = __shfl(rows.adapter, col, 64);
+    t = __shfl(rows.row, min(col, rows.count - 1), 64);
+    mine = col < rows.count ? e : -1;
+  } else {
+    t = (int64_t)tile * kRows + col;
+    mine = adapter_of(g, t);
+  }
+  // (32-bit offsets from the first row of the tile, or of all)
+  const uint32_t at = mine < 0 ? 0u : (UNITS ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
+  f32x4 kept[RT];
+  low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1>(g, g.x + (UNITS ? 0 : (int64_t)tile * kRows * g.x_ld), at, mine, begin, end, wave,
+                                              kWaves, lds.of[wave], kept);
+  leave_sums<RT>(kept, lds.of[wave]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
+    const int row = i / (RT * 4), c = i % (RT * 4) * 4;
+    int64_t to;
+    bool in;
     if constexpr (UNITS) {
-      rows = unit_rows(g, unit, group);
-      if (rows.count == 0) return;
-    }
-    int64_t t;
-    int mine;
-    if constexpr (UNITS) {
-      t = __shfl(rows.row, min(col, rows.count - 1), 64);
-      mine = col < rows.count ? rows.adapter : -1;
+      in = row < rows.count;
+      to = __shfl(rows.row, min(row, rows.count - 1), 64);
     } else {
-      t = (int64_t)tile * kRows + col;
-      mine = adapter_of(g, t);
+      to = (int64_t)tile * kRows + row;
+      in = to < g.rows;
     }
-    // (32-bit offsets from the first row of the tile, or of all)
-    const uint32_t at = mine < 0 ? 0u : (UNITS ? (uint32_t)t : (uint32_t)col) * (uint32_t)g.x_ld;
-    f32x4 kept[RT];
-    low_sums<RT, RT == 1 ? 3 : RT == 2 ? 2 : 1>(g, g.x + (UNITS ? 0 : (int64_t)tile * kRows * g.x_ld), at, mine, begin, end,
-                                                wave, kWaves, lds[wave], kept);
-    leave_sums<RT>(kept, lds[wave]);
-    __syncthreads();
-    for (int i = threadIdx.x; i < kRows * RT * 4; i += kThreads) {
-      const int row = i / (RT * 4), c = i % (RT * 4) * 4;
-      int64_t to;
-      bool in;
-      if constexpr (UNITS) {
-        in = row < rows.count;
-        to = __shfl(rows.row, min(row, rows.count - 1), 64);
-      } else {
-        to = (int64_t)tile * kRows + row;
-        in = to < g.rows;
-      }
-      const f32x4 s = sum_of_waves<RT>(lds, row, c);
-      if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
-    }
-    if (!UNITS || rows.count < kRows) return;
-    __syncthreads();
+    const f32x4 s = sum_of_waves<RT>(lds.of, row, c);
+    if (in) *reinterpret_cast<f32x4*>(g.low + ((int64_t)slice * g.rows + to) * (RT * 16) + c) = s;
   }
 }
 
@@ -433,230 +523,229 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
   const int lane = threadIdx.x & 63, col = lane & 15, quad = lane >> 4, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   char* mine_lds = lds[wave];
   auto chunk_at = [&](int i) { return mine_lds + ((i & ~15) | ((i + i / kTurn) & 15)) * 16; };
-  const int tile = blockIdx.x / g.blocks, sub = UNITS ? tile / (unsigned)g.units : 0, unit = tile - sub * g.units;
-  const bool copy = UNITS && sub >= g.subs;   // the rows without an adapter of tile `copied`
-  const int copied = tile - g.units * g.subs;
+  const int tile = blockIdx.x / g.blocks;
+  const bool copy = UNITS && tile >= g.units;   // the rows without an adapter of tile `copied`
+  const int copied = tile - g.units;
   const int block = blockIdx.x - (unsigned)tile * g.blocks;
   const int first = block * g.per_block + kCols * wave, end = min(g.outs, (block + 1) * g.per_block);
-  for (int group = sub;; group += g.subs) {
-    UnitRows rows{-1, kRows, 0};
-    if constexpr (UNITS) {
-      if (copy) {
-        const int r = copied * kRows + lane;
-        const bool without = lane < kRows && r < g.rows && adapter_of(g, r) < 0;
-        const uint64_t m = __ballot(without);
-        rows = {-1, (int)__popcll(m), __builtin_amdgcn_ds_permute(4 * (without ? bits_below(m) : kRows), r)};
-      } else {
-        rows = unit_rows(g, unit, group);
-      }
-      if (rows.count == 0) return;
+  UnitRows rows{kRows, 0, -1};
+  if constexpr (UNITS) {
+    if (copy) {
+      const int r = copied * kRows + lane;
+      const bool without = lane < kRows && r < g.rows && adapter_of(g, r) < 0;
+      const uint64_t m = __ballot(without);
+      rows = {(int)__popcll(m), __builtin_amdgcn_ds_permute(4 * (without ? bits_below(m) : kRows), r), -1};
+    } else if constexpr (FEW) {
+      rows = first_rows(g, tile);
+    } else {
+      const int2 f = g.found[tile * kRows + col];
+      rows = {(int)__popcll(__ballot(lane < kRows && f.x >= 0)), f.x, f.y};
     }
-    // rows of the tile
-    const int here = UNITS ? rows.count : (int)min((int64_t)kRows, g.rows - (int64_t)tile * kRows);
-    auto row_of = [&](int i) -> int64_t {   // (rows the tile does not have: its last one)
-      if constexpr (UNITS) return __shfl(rows.row, min(i, here - 1), 64);
-      else return (int64_t)tile * kRows + min(i, here - 1);
-    };
-    const int64_t t = row_of(col);
-    const int mine = col < here ? (UNITS ? rows.adapter : adapter_of(g, t)) : -1;
-    const uint64_t with = __ballot(mine >= 0);
-    const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
-    const bool alone = RT <= 4 && with != 0 && __ballot(mine >= 0 && mine != e0) == 0;   // one adapter in the tile
-    // the lane's four tokens of the result, and their adapters
-    int64_t out_row[4];
-    int theirs[4];
+    if (rows.count == 0) return;
+  }
+  // rows of the tile
+  const int here = UNITS ? rows.count : (int)min((int64_t)kRows, g.rows - (int64_t)tile * kRows);
+  auto row_of = [&](int i) -> int64_t {   // (rows the tile does not have: its last one)
+    if constexpr (UNITS) return __shfl(rows.row, min(i, here - 1), 64);
+    else return (int64_t)tile * kRows + min(i, here - 1);
+  };
+  const int64_t t = row_of(col);
+  const int e = UNITS ? __shfl(rows.adapter, col, 64) : adapter_of(g, t), mine = col < here ? e : -1;
+  const uint64_t with = __ballot(mine >= 0);
+  const int e0 = with ? __builtin_amdgcn_readlane(mine, __builtin_ctzll(with)) : -1;
+  const bool alone = RT <= 4 && with != 0 && __ballot(mine >= 0 && mine != e0) == 0;   // one adapter in the tile
+  // the lane's four tokens of the result, and their adapters
+  int64_t out_row[4];
+  int theirs[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      out_row[i] = row_of(4 * quad + i);
-      theirs[i] = __shfl(mine, 4 * quad + i, 64);
+  for (int i = 0; i < 4; ++i) {
+    out_row[i] = row_of(4 * quad + i);
+    theirs[i] = __shfl(mine, 4 * quad + i, 64);
+  }
+  auto load_base = [&](Operands& o, int c0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o.base[i] = *reinterpret_cast<const RawFour<T>*>(static_cast<const T*>(g.base) + out_row[i] * g.base_ld +
+                                                       min(c0 + 4 * col, g.outs - 4));
+  };
+  auto load_b = [&](u32x4 (&to)[kLoads], int e, int c0) {
+    const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int i = 64 * l + lane;
+      to[l] = *reinterpret_cast<const u32x4*>(b + ((uint32_t)min(c0 + i / (RT * 2), g.outs - 1) * (uint32_t)g.r +
+                                                    (uint32_t)min(i % (RT * 2) * 8, g.r - 8)));
     }
-    auto load_base = [&](Operands& o, int c0) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o.base[i] = *reinterpret_cast<const RawFour<T>*>(static_cast<const T*>(g.base) + out_row[i] * g.base_ld +
-                                                         min(c0 + 4 * col, g.outs - 4));
-    };
-    auto load_b = [&](u32x4 (&to)[kLoads], int e, int c0) {
-      const uint16_t* b = g.b + (int64_t)e * g.outs * g.r;
-#pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const int i = 64 * l + lane;
-        to[l] = *reinterpret_cast<const u32x4*>(b + ((uint32_t)min(c0 + i / (RT * 2), g.outs - 1) * (uint32_t)g.r +
-                                                      (uint32_t)min(i % (RT * 2) * 8, g.r - 8)));
-      }
-    };
-    Operands now{};
-    if (alone && first < end) load_b(now.b, e0, first);
-    if (g.base && first < end) load_base(now, first);
-    bf16x8 low[kSteps];
-    if (with) {   // (the wavefronts of a workgroup have the same rows)
-      if (UNITS && group > sub) __syncthreads();
-      const int items = here * RT * 4, shares = FEW ? 1 : max(1, min(kShares, kThreads / items));
-      if constexpr (FEW) {
-        f32x4 part[RT];
-        low_sums<RT, RT == 1 ? 3 : 2>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave,
-                                             kWaves, mine_lds, part);
-        leave_sums<RT>(part, mine_lds);
-        __syncthreads();
-        for (int i = threadIdx.x; i < items; i += kThreads) sums[i] = sum_of_waves<RT>(lds, i / (RT * 4), i % (RT * 4) * 4);
-      }
-      // the slices' sums, slices shared out among threads and loaded in batches
-      for (int i0 = FEW ? items : 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
-        const int i = min(i0 + (int)threadIdx.x, items * shares - 1), share = i / items, item = i - share * items;
-        f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-        const float* p = g.low + row_of(item / (RT * 4)) * (RT * 16) + item % (RT * 4) * 4;
-        for (int s0 = share; s0 < g.splits; s0 += shares * kBatch) {
-          f32x4 v[kBatch];
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b)
-            v[b] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + b * shares, g.splits - 1) * g.rows * (RT * 16));
-#pragma unroll
-          for (int b = 0; b < kBatch; ++b) sum += s0 + b * shares < g.splits ? v[b] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        }
-        sums[i] = sum;
-      }
-      const float factor = mine >= 0 ? g.scale[mine] : 0.0f;
+  };
+  Operands now{};
+  if (alone && first < end) load_b(now.b, e0, first);
+  if (g.base && first < end) load_base(now, first);
+  bf16x8 low[kSteps];
+  if (with) {   // (the wavefronts of a workgroup have the same rows)
+    const int items = here * RT * 4, shares = FEW ? 1 : max(1, min(kShares, kThreads / items));
+    if constexpr (FEW) {
+      f32x4 part[RT];
+      low_sums<RT, RT == 1 ? 3 : 2>(g, g.x, mine < 0 ? 0u : (uint32_t)t * (uint32_t)g.x_ld, mine, 0, g.in, wave,
+                                           kWaves, mine_lds, part);
+      leave_sums<RT>(part, mine_lds);
       __syncthreads();
-#pragma unroll
-      for (int run = 0; run < kRuns; ++run) {
-        const int at = min(col, here - 1) * RT * 4 + (RT == 1 ? 2 * (quad & 1) : 8 * run + 2 * quad);
-        f32x4 lo = sums[at], hi = sums[at + 1];
-        for (int w = 1; w < shares; ++w) {
-          lo += sums[w * items + at];
-          hi += sums[w * items + at + 1];
-        }
-        float v[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = mine >= 0 ? lo[i] * factor : 0.0f;
-          v[4 + i] = mine >= 0 ? hi[i] * factor : 0.0f;
-        }
-        if constexpr (RT == 1) {
-#pragma unroll
-          for (int s = 0; s < kSteps; ++s) {   // the lower half of the lanes has one part, the upper half the next
-            const bf16x8 even = part_of(v), odd = 2 * s + 1 < PARTS ? part_of(v) : no_values();
-            low[s] = quad < 2 ? even : odd;
-          }
-        } else {
-#pragma unroll
-          for (int p = 0; p < PARTS; ++p) low[p * kRuns + run] = part_of(v);
-        }
-      }
-      if (kShared) __syncthreads();
+      for (int i = threadIdx.x; i < items; i += kThreads) sums[i] = sum_of_waves<RT>(lds, i / (RT * 4), i % (RT * 4) * 4);
     }
-    // kept = the products with adapter e's rows of B, for the tokens that have e
-    auto multiply = [&](const u32x4 (&from)[kLoads], int e, int rank, f32x4 (&kept)[4]) {
-      __builtin_amdgcn_wave_barrier();   // (the LDS operations of one wavefront take effect in program order)
+    // the slices' sums, slices shared out among threads and loaded in batches
+    for (int i0 = FEW ? items : 0; i0 < items * shares; i0 += kThreads) {   // (all lanes: row_of reads other lanes' values)
+      const int i = min(i0 + (int)threadIdx.x, items * shares - 1), share = i / items, item = i - share * items;
+      f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+      const float* p = g.low + row_of(item / (RT * 4)) * (RT * 16) + item % (RT * 4) * 4;
+      for (int s0 = share; s0 < g.splits; s0 += shares * kBatch) {
+        f32x4 v[kBatch];
 #pragma unroll
-      for (int l = 0; l < kLoads; ++l) {
-        const int i = 64 * l + lane;
-        u32x4 q = from[l];
-        if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
-          const int left = rank - i % (RT * 2) * 8;
-          q[0] &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
-          q[1] &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
-          q[2] &= left > 5 ? ~0u : left > 4 ? 0xFFFFu : 0u;
-          q[3] &= left > 7 ? ~0u : left > 6 ? 0xFFFFu : 0u;
-        }
-        *reinterpret_cast<u32x4*>(chunk_at(i)) = q;
+        for (int b = 0; b < kBatch; ++b)
+          v[b] = *reinterpret_cast<const f32x4*>(p + (int64_t)min(s0 + b * shares, g.splits - 1) * g.rows * (RT * 16));
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) sum += s0 + b * shares < g.splits ? v[b] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
-      __builtin_amdgcn_wave_barrier();
-      float none_past = 0.0f;            // NaN once a product is not finite
-      auto operands = [&](int j, bf16x8 (&bv)[kRuns]) {
-        const int c = 4 * col + j;   // the lane's column of this tile
+      sums[i] = sum;
+    }
+    const float factor = mine >= 0 ? g.scale[mine] : 0.0f;
+    __syncthreads();
 #pragma unroll
-        for (int run = 0; run < kRuns; ++run)
-          bv[run] = *reinterpret_cast<const bf16x8*>(chunk_at(c * RT * 2 + (RT == 1 ? quad & 1 : 4 * run + quad)));
-      };
+    for (int run = 0; run < kRuns; ++run) {
+      const int at = min(col, here - 1) * RT * 4 + (RT == 1 ? 2 * (quad & 1) : 8 * run + 2 * quad);
+      f32x4 lo = sums[at], hi = sums[at + 1];
+      for (int w = 1; w < shares; ++w) {
+        lo += sums[w * items + at];
+        hi += sums[w * items + at + 1];
+      }
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = mine >= 0 ? lo[i] * factor : 0.0f;
+        v[4 + i] = mine >= 0 ? hi[i] * factor : 0.0f;
+      }
+      if constexpr (RT == 1) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {   // the lower half of the lanes has one part, the upper half the next
+          const bf16x8 even = part_of(v), odd = 2 * s + 1 < PARTS ? part_of(v) : no_values();
+          low[s] = quad < 2 ? even : odd;
+        }
+      } else {
+#pragma unroll
+        for (int p = 0; p < PARTS; ++p) low[p * kRuns + run] = part_of(v);
+      }
+    }
+    if (kShared) __syncthreads();
+  }
+  // kept = the products with adapter e's rows of B, for the tokens that have e
+  auto multiply = [&](const u32x4 (&from)[kLoads], int e, int rank, f32x4 (&kept)[4]) {
+    __builtin_amdgcn_wave_barrier();   // (the LDS operations of one wavefront take effect in program order)
+#pragma unroll
+    for (int l = 0; l < kLoads; ++l) {
+      const int i = 64 * l + lane;
+      u32x4 q = from[l];
+      if (rank < RT * 16) {   // what is behind the rank does not count, whatever it holds
+        const int left = rank - i % (RT * 2) * 8;
+        q[0] &= left > 1 ? ~0u : left > 0 ? 0xFFFFu : 0u;
+        q[1] &= left > 3 ? ~0u : left > 2 ? 0xFFFFu : 0u;
+        q[2] &= left > 5 ? ~0u : left > 4 ? 0xFFFFu : 0u;
+        q[3] &= left > 7 ? ~0u : left > 6 ? 0xFFFFu : 0u;
+      }
+      *reinterpret_cast<u32x4*>(chunk_at(i)) = q;
+    }
+    __builtin_amdgcn_wave_barrier();
+    float none_past = 0.0f;            // NaN once a product is not finite
+    auto operands = [&](int j, bf16x8 (&bv)[kRuns]) {
+      const int c = 4 * col + j;   // the lane's column of this tile
+#pragma unroll
+      for (int run = 0; run < kRuns; ++run)
+        bv[run] = *reinterpret_cast<const bf16x8*>(chunk_at(c * RT * 2 + (RT == 1 ? quad & 1 : 4 * run + quad)));
+    };
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bf16x8 bv[kRuns];
+      operands(j, bv);
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) acc = mfma(low[s], bv[RT == 1 ? 0 : s % kRuns], acc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        none_past = fmaf(acc[i], 0.0f, none_past);
+        kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
+      }
+    }
+    // Where B is not finite, the first part of a low-rank value makes the infinity or NaN of it; the others, which may be
+    // zero or of another sign, leave it out.  (Looked for in the products: 16 multiply-adds a turn, 1 to 2% of a call; in B as
+    // it is loaded, with the products' operands chosen on the way, 2 to 7%.)
+    if (__builtin_expect(__ballot(none_past != none_past) != 0, 0)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         bf16x8 bv[kRuns];
         operands(j, bv);
         f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) acc = mfma(low[s], bv[RT == 1 ? 0 : s % kRuns], acc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          none_past = fmaf(acc[i], 0.0f, none_past);
-          kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
+        for (int s = 0; s < kSteps; ++s) {
+          const bf16x8 b = bv[RT == 1 ? 0 : s % kRuns], rest = finite_of(b);
+          acc = mfma(low[s], RT == 1 ? (s == 0 && quad < 2 ? b : rest) : s < kRuns ? b : rest, acc);
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
       }
-      // Where B is not finite, the first part of a low-rank value makes the infinity or NaN of it; the others, which may be
-      // zero or of another sign, leave it out.  (Looked for in the products: 16 multiply-adds a turn, 1 to 2% of a call; in B as
-      // it is loaded, with the products' operands chosen on the way, 2 to 7%.)
-      if (__builtin_expect(__ballot(none_past != none_past) != 0, 0)) {
+    }
+  };
+  auto store = [&](const Operands& o, const f32x4 (&kept)[4], int c0) {
+    const int c = c0 + 4 * col;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          bf16x8 bv[kRuns];
-          operands(j, bv);
-          f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < 4; ++i) {
+      if (4 * quad + i >= here || c >= g.outs) continue;
+      float v[4];
 #pragma unroll
-          for (int s = 0; s < kSteps; ++s) {
-            const bf16x8 b = bv[RT == 1 ? 0 : s % kRuns], rest = finite_of(b);
-            acc = mfma(low[s], RT == 1 ? (s == 0 && quad < 2 ? b : rest) : s < kRuns ? b : rest, acc);
-          }
+      for (int k = 0; k < 4; ++k) v[k] = o.base[i].at(k) + kept[k][i];
+      RawFour<T> p;
+      p.set(v);
+      if (theirs[i] < 0) p = o.base[i];   // (a row without an adapter keeps its base's bits)
+      *reinterpret_cast<RawFour<T>*>(static_cast<T*>(g.out) + out_row[i] * g.out_ld + c) = p;
+    }
+  };
+  const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto clear = [&](f32x4 (&kept)[4]) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
-        }
-      }
-    };
-    auto store = [&](const Operands& o, const f32x4 (&kept)[4], int c0) {
-      const int c = c0 + 4 * col;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (4 * quad + i >= here || c >= g.outs) continue;
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = o.base[i].at(k) + kept[k][i];
-        RawFour<T> p;
-        p.set(v);
-        if (theirs[i] < 0) p = o.base[i];   // (a row without an adapter keeps its base's bits)
-        *reinterpret_cast<RawFour<T>*>(static_cast<T*>(g.out) + out_row[i] * g.out_ld + c) = p;
-      }
-    };
-    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
-    auto clear = [&](f32x4 (&kept)[4]) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) kept[j] = none;
-    };
-    f32x4 kept[4];
-    if (alone) {
-      const int rank = rank_of(g, e0);
-      int c0 = first;
-      for (; c0 + kStride < end; c0 += kStride) {
-        if constexpr (RT <= 2) {   // the next columns' operands on their way while these are worked on
-          Operands next{};
-          load_b(next.b, e0, c0 + kStride);
-          if (g.base) load_base(next, c0 + kStride);
-          clear(kept);
-          multiply(now.b, e0, rank, kept);
-          store(now, kept, c0);
-          now = next;
-        } else {   // (no registers for a second set)
-          clear(kept);
-          multiply(now.b, e0, rank, kept);
-          store(now, kept, c0);
-          load_b(now.b, e0, c0 + kStride);
-          if (g.base) load_base(now, c0 + kStride);
-        }
-      }
-      if (c0 < end) {
+    for (int j = 0; j < 4; ++j) kept[j] = none;
+  };
+  f32x4 kept[4];
+  if (alone) {
+    const int rank = rank_of(g, e0);
+    int c0 = first;
+    for (; c0 + kStride < end; c0 += kStride) {
+      if constexpr (RT <= 2) {   // the next columns' operands on their way while these are worked on
+        Operands next{};
+        load_b(next.b, e0, c0 + kStride);
+        if (g.base) load_base(next, c0 + kStride);
         clear(kept);
         multiply(now.b, e0, rank, kept);
         store(now, kept, c0);
-      }
-    } else {
-      for (int c0 = first; c0 < end; c0 += kStride) {
+        now = next;
+      } else {   // (no registers for a second set)
         clear(kept);
-        if (g.base && c0 > first) load_base(now, c0);
-        for_adapters(mine, [&](int e) {
-          load_b(now.b, e, c0);
-          multiply(now.b, e, rank_of(g, e), kept);
-        });
+        multiply(now.b, e0, rank, kept);
         store(now, kept, c0);
+        load_b(now.b, e0, c0 + kStride);
+        if (g.base) load_base(now, c0 + kStride);
       }
     }
-    if (!UNITS || copy || here < kRows) return;
+    if (c0 < end) {
+      clear(kept);
+      multiply(now.b, e0, rank, kept);
+      store(now, kept, c0);
+    }
+  } else {
+    for (int c0 = first; c0 < end; c0 += kStride) {
+      clear(kept);
+      if (g.base && c0 > first) load_base(now, c0);
+      for_adapters(mine, [&](int e) {
+        load_b(now.b, e, c0);
+        multiply(now.b, e, rank_of(g, e), kept);
+      });
+      store(now, kept, c0);
+    }
   }
 }
 
@@ -664,7 +753,7 @@ struct AdapterPlan {
   int tiles16;                   // RT
   AdapterForm form;
   int splits, per_split, blocks, per_block;
-  int units, subs;
+  int units;
 };
 
 AdapterPlan plan_of(const moe_adapter_shape& s) {
@@ -676,10 +765,11 @@ AdapterPlan plan_of(const moe_adapter_shape& s) {
                      s.rows * x_ld < (int64_t(1) << 32)   // (32-bit offsets)
                ? kUnitForm
                : kTileForm;
-  p.units = (int)std::min<int64_t>(s.rows, n);
-  p.subs = p.form != kUnitForm || s.rows <= 4 * n ? 1 : s.rows <= 8 * n ? 2 : 4;
-  // (at least one: the size query may be asked for no rows)
-  const int64_t tiles = std::max<int64_t>(1, p.form == kUnitForm ? p.units * p.subs : ceil_div(s.rows, kRows));
+  // an adapter's last group may be a part of one: n groups (or as many as there are rows) and one for every whole 16 rows
+  p.units = (int)(first_units(s.rows, s.n_adapters) + (p.form == kUnitForm ? s.rows / kRows : 0));
+  // (at least one: the size query may be asked for no rows; up to 64 rows hardly any adapter has further groups)
+  const int64_t tiles = std::max<int64_t>(
+      1, p.form != kUnitForm ? ceil_div(s.rows, kRows) : s.rows <= 64 ? first_units(s.rows, s.n_adapters) : p.units);
   const int64_t some = p.form == kUnitForm ? kUnitBlocks : p.tiles16 <= 2 ? kTileBlocks : kTileBlocks / 2;
   const int64_t run = kStep * kWaves;
   const int64_t want = std::max<int64_t>(1, std::min<int64_t>(ceil_div(some, tiles), ceil_div(s.in_cols, run)));
@@ -702,7 +792,7 @@ template <int RT>
 hipError_t run_t(const AdapterArgs& g, AdapterForm form, int out_dtype, hipStream_t st) {
   // (the slices or columns of a tile are neighbours in the grid: workgroups at work together cover whole rows)
   const int64_t row_tiles = ceil_div(g.rows, kRows);
-  const unsigned tiles = (unsigned)(form == kTileForm ? row_tiles : (int64_t)g.units * g.subs);
+  const unsigned tiles = (unsigned)(form == kTileForm ? row_tiles : (int64_t)g.units);
   // by adapters, the rows without one are copied by further workgroups, unless they are where they belong
   const dim3 grid((tiles + (unsigned)(form == kTileForm || g.base == g.out ? 0 : row_tiles)) * g.blocks);
   if constexpr (RT <= 2)
@@ -716,14 +806,18 @@ hipError_t run_t(const AdapterArgs& g, AdapterForm form, int out_dtype, hipStrea
 
 }  // namespace
 
-// What any batch of up to so many rows needs (the slices are fewer the more rows there are, and end unevenly): a plan's
-// slices are fewer than some / tiles + 1, and no more than the runs of 256 values.  With kRows rows a tile, or at most that many
-// for each workgroup by adapters and slice, slices * rows <= kRows * some + rows.
+// What any batch of up to so many rows needs (the slices are fewer the more rows there are, and end unevenly): the groups that
+// the first product finds, and its slices, which are fewer than some / tiles + 1 and no more than the runs of 256 values: with
+// kRows rows a tile or group at most, slices * rows <= kRows * some + rows.
+static int64_t found_bytes(const moe_adapter_shape& s) {
+  const int64_t rows = std::min<int64_t>(s.rows, kUnitRows);
+  return (first_units(rows, s.n_adapters) + rows / kRows) * kRows * sizeof(int2);
+}
 size_t adapters_workspace(const moe_adapter_shape& s) {
   const AdapterPlan p = plan_of(s);
   if (p.form == kFewForm) return 0;
   const int64_t most = kRows * (p.tiles16 <= 2 ? kTileBlocks : kTileBlocks / 2) + s.rows;
-  return (size_t)std::min(s.rows * ceil_div(s.in_cols, kStep * kWaves), most) * p.tiles16 * 16 * 4;
+  return (size_t)(found_bytes(s) + std::min(s.rows * ceil_div(s.in_cols, kStep * kWaves), most) * p.tiles16 * 16 * 4);
 }
 
 hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int32_t* row_adapter, const void* a, const void* b,
@@ -738,7 +832,8 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       ranks,
                       base,
                       out,
-                      low,
+                      low + (found_bytes(s) / 4),
+                      reinterpret_cast<int2*>(low),
                       s.rows,
                       s.x_ld ? s.x_ld : s.in_cols,
                       s.base_ld ? s.base_ld : s.out_cols,
@@ -751,8 +846,7 @@ hipError_t launch_adapters(const moe_adapter_shape& s, const void* x, const int3
                       p.per_split,
                       p.blocks,
                       p.per_block,
-                      p.units,
-                      p.subs};
+                      p.units};
   switch (p.tiles16) {
     case 1: return run_t<1>(g, p.form, s.out_dtype, st);
     case 2: return run_t<2>(g, p.form, s.out_dtype, st);
