@@ -328,7 +328,7 @@ typedef struct moe_gate_config {
   int64_t logits_ld;     /* elements between rows of logits; 0: n_routed */
 } moe_gate_config;
 
-/* Bytes of device workspace that moe_gate needs for `config` (0 without expert_load). */
+/* Bytes of device workspace that moe_gate needs for `config` (0 without expert_load).  For these tokens: fewer may need more. */
 moe_status moe_gate_workspace_size(const moe_gate_config* config, size_t* bytes);
 
 /* Selection and gates.
@@ -382,7 +382,7 @@ typedef struct moe_matmul_shape {
   int64_t ldo;          /* elements between rows of out; 0: n */
 } moe_matmul_shape;
 
-/* Bytes of device workspace that moe_matmul_fp8 needs for `shape`. */
+/* Bytes of device workspace that moe_matmul_fp8 needs for `shape`.  For this one: a smaller one may need more. */
 moe_status moe_matmul_fp8_workspace_size(const moe_matmul_shape* shape, size_t* bytes);
 
 /* out = the product of `shape`'s form.

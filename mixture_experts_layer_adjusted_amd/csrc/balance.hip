@@ -632,10 +632,15 @@ hipError_t with_lanes(int n, F f) {
   return f(integral_constant<int, 64>{}, integral_constant<int, 2>{}, bool_constant<true>{});
 }
 
-// One kernel, a workgroup a sequence, for few tokens: a block of them costs such a workgroup 0.8 us (1.5 us where a lane has
-// two runs), and the longest sequence may have them all.  In a graph, us with the gradient, one kernel against two: 64
-// experts: 64 tokens 5.6, 9.0; 256 7.8, 9.1; 512 10.9, 9.4; 7 sequences of 1021 9.1, 10.8; 64 of 2048 7.0, 17.9.  256
-// experts, sigmoid: 64 tokens 8.0, 10.4; 256 17.5, 11.8; 7 sequences of 256 10.5, 13.4; 64 of 512 8.5, 22.5.
+// One kernel, a workgroup a sequence, for few tokens: a block of them costs such a workgroup 0.75 us (1.5 us where a lane has
+// two runs), and two kernels cost more the more sequences there are.  How the tokens are shared out is not known here.  In a
+// graph, us with the gradient, one kernel against two, cut at random, evenly, and all tokens in one sequence; blocks of 64 tokens
+// of 64 experts: 1 sequence: 4 blocks 8.0, 9.3; 6 9.4, 9.4; 8 10.9, 9.4.  3 sequences: 8 blocks 8.2, 10.5; 7.3, 10.6; 10.9, 9.4; 12
+// blocks 10.5, 10.6; 8.3, 9.6; 13.9, 9.7.  7: 16 blocks 10.1, 11.4; 7.4, 10.7; 17.0, 9.8; 24 blocks 10.5, 10.7; 8.2, 10.6; 23.0,
+// 9.9.  15: 32 blocks 11.5, 11.8; 7.5, 10.8; 28.8, 9.9.  64: 32 blocks 7.2, 18.0; 6.7, 12.1; 29.0, 10.6.  256 experts, sigmoid, half
+// the blocks (of 32 tokens): 7 sequences, 8 blocks 10.9, 13.7; 8.5, 12.1; 18.7, 11.0; 64, 16 blocks 8.8, 22.6; 7.6, 16.4; 29.6, 12.5.
+// So random cuts of 1, 3, 7 and 15 sequences are even at 6, 12, 24 and 32 blocks; the rule stays at two thirds of that up to 7
+// sequences, which bounds what a batch loses whose tokens are all in one of them: 1.7 times up to 7 sequences, 2.9 beyond.
 bool few_tokens(const moe_balance_config& c) {
   const int runs = c.n_routed <= 64 && c.n_routed % 4 == 0 ? 1 : 2;
   const int64_t blocks = ceil_div(c.tokens, kPartWaves * (64 / lanes_of(c.n_routed)));

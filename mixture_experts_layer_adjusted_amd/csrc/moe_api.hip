@@ -1186,7 +1186,7 @@ static moe_status check_adapters(const moe_adapter_shape* s) {
   if (s->in_cols % 8 != 0 || s->out_cols % 8 != 0 || s->rank % 8 != 0 || s->rank > 128) return MOE_ERR_UNSUPPORTED;
   if (s->in_cols > (1 << 20) || s->out_cols > (1 << 20)) return MOE_ERR_UNSUPPORTED;
   if (s->x_ld % 8 != 0 || s->base_ld % 8 != 0 || s->out_ld % 8 != 0) return MOE_ERR_UNSUPPORTED;
-  if (s->x_ld >= (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;   // 32-bit offsets inside 128 rows
+  if (s->x_ld >= (int64_t(1) << 24)) return MOE_ERR_UNSUPPORTED;   // 32-bit offsets inside a tile's 16 rows
   if (s->rows >= (1 << 27)) return MOE_ERR_UNSUPPORTED;            // a workgroup for every 16 rows
   return MOE_OK;
 }

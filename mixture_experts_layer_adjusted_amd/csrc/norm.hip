@@ -14,9 +14,9 @@
 // every batch.  16 lanes hold a run of 128.  The weight's gradient: every thread sums its own columns over the
 // workgroup's rows, the workgroups' sums are joined in a fixed order by a second kernel; for few rows, further workgroups
 // sum up columns in the same kernel.
-// Bound by memory: 16384 x 7168 in bf16, forward with y and codes 177 us for 1.06 GB (6.0 TB/s), backward 176 us for 0.94 GB
-// (5.3 TB/s) and 5 us for the join; 8192 x 7168 forward with codes alone 76 us for 0.41 GB (5.4 TB/s).  Few rows by latency:
-// one row of 7168 3.2 us, 77 of 2048 3.5 us.
+// Bound by memory (traced): 16384 x 7168 in bf16, forward with y and codes 178 us for 1.06 GB (6.0 TB/s), backward 182 us for
+// 0.94 GB (5.2 TB/s) and 5 us for the join; 8192 x 7168 forward with codes alone 77 us for 0.41 GB (5.4 TB/s).  Few rows by
+// latency: one row of 7168 3.2 us, 77 of 2048 3.5 us.
 #include "fp8_codec.h"
 #include "lanes.h"
 #include "moe_internal.h"
@@ -25,7 +25,7 @@
 namespace moe {
 namespace {
 
-constexpr int kParts = 256;   // workgroups of a backward pass at most, one a CU
+constexpr int kParts = 256;   // workgroups at most that sum up the weight's gradient by rows: one a CU
 constexpr int kMostBlocks = 1 << 21;   // of a forward pass along x, the others along y: fewer than 2^32 threads in each
 
 struct NormArgs {
@@ -210,7 +210,8 @@ __device__ __forceinline__ void sum_columns(const NormBwdArgs& a, float (&place)
 }
 
 // kAhead: a workgroup goes through its rows with the next one's values on their way, which lets one workgroup a CU reach what
-// the memory gives (16384 x 7168, bf16: 169 us with 256 workgroups, 5.6 TB/s; 183 with 512; 230 with one row each).  Where
+// the memory gives (16384 x 7168, bf16, in a graph with the join: 169 us with 256 workgroups, 183 with 512, 230 with one row
+// each).  Where
 // the registers do not hold both rows, they are loaded one after the other.
 template <typename T, int V, int MOST>
 __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_bwd_kernel(NormBwdArgs a) {
@@ -384,10 +385,10 @@ hipError_t with_lanes(const NormLanes& l, F f) {
   return f(integral_constant<int, 4>{}, integral_constant<int, 1024>{});
 }
 
-// Workgroups of a backward pass, each with its own sums of the weight's gradient: half as many for few rows of a workgroup
-// each, whose sums cost as much as the rows (7168 values, us with the second kernel, 128 workgroups against 256: 300 rows
-// 11.7, 14.6; 512 rows 13.1, 14.9; 700 rows 14.7, 14.8; 1024 rows 17.5, 17.0; but rows of a wavefront, 1408 values in
-// fp32: 300 rows 6.1, 6.2; 600 rows 8.7, 7.3; 1021 rows 9.7, 9.0)
+// Workgroups of a backward pass that sums up the weight's gradient by rows, each with its own sums: half as many for few rows
+// of a workgroup each, whose sums cost as much as the rows (7168 values in bf16, us with the second kernel, 128 workgroups
+// against 256: 512 rows 13.1, 14.9; 700 rows 14.7, 14.8; 1024 rows 17.5, 17.0; but rows of a wavefront, 1408 values in
+// fp32: 600 rows 8.7, 7.3; 1021 rows 9.7, 9.0)
 int64_t norm_blocks(const NormLanes& l, int64_t rows) {
   const int64_t each = ceil_div(rows, l.per);
   return std::min<int64_t>(each, l.per == 1 && each <= 5 * (kParts / 2) ? kParts / 2 : kParts);
