@@ -484,8 +484,8 @@ moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
  *             residual itself; NULL: not kept.  NULL without a residual
  *   y         [rows, cols] out, or NULL
  *   codes     [rows, cols] out: E4M3FN, and scales [rows, cols/128] fp32: scale = amax/448 of the run
- *             of 128 (1 for zeros), code = round-to-nearest-even E4M3FN of fp32(y / scale), from y
- *             before its rounding to the type; both or neither NULL.  y or codes is needed
+ *             of 128 (1 where that is 0), code = round-to-nearest-even E4M3FN of fp32(y / scale), from
+ *             y before its rounding to the type; both or neither NULL.  y or codes is needed
  *   rstd      [rows] fp32 out: 1 / sqrt(mean(h^2) + eps), for moe_norm_backward; may be NULL
  * Squares and sums are fp32: a row whose sum of squares passes 3.4e38 has rstd 0, and a row of zeros
  * under eps = 0 is NaN.  A row's results do not depend on the other rows.  No buffer is another's, but for sum as above;

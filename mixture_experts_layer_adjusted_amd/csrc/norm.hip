@@ -3,7 +3,7 @@
 // Forward, for a row of n values:
 //   h = x + r, rounded to the stream's type (it is kept, and the backward pass reads it);
 //   rstd = 1 / sqrt(sum h^2 / n + eps);  y = h rstd w;
-//   a run of 128 of y: scale = amax / 448 (1 for zeros), code = E4M3 of the fp32 quotient y / scale, as quant_act_kernel
+//   a run of 128 of y: scale = amax / 448 (1 where that is 0), code = E4M3 of the fp32 quotient y / scale, as quant_act_kernel
 //   (bias_quant.hip) has them, from y in fp32 and not from its bf16 rounding.
 // Backward, with g = dy w and u = h rstd:
 //   dh = rstd (g - u sum(g u) / n) + what arrives at h from behind;  dw = sum over the rows of dy u.
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(MOST == 64 ? 256 : MOST) norm_fwd_kernel(NormA
     if (a.y) store8(static_cast<T*>(a.y) + r * a.y_ld + c, y);
     if (a.codes) {
       const float amax = run_amax(y);
-      const float scale = amax > 0.0f ? __fdiv_rn(amax, 448.0f) : 1.0f;
+      const float share = __fdiv_rn(amax, 448.0f), scale = share > 0.0f ? share : 1.0f;   // (amax below 3.2e-43: 0)
       *reinterpret_cast<uint2*>(a.codes + r * a.cols + c) = e4m3_codes8(y, scale);
       if ((lane & 15) == 0) a.scales[r * (a.cols / 128) + c / 128] = scale;
     }
