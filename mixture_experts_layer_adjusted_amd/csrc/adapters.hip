@@ -652,7 +652,7 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
       *reinterpret_cast<u32x4*>(chunk_at(i)) = q;
     }
     __builtin_amdgcn_wave_barrier();
-    float none_past = 0.0f;            // NaN once a product is not finite
+    float none_past = 0.0f;            // NaN where a product is not finite
     auto operands = [&](int j, bf16x8 (&bv)[kRuns]) {
       const int c = 4 * col + j;   // the lane's column of this tile
 #pragma unroll
@@ -666,15 +666,13 @@ __global__ void __launch_bounds__(FORM == kFewForm ? 64 * kFewWaves : kThreads, 
       f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) acc = mfma(low[s], bv[RT == 1 ? 0 : s % kRuns], acc);
+      none_past = fmaf(acc[0], 0.0f, none_past);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        none_past = fmaf(acc[i], 0.0f, none_past);
-        kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
-      }
+      for (int i = 0; i < 4; ++i) kept[j][i] = theirs[i] == e ? acc[i] : kept[j][i];
     }
     // Where B is not finite, the first part of a low-rank value makes the infinity or NaN of it; the others, which may be
-    // zero or of another sign, leave it out.  (Looked for in the products: 16 multiply-adds a turn, 1 to 2% of a call; in B as
-    // it is loaded, with the products' operands chosen on the way, 2 to 7%.)
+    // zero or of another sign, leave it out.  (Such a value leaves no token's product in its column finite, zeros' neither: one
+    // of the lane's four is looked at.  In B as it is loaded, with the operands chosen on the way, that cost 2 to 7% of a call.)
     if (__builtin_expect(__ballot(none_past != none_past) != 0, 0)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
