@@ -13,8 +13,8 @@
 // no sorting.  Rows of other adapters are computed and dropped, never added as zeros: an infinity or NaN stays in its row.
 // Few rows of many adapters (a decode batch) go by adapters instead: a workgroup finds 16 rows of one.
 //
-// Bound by memory at many rows: 8192 x 7168 -> 4096, rank 16, bf16: 29.5 us for the first product (121 MB, 4.1 TB/s), 31.6
-// for the second (134 MB and B, 4.3 TB/s); by latency at few (one row 3.5 + 4.6 us).  Operands loaded as the matrix instruction
+// Bound by memory at many rows (traced): 8192 x 7168 -> 4096, rank 16, bf16: 30.3 us for the first product (121 MB, 4.0 TB/s), 33
+// for the second (134 MB and B, 4.1 TB/s); by latency at few (one row 3.7 + 4.3 us).  Operands loaded as the matrix instruction
 // wants them took 37 + 37 us: the address unit takes a lane at a time there (57 accesses a load in place of 16).
 #include "moe_internal.h"
 #include "rows.h"

@@ -15,10 +15,10 @@
 // floating-point atomics.  (A sum over several workgroups a sequence, the last by a ticket, cost 2 us of device-wide
 // atomics and gained less.)  Few tokens take one kernel, a workgroup a sequence.
 //
-// Bound by latency and instructions: 32768 tokens of 64 experts, softmax: 6.0 us (8.4 MB), the second kernel 5.0, the gradient
-// 6.3 (16.8 MB); 16384 tokens of 256 experts, sigmoid: 10.0 (16.8 MB; 330 vector instructions for two tokens), 6.4, 9.5 (33.6
-// MB).  Loads of one value each where four lie side by side cost the gradient 14.0 in place of 9.4.  7 sequences of 1021 tokens
-// of 60 experts, softmax: 7.1 in one kernel (5.6 + 3.9 in two), the gradient 3.1.
+// Bound by latency and instructions (traced): 32768 tokens of 64 experts, softmax: 6.1 us (8.4 MB), the second kernel 5.1, the
+// gradient 6.4 (16.8 MB); 16384 tokens of 256 experts, sigmoid: 10.2 (16.8 MB; 330 vector instructions for two tokens), 6.5, 9.4
+// (33.6 MB).  Loads of one value each where four lie side by side cost the gradient 14.0 in place of 9.4.  7 sequences of 1021
+// tokens of 60 experts, softmax: 7.2 in one kernel (5.6 + 3.9 in two), the gradient 3.2.
 #include "lanes.h"
 #include "moe_internal.h"
 
