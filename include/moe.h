@@ -585,7 +585,8 @@ moe_status moe_adapters_workspace_size(const moe_adapter_shape* shape, size_t* b
  *   base         [T, out]    bf16 or fp32, or NULL (zeros); out may be base itself (equal strides)
  *   out          [T, out]    the same type
  * Sums are fp32 and the low-rank values (times the factor) keep 16 bits of their fp32 sums under a bf16 output, 24 under an
- * fp32 one; what of them lies below 2^-133 is lost.  A row's result is its own alone (an infinity or NaN in another row or adapter does not reach it).
+ * fp32 one; what of them lies below 2^-133 is lost.  A row's result is its own alone (an infinity or NaN in another row or
+ * adapter does not reach it).
  * Errors: MOE_ERR_INVALID_ARG (null pointers, pointers that are not multiples of 16 (row_adapter, scale and
  * ranks: of 4), strides below the row length, out or the workspace in place of another operand),
  * MOE_ERR_UNSUPPORTED (other limits), MOE_ERR_WORKSPACE. */

@@ -164,8 +164,8 @@ __device__ __forceinline__ UnitRows group_rows(const AdapterArgs& g, int unit, b
   }
   __syncthreads();
   const int4 c = reinterpret_cast<const int4*>(lds.rows_of)[tid];
-  auto groups = [&](int rows) { return (uint32_t)max(0, rows + (further ? -1 : kRows - 1)) / kRows; };
-  const int q[4] = {(int)groups(c.x), (int)groups(c.y), (int)groups(c.z), (int)groups(c.w)};
+  auto groups = [&](int n) { return (int)((uint32_t)max(0, n + (further ? -1 : kRows - 1)) / kRows); };
+  const int q[4] = {groups(c.x), groups(c.y), groups(c.z), groups(c.w)};
   const int own = q[0] + q[1] + q[2] + q[3];
   int upto = own;   // with the lanes before: row_shr 1, 2, 4, 8, then the last lane of the row, of the half before
   upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xF, 0xF, true);
