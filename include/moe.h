@@ -487,8 +487,8 @@ moe_status moe_norm_workspace_size(const moe_norm_shape* shape, size_t* bytes);
  *             of 128 (1 where that is 0), code = round-to-nearest-even E4M3FN of fp32(y / scale), from
  *             y before its rounding to the type; both or neither NULL.  y or codes is needed
  *   rstd      [rows] fp32 out: 1 / sqrt(mean(h^2) + eps), for moe_norm_backward; may be NULL
- * Squares and sums are fp32: a row whose sum of squares passes 3.4e38 has rstd 0, and a row of zeros
- * under eps = 0 is NaN.  A row's results do not depend on the other rows.  No buffer is another's, but for sum as above;
+ * Squares and sums are fp32: a row whose sum of squares passes 3.4e38 has rstd 0; under eps = 0 a row of
+ * zeros is NaN, and one whose squares are all 0 in fp32 (values below 2.6e-23) infinite.  A row's results do not depend on the other rows.  No buffer is another's, but for sum as above;
  * x_ld and y_ld are multiples of 8, and all pointers multiples of 16 (scales, rstd and d_weight: of 4).
  * Errors: MOE_ERR_INVALID_ARG (null or misaligned pointers, a negative size, ld < cols, buffers in
  * place of one another), MOE_ERR_UNSUPPORTED (other limits). */

@@ -1,5 +1,5 @@
-"""E4M3 codes of runs whose values are subnormal: a scale that amax / 448 rounds to is never zero.  Below 448 half steps of fp32's
-subnormals (3.1e-43) a run counts as zeros: codes of zero under the scale 1."""
+"""The norm of values near the bottom of the range.  E4M3 codes of subnormal runs: a scale that amax / 448 rounds to is never
+zero.  Below 448 half steps of fp32's subnormals (3.1e-43) a run counts as zeros: codes of zero under the scale 1."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -33,3 +33,14 @@ def test_runs_of_subnormal_values(cols, stream):
     tol = (2.0 ** -4 + 2.0 ** -17) * v.abs() + 2.0 ** -10 * step + 448 * 2.0 ** -150 + 2.0 ** -148
     assert ((codes * scales[:, None] - v).abs() <= tol).all()
     assert (codes[tiny == 0] == 0).all()
+
+
+def test_squares_that_are_zero_without_an_eps():
+    x = torch.full((4, 264), 1e-25, device="cuda")
+    x[1] = 0
+    x[2, 5] = 1.0
+    x[3] = 1e-15
+    out = forward(x, None, torch.ones(264, device="cuda"), "f32", eps=0.0)
+    assert torch.isposinf(out["y"][0]).all() and torch.isposinf(out["rstd"][0]) and torch.isnan(out["y"][1]).all()
+    assert torch.allclose(out["y"][2, 5], torch.tensor(264.0, device="cuda").sqrt(), rtol=2.0 ** -20)
+    assert torch.allclose(out["y"][3], torch.ones(264, device="cuda"), rtol=2.0 ** -18)
